@@ -125,6 +125,7 @@ def load():
         lib.gemm_nt_plan_ex.restype = ctypes.c_int
         lib.gemm_selftest_timeout.argtypes = [ctypes.c_int32, p]
         lib.gemm_selftest_timeout.restype = ctypes.c_int
+        _llm.declare(lib)
         _lib = lib
         return lib
 
@@ -307,3 +308,8 @@ def gemm(A, B, variant=Variant.AUTO, stream=None):
     D = torch.empty((A.shape[0], B.shape[0]), dtype=torch.float16, device=A.device)
     gemm_f16_nt_variant(A, B, D, variant=variant, stream=stream)
     return D
+
+
+from . import llm as _llm  # noqa: E402  (needs the names above)
+from .llm import (W4, MoeScoring, gemm_moe_ffn, gemm_moe_layer, gemm_moe_route,  # noqa: E402,F401
+                  gemm_w4_dequantize, gemm_w4_nt, gemm_w4_quantize)

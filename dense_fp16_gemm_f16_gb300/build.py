@@ -23,7 +23,8 @@ BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_NAME = "libgemm_f16.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 
-SOURCES = ["api.cu", "tiled_2cta.cu", "tiled_2cta512.cu", "tiled_1cta.cu", "skinny.cu", "streamk.cu"]
+SOURCES = ["api.cu", "tiled_2cta.cu", "tiled_2cta512.cu", "tiled_1cta.cu", "skinny.cu", "streamk.cu",
+           "llm/llm_api.cu", "llm/w4_codes.cu", "llm/w4_gemm.cu", "llm/moe_route.cu", "llm/moe_ffn.cu"]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH_FLAGS + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
                            "-I", INCLUDE, "-I", CSRC]
@@ -37,9 +38,9 @@ def nvcc() -> str:
 
 
 def _inputs() -> list[str]:
-    return (glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh"))
-            + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h"))
-            + [os.path.abspath(__file__)])
+    return ([p for d in (CSRC, os.path.join(CSRC, "llm")) for ext in ("*.cu", "*.cuh", "*.h")
+             for p in glob.glob(os.path.join(d, ext))]
+            + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
 
 
 def is_stale() -> bool:
@@ -78,7 +79,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
     objs = []
     cmds = []
     for src in SOURCES:
-        obj = os.path.join(build_dir, src.replace(".cu", ".o"))
+        obj = os.path.join(build_dir, src.replace("/", "_").replace(".cu", ".o"))
         objs.append(obj)
         cmds.append([cc, *NVCC_FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj])
     with cf.ThreadPoolExecutor(max_workers=len(cmds)) as ex:

@@ -16,6 +16,7 @@
 #include "config.h"
 #include "epilogue.cuh"
 #include "gemm_f16.h"
+#include "internal.h"
 #include "launch.h"
 #include "wait.cuh"
 
@@ -655,14 +656,6 @@ gemm_status_t get_workspace(int dev, gemm_stream_t stream, size_t partial_bytes,
     return GEMM_OK;
 }
 
-bool ranges_overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
-    if (a_bytes <= 0 || b_bytes <= 0) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-    return a0 < b0 + static_cast<uintptr_t>(b_bytes) && b0 < a0 + static_cast<uintptr_t>(a_bytes);
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 uint64_t timeout_for(int64_t k_blocks) {
     // two seconds plus a generous 2 us per K block of the longest tile
     return 2000000000ull + static_cast<uint64_t>(k_blocks) * 2000ull;
@@ -680,26 +673,6 @@ __global__ void epilogue_only_kernel(T* D, int64_t M, int64_t N, EpiParams e) {
     }
 }
 
-EpiParams epi_params(const gemm_epilogue_t* e) {
-    EpiParams p;
-    p.alpha = 1.0f;
-    p.beta = 0.0f;
-    p.C = nullptr;
-    p.bias = nullptr;
-    p.scale_n = nullptr;
-    p.act = 0;
-    p.on = 0;
-    if (e == nullptr) return p;
-    p.alpha = e->alpha;
-    p.beta = e->beta;
-    p.C = e->beta != 0.0f ? e->C : nullptr;
-    p.bias = e->bias;
-    p.scale_n = e->scale_n;
-    p.act = e->activation;
-    p.on = (p.alpha != 1.0f || p.C != nullptr || p.bias != nullptr || p.scale_n != nullptr || p.act != 0) ? 1 : 0;
-    return p;
-}
-
 gemm_status_t run(const void* A, const void* B, void* D, int64_t M, int64_t N, int64_t K,
                   gemm_variant_t variant, gemm_stream_t stream, int dtype = 0,
                   const gemm_epilogue_t* epilogue = nullptr) {
@@ -709,21 +682,8 @@ gemm_status_t run(const void* A, const void* B, void* D, int64_t M, int64_t N, i
     gemm_status_t st = check_sizes(M, N, K, in_bytes);
     if (st != GEMM_OK) return st;
     const EpiParams epi = epi_params(epilogue);
-    if (epilogue != nullptr) {
-        if (epilogue->activation != GEMM_ACT_NONE && epilogue->activation != GEMM_ACT_RELU)
-            return GEMM_ERR_INVALID_VALUE;
-        if (epilogue->beta != 0.0f && epilogue->C == nullptr) return GEMM_ERR_INVALID_VALUE;
-        if ((epi.C && !aligned16(epi.C)) || (epi.bias && !aligned16(epi.bias)) ||
-            (epi.scale_n && !aligned16(epi.scale_n)))
-            return GEMM_ERR_MISALIGNED;
-        // C may be D itself (an in-place update); it may not partly overlap D, and
-        // neither the bias nor the scales may overlap D at all
-        if (M > 0 && N > 0) {
-            if (epi.C && epi.C != D && ranges_overlap(epi.C, M * N * 2, D, M * N * 2)) return GEMM_ERR_INVALID_VALUE;
-            if (epi.bias && ranges_overlap(epi.bias, N * 2, D, M * N * 2)) return GEMM_ERR_INVALID_VALUE;
-            if (epi.scale_n && ranges_overlap(epi.scale_n, N * 4, D, M * N * 2)) return GEMM_ERR_INVALID_VALUE;
-        }
-    }
+    st = check_epilogue(epilogue, D, M, N);
+    if (st != GEMM_OK) return st;
     if (variant < GEMM_VARIANT_AUTO || variant > GEMM_VARIANT_TILE_1CTA_SPLITK) return GEMM_ERR_INVALID_VALUE;
     if ((variant == GEMM_VARIANT_SKINNY_SPLITK || variant == GEMM_VARIANT_SKINNY_STREAMK) && M > 64)
         return GEMM_ERR_INVALID_VALUE;
@@ -743,22 +703,7 @@ gemm_status_t run(const void* A, const void* B, void* D, int64_t M, int64_t N, i
     const int out_dtype = dtype_out(dtype);
     const int bk = stage_k(in_bytes);
 
-    if (K == 0) {  // the empty sum
-        if (epi.on) {
-            const int blocks = static_cast<int>(std::min<int64_t>(cdiv(M * N, 256), 8 * dev->sms));
-            if (out_dtype == GEMM_DTYPE_BF16)
-                epilogue_only_kernel<__nv_bfloat16><<<blocks, 256, 0, s>>>(static_cast<__nv_bfloat16*>(D), M, N, epi);
-            else
-                epilogue_only_kernel<__half><<<blocks, 256, 0, s>>>(static_cast<__half*>(D), M, N, epi);
-            if (cudaGetLastError() != cudaSuccess) return GEMM_ERR_LAUNCH;
-            return GEMM_OK;
-        }
-        if (cudaMemsetAsync(D, 0, static_cast<size_t>(d_bytes), s) != cudaSuccess) {
-            cudaGetLastError();
-            return GEMM_ERR_CUDA;
-        }
-        return GEMM_OK;
-    }
+    if (K == 0) return run_empty_sum(D, M, N, epi, out_dtype, dev->sms, s);
 
     gemm_plan_t pl;
     st = make_plan(M, N, K, variant, limits_of(*dev), &pl, in_bytes);
@@ -971,6 +916,92 @@ gemm_status_t run_noalloc(const void* A, const void* B, void* D, int64_t M, int6
 }
 
 }  // namespace
+
+namespace gemm_gb300 {
+
+gemm_status_t device_view(DeviceView* out) {
+    DeviceState* d = nullptr;
+    int dev = 0;
+    const gemm_status_t st = get_device(&d, &dev);
+    if (st != GEMM_OK) return st;
+    *out = DeviceView{dev, d->sms, d->status};
+    return GEMM_OK;
+}
+
+bool encode_map(CUtensorMap* map, const void* base, int elem_bytes, int64_t inner, int64_t outer, uint32_t box_inner,
+                uint32_t box_outer, bool swizzle128) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(inner) * elem_bytes};
+    const cuuint32_t box[2] = {box_inner, box_outer};
+    const cuuint32_t elem[2] = {1, 1};
+    return g_encode(map, elem_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
+                    const_cast<void*>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, kStreamL2Promotion,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+gemm_status_t check_epilogue(const gemm_epilogue_t* e, const void* D, int64_t M, int64_t N) {
+    if (e == nullptr) return GEMM_OK;
+    if (e->activation != GEMM_ACT_NONE && e->activation != GEMM_ACT_RELU) return GEMM_ERR_INVALID_VALUE;
+    if (e->beta != 0.0f && e->C == nullptr) return GEMM_ERR_INVALID_VALUE;
+    const EpiParams epi = epi_params(e);
+    if ((epi.C && !aligned16(epi.C)) || (epi.bias && !aligned16(epi.bias)) || (epi.scale_n && !aligned16(epi.scale_n)))
+        return GEMM_ERR_MISALIGNED;
+    // C may be D itself (an in-place update); it may not partly overlap D, and
+    // neither the bias nor the scales may overlap D at all
+    if (M > 0 && N > 0) {
+        if (epi.C && epi.C != D && ranges_overlap(epi.C, M * N * 2, D, M * N * 2)) return GEMM_ERR_INVALID_VALUE;
+        if (epi.bias && ranges_overlap(epi.bias, N * 2, D, M * N * 2)) return GEMM_ERR_INVALID_VALUE;
+        if (epi.scale_n && ranges_overlap(epi.scale_n, N * 4, D, M * N * 2)) return GEMM_ERR_INVALID_VALUE;
+    }
+    return GEMM_OK;
+}
+
+gemm_status_t run_empty_sum(void* D, int64_t M, int64_t N, const EpiParams& epi, int out_dtype, int sms,
+                            cudaStream_t s) {
+    if (epi.on) {
+        const int blocks = static_cast<int>(std::min<int64_t>(cdiv(M * N, 256), 8 * sms));
+        if (out_dtype == GEMM_DTYPE_BF16)
+            epilogue_only_kernel<__nv_bfloat16><<<blocks, 256, 0, s>>>(static_cast<__nv_bfloat16*>(D), M, N, epi);
+        else
+            epilogue_only_kernel<__half><<<blocks, 256, 0, s>>>(static_cast<__half*>(D), M, N, epi);
+        if (cudaGetLastError() != cudaSuccess) return GEMM_ERR_LAUNCH;
+        return GEMM_OK;
+    }
+    if (cudaMemsetAsync(D, 0, static_cast<size_t>(M * N * 2), s) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_CUDA;
+    }
+    return GEMM_OK;
+}
+
+bool ranges_overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+    if (a_bytes <= 0 || b_bytes <= 0) return false;
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+    return a0 < b0 + static_cast<uintptr_t>(b_bytes) && b0 < a0 + static_cast<uintptr_t>(a_bytes);
+}
+
+EpiParams epi_params(const gemm_epilogue_t* e) {
+    EpiParams p;
+    p.alpha = 1.0f;
+    p.beta = 0.0f;
+    p.C = nullptr;
+    p.bias = nullptr;
+    p.scale_n = nullptr;
+    p.act = 0;
+    p.on = 0;
+    if (e == nullptr) return p;
+    p.alpha = e->alpha;
+    p.beta = e->beta;
+    p.C = e->beta != 0.0f ? e->C : nullptr;
+    p.bias = e->bias;
+    p.scale_n = e->scale_n;
+    p.act = e->activation;
+    p.on = (p.alpha != 1.0f || p.C != nullptr || p.bias != nullptr || p.scale_n != nullptr || p.act != 0) ? 1 : 0;
+    return p;
+}
+
+}  // namespace gemm_gb300
 
 extern "C" {
 

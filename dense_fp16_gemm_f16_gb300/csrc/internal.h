@@ -1,0 +1,50 @@
+// internal.h -- what the C-ABI layers share: the current device's state, tensor
+// map encoding, the fused epilogue's checks and per-stream scratch.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "epilogue.cuh"
+#include "gemm_f16.h"
+
+namespace gemm_gb300 {
+
+struct DeviceView {
+    int dev;            // CUDA device ordinal
+    int sms;
+    uint32_t* status;   // device status word (wait.cuh)
+};
+
+// The current device, set up on first use (api.cu).
+gemm_status_t device_view(DeviceView* out);
+
+// The epilogue's argument checks and its kernel form (api.cu).
+gemm_status_t check_epilogue(const gemm_epilogue_t* e, const void* D, int64_t M, int64_t N);
+EpiParams epi_params(const gemm_epilogue_t* e);
+
+// D = act(beta * C + bias), the K == 0 result (api.cu).
+gemm_status_t run_empty_sum(void* D, int64_t M, int64_t N, const EpiParams& epi, int out_dtype, int sms,
+                            cudaStream_t s);
+
+// 2-D tensor map over `outer` rows of `inner` elements of elem_bytes (1 or 2),
+// rows `inner` elements apart, zero fill outside (api.cu).
+bool encode_map(CUtensorMap* map, const void* base, int elem_bytes, int64_t inner, int64_t outer, uint32_t box_inner,
+                uint32_t box_outer, bool swizzle128);
+
+bool ranges_overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes);
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// `bytes` of scratch for (device, stream), 256-byte aligned, and its counters:
+// kScratchCounters zeros that every kernel using them leaves at zero (llm/llm_api.cu).
+constexpr int kScratchCounters = 1024;
+struct Scratch {
+    uint8_t* data;
+    uint32_t* counters;
+};
+gemm_status_t get_scratch(int dev, gemm_stream_t stream, size_t bytes, Scratch* out);
+
+}  // namespace gemm_gb300
