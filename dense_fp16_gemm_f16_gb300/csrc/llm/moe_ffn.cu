@@ -1,86 +1,133 @@
-// moe_ffn.cu -- the experts' gated products for a few tokens.
-//
-// Simple form: one warp per (token's choice, row of the expert's first
-// product), fp32 h in scratch, then one warp per (token, output).
-#include "llm/llm.h"
-#include "llm/w4.cuh"
+// moe_ffn.cu -- launches of the experts' two products (moe_up.cuh, rows.cuh).
+#include <algorithm>
+#include <mutex>
+
+#include "llm/moe_up.cuh"
+#include "llm/rows.cuh"
+#include "llm/rows_host.cuh"
 
 namespace gemm_gb300 {
 namespace {
 
-__device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
+// Shared memory of each of the two kernels: at most half of an SM's, so the
+// second product's CTA finds room beside the first's and has its first ring of
+// weights in flight when the first product ends.
+constexpr int kFfnSmem = 200 * 1024;
 
-// One row of one matrix times a vector x of K elements (type TX), by a warp.
-template <class T, class TX>
-__device__ float row_dot(const Weights& w, int64_t matrix, int64_t rows, int64_t row, int64_t K, const TX* x, int lane) {
-    const int64_t r = matrix * rows + row;
-    float acc = 0.0f;
-    for (int64_t k = lane * 8; k < K; k += 256) {
-        float b[8];
-        if (w.scales == nullptr) {
-            unpack8<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(w.data) + r * K + k), b);
-        } else {
-            const uint32_t c = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(w.data) + r * (K / 2) + k / 2);
-            const int64_t at = (matrix * (K / w.group) + k / w.group) * rows + row;
-            const float s = Elem<T>::to_float(static_cast<const T*>(w.scales)[at]);
-            const float z = w.zeros != nullptr ? Elem<T>::to_float(static_cast<const T*>(w.zeros)[at]) : 8.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) b[i] = s * (static_cast<float>((c >> (4 * i)) & 15u) - z);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if constexpr (sizeof(TX) == 4) acc += x[k + i] * b[i];
-            else acc += Elem<T>::to_float(x[k + i]) * b[i];
-        }
+template <class T, bool W4, int NT>
+gemm_status_t launch_up(const FfnParams& f, void* h, const DeviceView& dev, cudaStream_t s) {
+    UpParams p{};
+    p.H = f.H;
+    p.I = f.I;
+    p.k_stages = (f.H + kStageElems<W4> - 1) / kStageElems<W4>;
+    const SideGroups sg(f.w13, f.H);
+    p.groups_k = sg.groups_k;
+    p.stage_groups = sg.stage_groups;
+    p.chunks_per_group = sg.chunks_per_group;
+    p.has_zeros = f.w13.zeros != nullptr;
+    const int64_t rows = 2ll * f.I * f.E;
+    p.stream_w = stream_weights(W4, rows, f.H);
+    p.X = f.X;
+    p.h = h;
+    p.ids = f.ids;
+    p.weights = f.weights;
+    p.T = f.T;
+    p.k = f.k;
+    p.E = f.E;
+    p.status = dev.status;
+    p.timeout_ns = kStreamTimeoutNs;
+    const int lists = list_offsets(f.T * f.k, f.E).end;
+    const int cols = std::min(8 * NT, f.T);
+    int smem = 0;
+    for (p.mw = kUpGranules / kTilesPerWarp<NT>; p.mw <= kUpGranules; p.mw *= 2) {
+        // as few warps per stage as the registers allow, more where the sums or
+        // a ring of KW stages would leave too little in flight
+        const int kw = kConsumers / p.mw;
+        const int sums = 2 * kw * 8 * NT * kUpPitch * 4;
+        p.ring = ring_layout(W4, kUpRows, 2 * kUpGranules * 8, sg.stage_groups, cols, kFfnSmem - 1024 - lists - sums, kw);
+        p.list_off = p.ring.end;
+        p.sums_off = p.list_off + lists;
+        smem = p.sums_off + sums + 1024;
+        if (smem <= kFfnSmem && p.ring.stages >= 4) break;
     }
-    for (int d = 16; d > 0; d >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, d);
-    return acc;
-}
-
-template <class T>
-__global__ void __launch_bounds__(256) moe_up_kernel(const FfnParams p, float* h) {
-    const int lane = threadIdx.x & 31;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int slot = blockIdx.y;
-    const int e = p.ids[slot];
-    if (i >= p.I || e < 0 || e >= p.E) return;
-    const T* x = static_cast<const T*>(p.X) + static_cast<int64_t>(slot / p.k) * p.H;
-    const float gate = row_dot<T, T>(p.w13, e, 2 * static_cast<int64_t>(p.I), i, p.H, x, lane);
-    const float up = row_dot<T, T>(p.w13, e, 2 * static_cast<int64_t>(p.I), p.I + i, p.H, x, lane);
-    if (lane == 0) h[static_cast<int64_t>(slot) * p.I + i] = silu(gate) * up;
-}
-
-template <class T>
-__global__ void __launch_bounds__(256) moe_down_kernel(const FfnParams p, const float* h) {
-    const int lane = threadIdx.x & 31;
-    const int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int t = blockIdx.y;
-    if (r >= p.H) return;
-    float y = 0.0f;
-    for (int j = 0; j < p.k; ++j) {
-        const int e = p.ids[t * p.k + j];
-        if (e < 0 || e >= p.E) continue;
-        y += p.weights[t * p.k + j] * row_dot<T, float>(p.w2, e, p.H, r, p.I, h + static_cast<int64_t>(t * p.k + j) * p.I, lane);
+    if (p.mw > kUpGranules) {
+        p.mw = kUpGranules;
+        if (smem > kMaxDynamicSmem) return GEMM_ERR_CUDA;
     }
-    if (lane == 0) static_cast<T*>(p.Y)[static_cast<int64_t>(t) * p.H + r] = Elem<T>::from_float(y);
+    CUtensorMap w, sc, zr;
+    if (!encode_weights(f.w13, rows, static_cast<int64_t>(f.E) * sg.groups_k, 2 * f.I, f.H, 8, kUpGranules * 8, sg.stage_groups, &w, &sc, &zr))
+        return GEMM_ERR_INVALID_VALUE;
+    return launch_stream(moe_up_kernel<T, W4, NT>, dev.dev, dev.sms, 1, smem, s, w, sc, zr, p);
+}
+
+template <class T, bool W4, int NT>
+gemm_status_t launch_down(const FfnParams& f, const void* h, const DeviceView& dev, cudaStream_t s) {
+    RowsParams p{};
+    const SideGroups sg(f.w2, f.I);
+    const int lists = list_offsets(f.T * f.k, f.E).end;
+    p.N = f.H;
+    p.K = f.I;
+    p.k_stages = (f.I + kStageElems<W4> - 1) / kStageElems<W4>;
+    const int smem = plan_rows<T, W4, NT, true>(&p, f.T, std::min(8 * NT, 2 * f.T), sg.stage_groups, lists, kFfnSmem, dev);
+    if (smem <= 0) return GEMM_ERR_CUDA;
+    p.groups_k = sg.groups_k;
+    p.stage_groups = sg.stage_groups;
+    p.chunks_per_group = sg.chunks_per_group;
+    p.has_zeros = f.w2.zeros != nullptr;
+    const int64_t rows = static_cast<int64_t>(f.H) * f.E;
+    p.stream_w = stream_weights(W4, rows, f.I);
+    p.cols = f.T;
+    p.X = h;
+    p.D = f.Y;
+    p.ids = f.ids;
+    p.weights = f.weights;
+    p.k = f.k;
+    p.E = f.E;
+    p.status = dev.status;
+    p.timeout_ns = kStreamTimeoutNs;
+    CUtensorMap w, sc, zr;
+    if (!encode_weights(f.w2, rows, static_cast<int64_t>(f.E) * sg.groups_k, f.H, f.I, p.width, p.width, sg.stage_groups, &w, &sc, &zr))
+        return GEMM_ERR_INVALID_VALUE;
+    return launch_stream(weight_rows_kernel<T, W4, NT, true>, dev.dev, p.ranges * p.pieces, p.pieces, smem, s, w, sc, zr, p);
+}
+
+// Columns a segment may have: as many as one expert can get, up to 64 for
+// 16-bit weights and 32 for 4-bit ones, whose group sums take registers too.
+template <class T>
+gemm_status_t up(const FfnParams& f, void* h, const DeviceView& dev, cudaStream_t s) {
+    if (f.w13.scales != nullptr) {
+        if (f.T <= 8) return launch_up<T, true, 1>(f, h, dev, s);
+        if (f.T <= 16) return launch_up<T, true, 2>(f, h, dev, s);
+        return launch_up<T, true, 4>(f, h, dev, s);
+    }
+    if (f.T <= 8) return launch_up<T, false, 1>(f, h, dev, s);
+    if (f.T <= 16) return launch_up<T, false, 2>(f, h, dev, s);
+    if (f.T <= 32) return launch_up<T, false, 4>(f, h, dev, s);
+    return launch_up<T, false, 8>(f, h, dev, s);
 }
 
 template <class T>
-cudaError_t launch(const FfnParams& p, float* h, cudaStream_t s) {
-    moe_up_kernel<T><<<dim3(static_cast<unsigned>((p.I + 7) / 8), static_cast<unsigned>(p.T * p.k), 1), 256, 0, s>>>(p, h);
-    moe_down_kernel<T><<<dim3(static_cast<unsigned>((p.H + 7) / 8), static_cast<unsigned>(p.T), 1), 256, 0, s>>>(p, h);
-    return cudaGetLastError();
+gemm_status_t down(const FfnParams& f, const void* h, const DeviceView& dev, cudaStream_t s) {
+    if (f.w2.scales != nullptr) {
+        if (f.T <= 4) return launch_down<T, true, 1>(f, h, dev, s);
+        if (f.T <= 8) return launch_down<T, true, 2>(f, h, dev, s);
+        return launch_down<T, true, 4>(f, h, dev, s);
+    }
+    if (f.T <= 4) return launch_down<T, false, 1>(f, h, dev, s);
+    if (f.T <= 8) return launch_down<T, false, 2>(f, h, dev, s);
+    if (f.T <= 16) return launch_down<T, false, 4>(f, h, dev, s);
+    return launch_down<T, false, 8>(f, h, dev, s);
 }
 
 }  // namespace
 
-size_t ffn_scratch_bytes(int64_t T, int64_t I, int k) { return static_cast<size_t>(T) * k * I * 4; }
+size_t ffn_scratch_bytes(int64_t T, int64_t I, int k) { return static_cast<size_t>(T) * k * 2 * I * 2; }
 
-gemm_status_t run_ffn(bool bf16, const FfnParams& p, uint8_t* data, const DeviceView&, gemm_stream_t stream) {
+gemm_status_t run_ffn(bool bf16, const FfnParams& p, uint8_t* data, const DeviceView& dev, gemm_stream_t stream) {
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    float* h = reinterpret_cast<float*>(data);
-    const cudaError_t e = bf16 ? launch<__nv_bfloat16>(p, h, s) : launch<__half>(p, h, s);
-    return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+    const gemm_status_t st = bf16 ? up<__nv_bfloat16>(p, data, dev, s) : up<__half>(p, data, dev, s);
+    if (st != GEMM_OK) return st;
+    return bf16 ? down<__nv_bfloat16>(p, data, dev, s) : down<__half>(p, data, dev, s);
 }
 
 }  // namespace gemm_gb300

@@ -1,0 +1,146 @@
+// rows_host.cuh -- host side of the weight-streaming kernels: tensor maps,
+// the split of rows over clusters, launches.
+#pragma once
+
+#include <algorithm>
+#include <map>
+#include <mutex>
+
+#include "llm/rows.cuh"
+
+namespace gemm_gb300 {
+
+constexpr uint64_t kStreamTimeoutNs = 4000000000ull;
+constexpr int kMaxDynamicSmem = 226 * 1024;   // 227 KB less the barriers
+
+struct SideGroups {
+    int groups_k = 0, stage_groups = 0, chunks_per_group = 0;
+    SideGroups(const Weights& w, int64_t K) {
+        if (w.scales == nullptr) return;
+        groups_k = static_cast<int>(K / w.group);
+        stage_groups = 256 / w.group;
+        chunks_per_group = w.group / 32;
+    }
+};
+
+// Weights that cannot stay in L2 (129 MB) from one call to the next anyway
+// are read with evict-first, so they do not push out what can.
+inline int32_t stream_weights(bool w4, int64_t rows, int64_t K) { return (w4 ? rows * K / 2 : rows * K * 2) > (48ll << 20); }
+
+// Tensor maps of a stack: rows x K codes or 16-bit numbers in boxes of
+// box_rows x 128 bytes; scales and zero points [side_rows][N] in boxes of
+// stage_groups x side_box.
+inline bool encode_weights(const Weights& w, int64_t rows, int64_t side_rows, int64_t N, int64_t K, int box_rows,
+                           int side_box, int stage_groups, CUtensorMap* tw, CUtensorMap* ts, CUtensorMap* tz) {
+    if (w.scales == nullptr) {
+        if (!encode_map(tw, w.data, 2, K, rows, 64, static_cast<uint32_t>(box_rows), true)) return false;
+        *ts = *tz = *tw;   // not used
+        return true;
+    }
+    if (!encode_map(tw, w.data, 1, K / 2, rows, 128, static_cast<uint32_t>(box_rows), true)) return false;
+    if (!encode_map(ts, w.scales, 2, N, side_rows, static_cast<uint32_t>(side_box), static_cast<uint32_t>(stage_groups), false)) return false;
+    if (w.zeros == nullptr) {
+        *tz = *ts;
+        return true;
+    }
+    return encode_map(tz, w.zeros, 2, N, side_rows, static_cast<uint32_t>(side_box), static_cast<uint32_t>(stage_groups), false);
+}
+
+// Lifts a kernel's shared-memory limit, once per kernel and device.
+inline cudaError_t allow_smem(const void* kernel, int dev) {
+    static std::mutex mu;
+    static std::map<std::pair<const void*, int>, bool> done;
+    std::lock_guard<std::mutex> lock(mu);
+    bool& ready = done[std::make_pair(kernel, dev)];
+    if (ready) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicSmem);
+    ready = e == cudaSuccess;
+    return e;
+}
+
+// Programmatic stream serialisation, and clusters of `cluster` CTAs.
+template <class Kernel, class Params>
+gemm_status_t launch_stream(Kernel kernel, int dev, int grid, int cluster, int smem, cudaStream_t s, const CUtensorMap& w,
+                            const CUtensorMap& sc, const CUtensorMap& zr, const Params& p) {
+    if (allow_smem(reinterpret_cast<const void*>(kernel), dev) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_CUDA;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(kStreamThreads, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
+    if (cluster > 1) {
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+    }
+    cfg.attrs = attr;
+    if (cudaLaunchKernelEx(&cfg, kernel, w, sc, zr, p) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_LAUNCH;
+    }
+    return GEMM_OK;
+}
+
+// Fills the split and the shared-memory layout of `p` (N, K, k_stages set):
+// `tokens` outputs per row, `cols` columns per stage.  Returns the dynamic
+// shared memory of the launch, 0 when nothing fits.
+template <class T, bool W4, int NT, bool MOE>
+int plan_rows(RowsParams* p, int tokens, int cols, int stage_groups, int lists, int budget, const DeviceView& dev) {
+    constexpr int MT = kTilesPerWarp<NT>;
+    const int table_cols = MOE ? tokens : 8 * NT;
+    int best = 0;
+    double best_t = 0.0;
+    RowsParams got = *p;
+    for (int P = 1; P <= 8; P *= 2) {
+        const int clusters = dev.sms / P;
+        // as few rounds of clusters as keep a range within a TMA box (256 rows)
+        // and the consumers' registers
+        const int most = std::min(256, kConsumers * MT * 16);
+        const int rounds = (p->N + clusters * most - 1) / (clusters * most);
+        const int width = up_to((p->N + clusters * rounds - 1) / (clusters * rounds), 8);
+        const int tiles = (width + 15) / 16;
+        // As few warps per stage as the registers allow, more where the tables
+        // or a ring of KW stages would leave too little in flight.
+        for (int mw = 1; mw <= kConsumers; mw *= 2) {
+            if (mw * MT < tiles) continue;
+            const int kw = kConsumers / mw;
+            RowsParams c = *p;
+            c.width = width;
+            c.ranges = (p->N + width - 1) / width;
+            c.pieces = P;
+            c.mw = mw;
+            c.table_pitch = up_to(tiles * 16, 32) + 8;
+            const int tables = kw * table_cols * c.table_pitch * 4;
+            const int recv = P > 1 ? up_to((tokens * width + P - 1) / P * P * 4, 128) : 0;
+            const int fixed = lists + tables + recv + 1024;
+            c.ring = ring_layout(W4, width, width, stage_groups, cols, budget - fixed, kw);
+            if (c.ring.end + fixed > kMaxDynamicSmem || c.ring.stages < 2) continue;
+            // bytes a CTA streams, slowed by a shallow ring, and the exchange
+            const double stages = static_cast<double>((p->k_stages + P - 1) / P);
+            const double flight = std::min(1.0, c.ring.stages * width * 128 / 65536.0);
+            const double t = rounds * stages * (width + (W4 ? 4 : 1) * cols * 0.5) * 128 / 45000.0 / flight +
+                             (P > 1 ? 1.0 : 0.0);
+            if (best == 0 || t < best_t) {
+                best_t = t;
+                c.list_off = c.ring.end;
+                c.table_off = c.list_off + lists;
+                c.recv_off = c.table_off + tables;
+                best = c.recv_off + recv + 1024;
+                got = c;
+            }
+        }
+    }
+    if (best) *p = got;
+    return best;
+}
+
+}  // namespace gemm_gb300
