@@ -53,7 +53,10 @@ cudaError_t launch_w4_dequantize(bool bf16, const Weights& w, int64_t batch, int
 gemm_status_t run_w4_gemm(bool bf16, const void* A, const Weights& w, void* D, int64_t M, int64_t N, int64_t K,
                           const EpiParams& epi, const DeviceView& dev, gemm_stream_t stream);
 
-gemm_status_t run_route(bool bf16, const RouteParams& p, const DeviceView& dev, gemm_stream_t stream);
+// bytes of scratch that run_route needs at `data`; counters: one zero, left at zero
+size_t route_scratch_bytes(int64_t T, int64_t E);
+gemm_status_t run_route(bool bf16, const RouteParams& p, uint8_t* data, uint32_t* counters, const DeviceView& dev,
+                        gemm_stream_t stream);
 
 // bytes of scratch that run_ffn needs at `data`
 size_t ffn_scratch_bytes(int64_t T, int64_t I, int k);

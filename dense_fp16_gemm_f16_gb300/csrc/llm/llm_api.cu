@@ -210,7 +210,10 @@ gemm_status_t route(int dtype, const void* X, const void* Wr, const float* bias,
     if (st != GEMM_OK) return st;
     const RouteParams p{X, Wr, bias, T, static_cast<int32_t>(H), static_cast<int32_t>(E), k, scoring, renormalize, ids,
                         weights};
-    return run_route(dtype == GEMM_DTYPE_BF16, p, dev, stream);
+    Scratch ws;
+    st = get_scratch(dev.dev, stream, route_scratch_bytes(T, E), &ws);
+    if (st != GEMM_OK) return st;
+    return run_route(dtype == GEMM_DTYPE_BF16, p, ws.data, ws.counters, dev, stream);
 }
 
 // The checks that gemm_moe_ffn and gemm_moe_layer share; fills all of `p` but ids and weights.
@@ -276,21 +279,21 @@ gemm_status_t layer(int dtype, const void* X, const void* Wr, const float* bias,
     DeviceView dev;
     st = device_view(&dev);
     if (st != GEMM_OK) return st;
-    // scratch: ids, weights (256-byte padded each), then run_ffn's own
-    const size_t side = (static_cast<size_t>(T) * k * 4 + 255) / 256 * 256;
+    // scratch: run_route's, ids and weights (256-byte padded each), run_ffn's
+    const size_t logits = route_scratch_bytes(T, E), side = (static_cast<size_t>(T) * k * 4 + 255) / 256 * 256;
     Scratch ws;
-    st = get_scratch(dev.dev, stream, 2 * side + ffn_scratch_bytes(T, I, k), &ws);
+    st = get_scratch(dev.dev, stream, logits + 2 * side + ffn_scratch_bytes(T, I, k), &ws);
     if (st != GEMM_OK) return st;
-    int32_t* ids = reinterpret_cast<int32_t*>(ws.data);
-    float* weights = reinterpret_cast<float*>(ws.data + side);
+    int32_t* ids = reinterpret_cast<int32_t*>(ws.data + logits);
+    float* weights = reinterpret_cast<float*>(ws.data + logits + side);
     const RouteParams r{X, Wr, bias, T, static_cast<int32_t>(H), static_cast<int32_t>(E), k, scoring, renormalize, ids,
                         weights};
     const bool bf16 = dtype == GEMM_DTYPE_BF16;
-    st = run_route(bf16, r, dev, stream);
+    st = run_route(bf16, r, ws.data, ws.counters, dev, stream);
     if (st != GEMM_OK) return st;
     p.ids = ids;
     p.weights = weights;
-    return run_ffn(bf16, p, ws.data + 2 * side, dev, stream);
+    return run_ffn(bf16, p, ws.data + logits + 2 * side, dev, stream);
 }
 
 }  // namespace

@@ -9,21 +9,18 @@
 namespace gemm_gb300 {
 namespace {
 
-// Shared memory of each of the two kernels: at most half of an SM's, so the
-// second product's CTA finds room beside the first's and has its first ring of
-// weights in flight when the first product ends.
-constexpr int kFfnSmem = 200 * 1024;
+// Slots of an expert when the choices are even, for the experts that get any.
+int typical_slots(const FfnParams& f) { return std::max(1, (f.T * f.k + f.E - 1) / f.E); }
 
-template <class T, bool W4, int NT>
+template <class T, int CPG, int NT>
 gemm_status_t launch_up(const FfnParams& f, void* h, const DeviceView& dev, cudaStream_t s) {
+    constexpr bool W4 = CPG != 0;
     UpParams p{};
     p.H = f.H;
     p.I = f.I;
-    p.k_stages = (f.H + kStageElems<W4> - 1) / kStageElems<W4>;
     const SideGroups sg(f.w13, f.H);
     p.groups_k = sg.groups_k;
-    p.stage_groups = sg.stage_groups;
-    p.chunks_per_group = sg.chunks_per_group;
+    p.atom_groups = sg.atom_groups;
     p.has_zeros = f.w13.zeros != nullptr;
     const int64_t rows = 2ll * f.I * f.E;
     p.stream_w = stream_weights(W4, rows, f.H);
@@ -39,40 +36,39 @@ gemm_status_t launch_up(const FfnParams& f, void* h, const DeviceView& dev, cuda
     const int lists = list_offsets(f.T * f.k, f.E).end;
     const int cols = std::min(8 * NT, f.T);
     int smem = 0;
-    for (p.mw = kUpGranules / kTilesPerWarp<NT>; p.mw <= kUpGranules; p.mw *= 2) {
-        // as few warps per stage as the registers allow, more where the sums or
-        // a ring of KW stages would leave too little in flight
-        const int kw = kConsumers / p.mw;
-        const int sums = 2 * kw * 8 * NT * kUpPitch * 4;
-        p.ring = ring_layout(W4, kUpRows, 2 * kUpGranules * 8, sg.stage_groups, cols, kFfnSmem - 1024 - lists - sums, kw);
+    for (int mw = kUpGranules / kTilesPerWarp<W4, NT>; mw <= kUpGranules; mw *= 2) {
+        // as few warps per stage as the registers allow, more where the sums
+        // would leave too little in flight
+        const int kw = kConsumers / mw;
+        const int sums = kw * 8 * NT * kUpPitch * 4;
+        p.mw = mw;
+        p.ring = ring_layout(W4, 1, kUpRows, 2 * kUpGranules * 8, sg.atom_groups, cols, kSmemBudget<NT> - 1024 - lists - sums, kw);
         p.list_off = p.ring.end;
         p.sums_off = p.list_off + lists;
         smem = p.sums_off + sums + 1024;
-        if (smem <= kFfnSmem && p.ring.stages >= 4) break;
+        if (smem <= kSmemBudget<NT> && p.ring.slots >= 8) break;
     }
-    if (p.mw > kUpGranules) {
-        p.mw = kUpGranules;
-        if (smem > kMaxDynamicSmem) return GEMM_ERR_CUDA;
-    }
+    if (smem > kMaxDynamicSmem) return GEMM_ERR_CUDA;
+    p.k_stages = (f.H + kAtomElems<W4> - 1) / kAtomElems<W4>;
     CUtensorMap w, sc, zr;
-    if (!encode_weights(f.w13, rows, static_cast<int64_t>(f.E) * sg.groups_k, 2 * f.I, f.H, 8, kUpGranules * 8, sg.stage_groups, &w, &sc, &zr))
+    if (!encode_weights(f.w13, rows, static_cast<int64_t>(f.E) * sg.groups_k, 2 * f.I, f.H, 8, kUpGranules * 8, sg.atom_groups, &w, &sc, &zr) ||
+        !encode_weights_box(f.w13, rows, f.H, 8 * kUpGranules, &p.tm_piece))
         return GEMM_ERR_INVALID_VALUE;
-    return launch_stream(moe_up_kernel<T, W4, NT>, dev.dev, dev.sms, 1, smem, s, w, sc, zr, p);
+    return launch_stream(moe_up_kernel<T, CPG, NT>, dev.dev, kCtasPerSm<NT> * dev.sms, 1, smem, s, w, sc, zr, p);
 }
 
-template <class T, bool W4, int NT>
+template <class T, int CPG, int NT>
 gemm_status_t launch_down(const FfnParams& f, const void* h, const DeviceView& dev, cudaStream_t s) {
+    constexpr bool W4 = CPG != 0;
     RowsParams p{};
     const SideGroups sg(f.w2, f.I);
     const int lists = list_offsets(f.T * f.k, f.E).end;
     p.N = f.H;
     p.K = f.I;
-    p.k_stages = (f.I + kStageElems<W4> - 1) / kStageElems<W4>;
-    const int smem = plan_rows<T, W4, NT, true>(&p, f.T, std::min(8 * NT, 2 * f.T), sg.stage_groups, lists, kFfnSmem, dev);
+    const int smem = plan_rows<W4, NT, true>(&p, f.T, std::min(8 * NT, 2 * f.T), std::min(8 * NT, 2 * typical_slots(f)), sg.atom_groups, lists, dev);
     if (smem <= 0) return GEMM_ERR_CUDA;
     p.groups_k = sg.groups_k;
-    p.stage_groups = sg.stage_groups;
-    p.chunks_per_group = sg.chunks_per_group;
+    p.atom_groups = sg.atom_groups;
     p.has_zeros = f.w2.zeros != nullptr;
     const int64_t rows = static_cast<int64_t>(f.H) * f.E;
     p.stream_w = stream_weights(W4, rows, f.I);
@@ -86,37 +82,55 @@ gemm_status_t launch_down(const FfnParams& f, const void* h, const DeviceView& d
     p.status = dev.status;
     p.timeout_ns = kStreamTimeoutNs;
     CUtensorMap w, sc, zr;
-    if (!encode_weights(f.w2, rows, static_cast<int64_t>(f.E) * sg.groups_k, f.H, f.I, p.width, p.width, sg.stage_groups, &w, &sc, &zr))
+    if (!encode_weights(f.w2, rows, static_cast<int64_t>(f.E) * sg.groups_k, f.H, f.I, p.width, p.width, p.ring.atoms * sg.atom_groups, &w, &sc, &zr))
         return GEMM_ERR_INVALID_VALUE;
-    return launch_stream(weight_rows_kernel<T, W4, NT, true>, dev.dev, p.ranges * p.pieces, p.pieces, smem, s, w, sc, zr, p);
+    return launch_stream(weight_rows_kernel<T, CPG, NT, true>, dev.dev, p.ranges * p.pieces, p.pieces, smem, s, w, sc, zr, p);
 }
 
-// Columns a segment may have: as many as one expert can get, up to 64 for
-// 16-bit weights and 32 for 4-bit ones, whose group sums take registers too.
-template <class T>
+// Columns a segment may have: twice what an expert gets when the choices are
+// even (an expert with more has its weights read again, mostly from L2), at most
+// 64 for 16-bit weights and 32 for 4-bit ones, whose group sums take registers
+// too.  Narrow kernels keep more tiles per warp and two CTAs per SM.
+int segment_slots(const FfnParams& f) { return std::min(f.T, 2 * typical_slots(f)); }
+
+template <class T, int CPG>
 gemm_status_t up(const FfnParams& f, void* h, const DeviceView& dev, cudaStream_t s) {
-    if (f.w13.scales != nullptr) {
-        if (f.T <= 8) return launch_up<T, true, 1>(f, h, dev, s);
-        if (f.T <= 16) return launch_up<T, true, 2>(f, h, dev, s);
-        return launch_up<T, true, 4>(f, h, dev, s);
+    const int cols = segment_slots(f);
+    if (cols <= 8) return launch_up<T, CPG, 1>(f, h, dev, s);
+    if (cols <= 16) return launch_up<T, CPG, 2>(f, h, dev, s);
+    if constexpr (CPG == 0) {
+        if (cols > 32) return launch_up<T, CPG, 8>(f, h, dev, s);
     }
-    if (f.T <= 8) return launch_up<T, false, 1>(f, h, dev, s);
-    if (f.T <= 16) return launch_up<T, false, 2>(f, h, dev, s);
-    if (f.T <= 32) return launch_up<T, false, 4>(f, h, dev, s);
-    return launch_up<T, false, 8>(f, h, dev, s);
+    return launch_up<T, CPG, 4>(f, h, dev, s);
+}
+
+template <class T, int CPG>
+gemm_status_t down(const FfnParams& f, const void* h, const DeviceView& dev, cudaStream_t s) {
+    const int cols = 2 * segment_slots(f);
+    if (cols <= 8) return launch_down<T, CPG, 1>(f, h, dev, s);
+    if (cols <= 16) return launch_down<T, CPG, 2>(f, h, dev, s);
+    if constexpr (CPG == 0) {
+        if (cols > 32) return launch_down<T, CPG, 8>(f, h, dev, s);
+    }
+    return launch_down<T, CPG, 4>(f, h, dev, s);
 }
 
 template <class T>
-gemm_status_t down(const FfnParams& f, const void* h, const DeviceView& dev, cudaStream_t s) {
-    if (f.w2.scales != nullptr) {
-        if (f.T <= 4) return launch_down<T, true, 1>(f, h, dev, s);
-        if (f.T <= 8) return launch_down<T, true, 2>(f, h, dev, s);
-        return launch_down<T, true, 4>(f, h, dev, s);
+gemm_status_t both(const FfnParams& f, void* h, const DeviceView& dev, cudaStream_t s) {
+    gemm_status_t st;
+    switch (f.w13.group) {
+        case 32: st = up<T, 1>(f, h, dev, s); break;
+        case 64: st = up<T, 2>(f, h, dev, s); break;
+        case 128: st = up<T, 4>(f, h, dev, s); break;
+        default: st = up<T, 0>(f, h, dev, s);
     }
-    if (f.T <= 4) return launch_down<T, false, 1>(f, h, dev, s);
-    if (f.T <= 8) return launch_down<T, false, 2>(f, h, dev, s);
-    if (f.T <= 16) return launch_down<T, false, 4>(f, h, dev, s);
-    return launch_down<T, false, 8>(f, h, dev, s);
+    if (st != GEMM_OK) return st;
+    switch (f.w2.group) {
+        case 32: return down<T, 1>(f, h, dev, s);
+        case 64: return down<T, 2>(f, h, dev, s);
+        case 128: return down<T, 4>(f, h, dev, s);
+        default: return down<T, 0>(f, h, dev, s);
+    }
 }
 
 }  // namespace
@@ -125,9 +139,7 @@ size_t ffn_scratch_bytes(int64_t T, int64_t I, int k) { return static_cast<size_
 
 gemm_status_t run_ffn(bool bf16, const FfnParams& p, uint8_t* data, const DeviceView& dev, gemm_stream_t stream) {
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const gemm_status_t st = bf16 ? up<__nv_bfloat16>(p, data, dev, s) : up<__half>(p, data, dev, s);
-    if (st != GEMM_OK) return st;
-    return bf16 ? down<__nv_bfloat16>(p, data, dev, s) : down<__half>(p, data, dev, s);
+    return bf16 ? both<__nv_bfloat16>(p, data, dev, s) : both<__half>(p, data, dev, s);
 }
 
 }  // namespace gemm_gb300

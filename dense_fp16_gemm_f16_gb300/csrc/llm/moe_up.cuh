@@ -2,12 +2,12 @@
 // them: h = silu(G x) * (U x) for every (token, expert) pair.
 //
 // Work split.  The gate rows of all segments, in granules of 8, form one list
-// that the CTAs (one per SM) share evenly; each granule brings the 8 up rows that
+// that the CTAs (one per SM or two) share evenly; each granule brings the 8 up rows that
 // belong to it, as the other half of a 16-row MMA tile, so both sums of an h
 // lie in one thread.  A CTA takes its granules in pieces of up to 4 of one
 // expert, each piece over all of K: no sums cross CTAs.  The stage groups' sums
-// of a piece meet in shared memory (two buffers in turn), where the gated
-// product is formed in fp32.
+// of a piece meet in shared memory, where the gated product is formed in fp32,
+// while the copies of the next pieces are in flight.
 // h goes to the second product as the sum of two numbers of the activations'
 // type, rows 2 s and 2 s + 1 for slot s: one rounding to 16 bits here would cost
 // as much accuracy as the output's own, and two columns instead of one are
@@ -26,10 +26,11 @@ constexpr int kUpRows = kUpGranules * 16;         // rows of gate and up togethe
 constexpr int kUpPitch = kUpRows + 8;
 
 struct UpParams {
+    CUtensorMap tm_piece;         // the weights in boxes of kUpGranules granules (tmW: of one)
     RingLayout ring;
     int32_t list_off, sums_off;
     int32_t H, I, k_stages, mw;
-    int32_t groups_k, stage_groups, chunks_per_group, has_zeros;
+    int32_t groups_k, atom_groups, has_zeros;
     int32_t stream_w;
     const void* X;                // [T][H]
     void* h;                      // [2 T k][I]
@@ -56,10 +57,11 @@ struct UpPieces {
     }
 };
 
-template <class T, bool W4, int NT>
-__global__ void __launch_bounds__(kStreamThreads, 1)
+template <class T, int CPG, int NT>
+__global__ void __launch_bounds__(kStreamThreads, kCtasPerSm<NT>)
 moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmS,
-              const __grid_constant__ CUtensorMap tmZ, const UpParams p) {
+              const __grid_constant__ CUtensorMap tmZ, const __grid_constant__ UpParams p) {
+    constexpr bool W4 = CPG != 0;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_u32(smem_raw);
     uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -67,15 +69,16 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
     __shared__ __align__(8) uint64_t bars[2 * kMaxRing];
     const uint32_t bar0 = ptx::smem_u32(bars);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int NS = p.ring.stages;
+    const int KW = kConsumers / p.mw;
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (kMaxRing + s); };
     if (warp == 0 && lane == 0) {
         ptx::prefetch_tensormap(&tmW);
-        for (int s = 0; s < NS; ++s) {
-            ptx::mbar_init(full_bar(s), 1);
-            ptx::mbar_init(empty_bar(s), static_cast<uint32_t>(p.mw));
-        }
+        ptx::prefetch_tensormap(&p.tm_piece);
+    }
+    if (static_cast<int>(threadIdx.x) < p.ring.slots) {
+        ptx::mbar_init(full_bar(threadIdx.x), kFullArrivals);
+        ptx::mbar_init(empty_bar(threadIdx.x), static_cast<uint32_t>(p.mw));
         ptx::fence_mbar_init();
     }
     ptx::griddep_wait();
@@ -85,97 +88,120 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
     const SlotLists lists = build_lists(p.ids, p.weights, p.T, p.k, p.E, NT * 8, smem + p.list_off);
     const int per_seg = p.I / 8;
     const int64_t total = static_cast<int64_t>(lists.nseg) * per_seg;
-    UpPieces pieces{total * blockIdx.x / gridDim.x, total * (blockIdx.x + 1) / gridDim.x, per_seg};
-    int seg, at, count;
+    const UpPieces all{total * blockIdx.x / gridDim.x, total * (blockIdx.x + 1) / gridDim.x, per_seg};
 
-    if (warp == kConsumers) {
-        // ------------------------------------------------------------ producer
-        const uint64_t pol_w = p.stream_w ? ptx::policy_evict_first() : ptx::policy_evict_normal();
-        const T* X = static_cast<const T*>(p.X);
-        bool ok = true;
-        int i = 0;
-        while (ok && pieces.next(seg, at, count)) {
-            const int first = lists.seg_begin[seg], n = lists.seg_begin[seg + 1] - first;
-            const int32_t gate = lists.seg_e[seg] * 2 * p.I + at * 8, up = gate + p.I;   // rows of the stack
-            const uint32_t side_tx = W4 ? static_cast<uint32_t>(2 * kUpGranules * 8 * p.stage_groups * 2) * (p.has_zeros ? 2u : 1u) : 0u;
-            for (int kb = 0; kb < p.k_stages; ++kb, ++i) {
-                const int s = i % NS;
-                if (i >= NS && !wait_phase_warp(empty_bar(s), ((i / NS) & 1) ^ 1u, p.status, kSiteStreamEmpty, p.timeout_ns)) {
-                    ok = false;
-                    break;
-                }
-                const int kv = min(kStageElems<W4>, p.H - kb * kStageElems<W4>);
-                if (lane == 0)
-                    ptx::mbar_arrive_expect_tx(full_bar(s), static_cast<uint32_t>(count) * 2048u + side_tx + static_cast<uint32_t>(n * kv * 2));
-                __syncwarp();
-                // granule i: 8 gate rows, then its 8 up rows
-                if (lane < 2 * count) {
-                    const int32_t y = ((lane & 1) ? up : gate) + (lane >> 1) * 8;
-                    ptx::tma_load_2d_hint(base + static_cast<uint32_t>(s * p.ring.w_bytes + lane * 1024), &tmW, full_bar(s),
-                                          kb * (W4 ? 128 : 64), y, pol_w);
-                }
-                if constexpr (W4) {
-                    // [gate | up] x [groups][32 rows] of scales, then of zero points
-                    const uint32_t side = base + static_cast<uint32_t>(p.ring.side_off + s * p.ring.side_bytes);
-                    if (lane < (p.has_zeros ? 4 : 2)) {
-                        const int x = at * 8 + ((lane & 1) ? p.I : 0);
-                        ptx::tma_load_2d(side + static_cast<uint32_t>((lane >> 1) * (p.ring.side_bytes / 2) + (lane & 1) * kUpGranules * 8 * p.stage_groups * 2),
-                                         (lane >> 1) ? &tmZ : &tmS, full_bar(s), x, lists.seg_e[seg] * p.groups_k + kb * p.stage_groups);
-                    }
-                }
-                const uint32_t dst = base + static_cast<uint32_t>(p.ring.x_off + s * p.ring.x_bytes);
-                for (int c = lane; c < n; c += 32)
-                    ptx::bulk_load(dst + static_cast<uint32_t>(c * kColPitch<W4>),
-                                   X + static_cast<int64_t>(lists.slot[first + c] / p.k) * p.H + static_cast<int64_t>(kb) * kStageElems<W4>,
-                                   static_cast<uint32_t>(kv * 2), full_bar(s));
-            }
+    constexpr int KE = kAtomElems<W4>;
+    const int pitch = col_pitch(W4, 1);
+    const int mg = warp % p.mw, kg = warp / p.mw;
+    const GroupSlots own(p.ring.slots, KW, kg);
+    const uint64_t pol_w = p.stream_w ? ptx::policy_evict_first() : ptx::policy_evict_normal();
+    const uint32_t side_half = static_cast<uint32_t>(kUpGranules * 8 * p.atom_groups * 2);
+    constexpr uint32_t kHalf = kUpGranules * 1024;   // up rows behind the gate rows
+
+    // The copies of one stage (K atom kb of a piece) into slot s.
+    auto issue = [&](int seg, int at, int count, int kb, int s) {
+        const int first = lists.seg_begin[seg], n = lists.seg_begin[seg + 1] - first;
+        const int e = lists.seg_e[seg];
+        const int kv = min(KE, p.H - kb * KE);
+        if (lane == 0)
+            ptx::mbar_arrive_expect_tx(full_bar(s), static_cast<uint32_t>(count) * 2048u +
+                                                        (W4 ? 2u * side_half * (p.has_zeros ? 2u : 1u) : 0u));
+        __syncwarp();
+        const int32_t y = e * 2 * p.I + at * 8 + ((lane & 1) ? p.I : 0);   // even lanes: gate rows, odd lanes: up rows
+        const uint32_t dst = base + static_cast<uint32_t>(s * p.ring.w_bytes) + (lane & 1) * kHalf;
+        if (count == kUpGranules) {
+            if (lane < 2) ptx::tma_load_2d_hint(dst, &p.tm_piece, full_bar(s), kb * (W4 ? 128 : 64), y, pol_w);
+        } else if (lane < 2 * count) {
+            ptx::tma_load_2d_hint(dst + (lane >> 1) * 1024u, &tmW, full_bar(s), kb * (W4 ? 128 : 64), y + (lane >> 1) * 8, pol_w);
         }
-        if (!ok) {   // leave no copy in flight behind
-            for (int s = 0; s < NS; ++s)
-                for (uint32_t ph = 0; ph < 2; ++ph) wait_phase(full_bar(s), ph, p.status, kSiteStreamDrain, 1000000);
+        if constexpr (W4) {
+            // [scales | zero points] x [gate | up] x [groups][32 rows]
+            const int q = lane - 8;
+            if (q >= 0 && q < (p.has_zeros ? 4 : 2))
+                ptx::tma_load_2d(base + static_cast<uint32_t>(p.ring.side_off + s * p.ring.side_bytes + (q >> 1) * (p.ring.side_bytes / 2)) + (q & 1) * side_half,
+                                 (q >> 1) ? &tmZ : &tmS, full_bar(s), at * 8 + ((q & 1) ? p.I : 0), e * p.groups_k + kb * p.atom_groups);
         }
-    } else {
-        // ------------------------------------------------------------ consumers
-        const int KW = kConsumers / p.mw;
-        const int mg = warp % p.mw, kg = warp / p.mw;
+        const uint32_t x = base + static_cast<uint32_t>(p.ring.x_off + s * p.ring.x_bytes);
+        constexpr int kShift = W4 ? 5 : 3;   // 32 or 8 pieces of 16 bytes per column
+        for (int i = lane; i < n << kShift; i += 32) {
+            const int c = i >> kShift, o = (i - (c << kShift)) * 8;
+            if (o < kv)
+                ptx::cp_async16(x + static_cast<uint32_t>(c * pitch + o * 2),
+                                static_cast<const T*>(p.X) + static_cast<int64_t>(lists.slot[first + c] / p.k) * p.H + static_cast<int64_t>(kb) * KE + o);
+        }
+        ptx::cp_async_arrive(full_bar(s));
+    };
+    // The group's next stage to fetch: it walks the pieces ahead of the sums.
+    UpPieces ahead = all;
+    int f_seg = 0, f_at = 0, f_count = 0, f_kb = kg - KW;
+    bool f_more = ahead.next(f_seg, f_at, f_count);
+    auto fetch_next = [&](int s) {
+        f_kb += KW;
+        while (f_more && f_kb >= p.k_stages) {
+            f_kb -= p.k_stages;
+            f_more = ahead.next(f_seg, f_at, f_count);
+        }
+        if (f_more) issue(f_seg, f_at, f_count, f_kb, s);
+        return f_more;
+    };
+
+    {
         const int g = lane >> 2, t = lane & 3;
         constexpr int kCols = 8 * NT;
+        const int tile0 = mg * StreamWarp<T, W4, NT>::MT;   // this warp's tiles
         float* sums = reinterpret_cast<float*>(smem + p.sums_off);
         T* h = static_cast<T*>(p.h);
+        if (mg == 0)
+            for (int d = 0; d < own.depth; ++d)
+                if (!fetch_next(own.first + d)) break;
         StreamWarp<T, W4, NT> sw;
         bool ok = true;
-        int i = 0;   // stages before this piece
-        for (int buf = 0; pieces.next(seg, at, count); buf ^= 1) {
+        int d = 0, kb = kg;
+        uint32_t phase = 0;
+        UpPieces pieces = all;
+        int seg, at, count;
+        while (pieces.next(seg, at, count)) {
             const int first = lists.seg_begin[seg], n = lists.seg_begin[seg + 1] - first;
             const int nt = (n + 7) >> 3;
             sw.clear();
-            for (int kb = (kg - i % KW + KW) % KW; ok && kb < p.k_stages; kb += KW) {
-                const int s = (i + kb) % NS;
-                if (!wait_phase_warp(full_bar(s), ((i + kb) / NS) & 1, p.status, kSiteStreamFull, p.timeout_ns)) {
+            for (; ok && kb < p.k_stages; kb += KW) {
+                const int s = own.first + d;
+                if (!wait_phase_warp(full_bar(s), phase, p.status, kSiteStreamFull, p.timeout_ns)) {
                     ok = false;
                     break;
                 }
-                const int kv = min(kStageElems<W4>, p.H - kb * kStageElems<W4>);
-                const uint32_t w = base + static_cast<uint32_t>(s * p.ring.w_bytes);
-                const uint32_t x = base + static_cast<uint32_t>(p.ring.x_off + s * p.ring.x_bytes);
+                const int kv = min(KE, p.H - kb * KE);
+                const uint32_t there = base + ptx::stage_token();
+                const uint32_t w = there + static_cast<uint32_t>(s * p.ring.w_bytes + tile0 * 1024);
+                const uint32_t x = there + static_cast<uint32_t>(p.ring.x_off + s * p.ring.x_bytes);
                 if constexpr (W4) {
-                    const uint32_t sc = base + static_cast<uint32_t>(p.ring.side_off + s * p.ring.side_bytes);
-                    const uint32_t zr = sc + static_cast<uint32_t>(p.ring.side_bytes / 2);
-                    const uint32_t half = static_cast<uint32_t>(kUpGranules * 8 * p.stage_groups * 2);
-                    const SideView side{{sc, sc + half}, {zr, zr + half}, kUpGranules * 8, 8};
-                    sw.stage4(w, x, side, p.has_zeros != 0, kv, p.chunks_per_group, count, mg, p.mw, nt, lane);
+                    const uint32_t sc = there + static_cast<uint32_t>(p.ring.side_off + s * p.ring.side_bytes + tile0 * 16);
+                    const SideView side{sc, sc + static_cast<uint32_t>(p.ring.side_bytes / 2), side_half, kUpGranules * 16u};
+                    sw.template atom4<CPG, 1024, 16>(w, kHalf, x, pitch, side, p.has_zeros != 0, kv, count - tile0, nt, lane);
                 } else {
-                    sw.stage16(w, x, kv, count, mg, p.mw, nt, lane);
+                    sw.template atom16<1024>(w, kHalf, x, pitch, kv, count - tile0, nt, lane);
                 }
+                sw.hold();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(empty_bar(s));
+                if (p.mw > 1) {
+                    if (lane == 0) ptx::mbar_arrive(empty_bar(s));
+                    if (mg == 0 && f_more && !wait_phase_warp(empty_bar(s), phase, p.status, kSiteStreamEmpty, p.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                }
+                if (mg == 0 && f_more) fetch_next(s);
+                if (++d == own.depth) {
+                    d = 0;
+                    phase ^= 1u;
+                }
             }
-            i += p.k_stages;
+            kb -= p.k_stages;   // where this group's stages go on in the next piece
             // [stage group][column][tile * 16 + (gate: g, up: 8 + g)]
-            float* mine = sums + (buf * KW + kg) * kCols * kUpPitch;
+            float* mine = sums + kg * kCols * kUpPitch;
 #pragma unroll
             for (int jt = 0; jt < sw.MT; ++jt) {
-                const int tile = mg + jt * p.mw;
+                const int tile = tile0 + jt;
                 if (tile < count) {
 #pragma unroll
                     for (int q = 0; q < NT; ++q) {
@@ -189,13 +215,11 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                     }
                 }
             }
-            ptx::named_bar_sync(1, kConsumers * 32);
-            // a buffer is written again only after the barrier of the piece in between
-            const float* from = sums + buf * KW * kCols * kUpPitch;
+            __syncthreads();
             const int rows = count * 8;
             for (int e = threadIdx.x; e < n * rows; e += kConsumers * 32) {
                 const int c = e / rows, r = e - c * rows;
-                const float* a = from + c * kUpPitch + (r >> 3) * 16 + (r & 7);
+                const float* a = sums + c * kUpPitch + (r >> 3) * 16 + (r & 7);
                 float gate = a[0], up = a[8];
                 for (int q = 1; q < KW; ++q) {
                     gate += a[q * kCols * kUpPitch];
@@ -209,6 +233,12 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 // past the type's largest number the first part is infinite and stays the value
                 h[to + p.I] = Elem<T>::from_float(isfinite(back) ? v - back : 0.0f);
             }
+            __syncthreads();   // the next piece's sums go to the same place
+        }
+        if (!ok && mg == 0) {   // leave no copy in flight behind
+            for (int q = 0; q < own.depth; ++q)
+                for (uint32_t ph = 0; ph < 2; ++ph)
+                    wait_phase(full_bar(own.first + q), ph, p.status, kSiteStreamDrain, 1000000);
         }
     }
 }

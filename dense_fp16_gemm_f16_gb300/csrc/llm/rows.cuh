@@ -8,7 +8,8 @@
 // CTA j of the cluster takes the j-th of P even shares of it.  Nearly all
 // ranges are equally wide, so every SM streams nearly the same bytes.
 // Sums.  A warp adds its registers to its own fp32 table [column or token][row]
-// in shared memory whenever it moves to another segment; warps that own the
+// in shared memory whenever it moves to another segment (the plain product has
+// one and just stores); warps that own the
 // same rows (the KW stage groups) have tables of their own, so no two threads
 // ever add to one number.  At the end the tables are added in a fixed order,
 // across the cluster through distributed shared memory, and each output is
@@ -25,11 +26,11 @@ struct RowsParams {
     RingLayout ring;
     int32_t list_off, table_off, recv_off;   // shared-memory offsets (list only for experts)
     int32_t table_pitch;                     // floats from one column to the next
-    int32_t N, K, k_stages;                  // rows of one matrix; K; stages over K
+    int32_t N, K, k_stages;                  // rows of one matrix; K; stages over K (of ring.atoms atoms)
     int32_t width, ranges, pieces;           // pieces = P
     int32_t mw;                              // warps that share a stage's tiles
     int32_t groups_k;                        // K / group (4-bit)
-    int32_t stage_groups, chunks_per_group;  // 256 / group, group / 32
+    int32_t atom_groups;                     // 256 / group
     int32_t has_zeros;
     int32_t stream_w;                        // weights larger than L2 should hold: evict first
     int32_t cols;                            // plain: rows of A in this launch; experts: tokens T
@@ -44,10 +45,12 @@ struct RowsParams {
     uint64_t timeout_ns;
 };
 
-template <class T, bool W4, int NT, bool MOE>
-__global__ void __launch_bounds__(kStreamThreads, 1)
+// CPG: 32-k chunks per group of 4-bit weights, 0 for 16-bit weights
+template <class T, int CPG, int NT, bool MOE>
+__global__ void __launch_bounds__(kStreamThreads, kCtasPerSm<NT>)
 weight_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmS,
                    const __grid_constant__ CUtensorMap tmZ, const RowsParams p) {
+    constexpr bool W4 = CPG != 0;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_u32(smem_raw);
     uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -55,23 +58,23 @@ weight_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     __shared__ __align__(8) uint64_t bars[2 * kMaxRing];
     const uint32_t bar0 = ptx::smem_u32(bars);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int NS = p.ring.stages;
+    const int KW = kConsumers / p.mw;
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (kMaxRing + s); };
 
     if (warp == 0 && lane == 0) {
         ptx::prefetch_tensormap(&tmW);
-        for (int s = 0; s < NS; ++s) {
-            ptx::mbar_init(full_bar(s), 1);
-            ptx::mbar_init(empty_bar(s), static_cast<uint32_t>(p.mw));
-        }
+    }
+    if (static_cast<int>(threadIdx.x) < p.ring.slots) {
+        ptx::mbar_init(full_bar(threadIdx.x), kFullArrivals);
+        ptx::mbar_init(empty_bar(threadIdx.x), static_cast<uint32_t>(p.mw));
         ptx::fence_mbar_init();
     }
-    const int KW = kConsumers / p.mw;
     float* table = reinterpret_cast<float*>(smem + p.table_off);
     const int tokens = MOE ? p.cols : 8 * NT;
     const int table_size = tokens * p.table_pitch;   // one stage group's
-    for (int i = threadIdx.x; i < KW * table_size; i += kStreamThreads) table[i] = 0.0f;
+    if constexpr (MOE)   // the plain product stores whole tables
+        for (int i = threadIdx.x; i < KW * table_size; i += kStreamThreads) table[i] = 0.0f;
 
     const int P = p.pieces;
     const int64_t cid = blockIdx.x / P;
@@ -87,94 +90,99 @@ weight_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     if (P > 1) ptx::cluster_sync(); else __syncthreads();
     const int total = (MOE ? lists.nseg : 1) * p.k_stages;
     const int i0 = static_cast<int>(static_cast<int64_t>(j) * total / P);
-    const int i1 = static_cast<int>(static_cast<int64_t>(j + 1) * total / P);
+    const int mine_n = static_cast<int>(static_cast<int64_t>(j + 1) * total / P) - i0;   // this CTA's stages
 
-    if (warp == kConsumers) {
-        // ------------------------------------------------------------ producer
-        const uint64_t pol_w = p.stream_w ? ptx::policy_evict_first() : ptx::policy_evict_normal();
-        const uint32_t w_tx = static_cast<uint32_t>(p.width) * 128u;
-        const uint32_t side_tx = W4 ? static_cast<uint32_t>(p.width * p.stage_groups * 2) : 0u;
-        const T* X = static_cast<const T*>(p.X);
-        bool ok = true;
-        // weights and scales of list entry i
-        auto issue_w = [&](int i, int s) {
-            const int seg = MOE ? i / p.k_stages : 0;
-            const int kb = i - seg * p.k_stages;
-            const int matrix = MOE ? lists.seg_e[seg] : 0;
-            const uint32_t dst = base + static_cast<uint32_t>(s * p.ring.w_bytes);
-            ptx::tma_load_2d_hint(dst, &tmW, full_bar(s), kb * (W4 ? 128 : 64), matrix * p.N + row0, pol_w);
-            if constexpr (W4) {
-                const uint32_t side = base + static_cast<uint32_t>(p.ring.side_off + s * p.ring.side_bytes);
-                const int y = matrix * p.groups_k + kb * p.stage_groups;
-                ptx::tma_load_2d(side, &tmS, full_bar(s), row0, y);
-                if (p.has_zeros) ptx::tma_load_2d(side + static_cast<uint32_t>(p.ring.side_bytes / 2), &tmZ, full_bar(s), row0, y);
-            }
-        };
-        auto columns = [&](int i, int& first, int& n, int& kb) {
-            const int seg = MOE ? i / p.k_stages : 0;
-            kb = i - seg * p.k_stages;
-            first = MOE ? lists.seg_begin[seg] : 0;
-            n = MOE ? 2 * (lists.seg_begin[seg + 1] - first) : p.cols;
-        };
-        auto arm = [&](int i, int s) {
-            int first, n, kb;
-            columns(i, first, n, kb);
-            const int kv = min(kStageElems<W4>, p.K - kb * kStageElems<W4>);
-            ptx::mbar_arrive_expect_tx(full_bar(s), w_tx + side_tx * (p.has_zeros ? 2u : 1u) + static_cast<uint32_t>(n * kv * 2));
-        };
-        auto issue_x = [&](int i, int s) {
-            int first, n, kb;
-            columns(i, first, n, kb);
-            const int kv = min(kStageElems<W4>, p.K - kb * kStageElems<W4>);
-            const uint32_t dst = base + static_cast<uint32_t>(p.ring.x_off + s * p.ring.x_bytes);
-            for (int c = lane; c < n; c += 32) {
-                const int64_t row = MOE ? 2 * static_cast<int64_t>(lists.slot[first + (c >> 1)]) + (c & 1) : c;
-                ptx::bulk_load(dst + static_cast<uint32_t>(c * kColPitch<W4>),
-                               X + row * p.K + static_cast<int64_t>(kb) * kStageElems<W4>, static_cast<uint32_t>(kv * 2), full_bar(s));
-            }
-        };
-        // Before the wait for the kernel before this one: with experts the first
-        // ring of weights (they were complete before that kernel began); in the
-        // plain product only a prefetch into L2, which cannot expose stale data.
-        const int pre = min(NS, i1 - i0);
-        if (lane == 0) {
-            for (int i = 0; i < pre; ++i) {
-                if constexpr (MOE) {
-                    arm(i0 + i, i);
-                    issue_w(i0 + i, i);
-                } else {
-                    ptx::tma_prefetch_2d(&tmW, (i0 + i) * (W4 ? 128 : 64), row0);
-                }
-            }
-        }
+    constexpr int KE = kAtomElems<W4>;
+    const int stage_elems = p.ring.atoms * KE;
+    const int pitch = col_pitch(W4, p.ring.atoms);
+    const int mg = warp % p.mw, kg = warp / p.mw;
+    const GroupSlots own(p.ring.slots, KW, kg);
+    const uint64_t pol_w = p.stream_w ? ptx::policy_evict_first() : ptx::policy_evict_normal();
+
+    // The weights and scales of K stage kb of segment seg into slot s, with the byte count ...
+    auto issue_w = [&](int seg, int kb, int s) {
+        const int kv = min(stage_elems, p.K - kb * stage_elems);
+        const int na = (kv + KE - 1) / KE;
+        const int matrix = MOE ? lists.seg_e[seg] : 0;
+        if (lane == 0)
+            ptx::mbar_arrive_expect_tx(full_bar(s), static_cast<uint32_t>(na * p.width * 128) +
+                                                        (W4 ? static_cast<uint32_t>(p.width * p.ring.atoms * p.atom_groups * 2) * (p.has_zeros ? 2u : 1u) : 0u));
         __syncwarp();
-        ptx::griddep_wait();
-        ptx::griddep_launch_dependents();
-        for (int i = 0; i < i1 - i0; ++i) {
-            const int s = i % NS;
-            if (i >= pre || !MOE) {
-                if (i >= NS && !wait_phase_warp(empty_bar(s), ((i / NS) & 1) ^ 1u, p.status, kSiteStreamEmpty, p.timeout_ns)) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) {
-                    arm(i0 + i, s);
-                    issue_w(i0 + i, s);
-                }
-                __syncwarp();
+        if (lane < na)
+            ptx::tma_load_2d_hint(base + static_cast<uint32_t>(s * p.ring.w_bytes + lane * p.ring.atom_bytes), &tmW, full_bar(s),
+                                  (kb * p.ring.atoms + lane) * (W4 ? 128 : 64), matrix * p.N + row0, pol_w);
+        if constexpr (W4) {
+            const uint32_t side = base + static_cast<uint32_t>(p.ring.side_off + s * p.ring.side_bytes);
+            const int y = matrix * p.groups_k + kb * p.ring.atoms * p.atom_groups;
+            if (lane == 8) ptx::tma_load_2d(side, &tmS, full_bar(s), row0, y);
+            if (lane == 9 && p.has_zeros) ptx::tma_load_2d(side + static_cast<uint32_t>(p.ring.side_bytes / 2), &tmZ, full_bar(s), row0, y);
+        }
+    };
+    // ... and the columns
+    const int row_shift = 31 - __clz(stage_elems / 8);   // 16-byte pieces of a column in a whole stage
+    auto issue_x = [&](int seg, int kb, int s) {
+        const int kv = min(stage_elems, p.K - kb * stage_elems);
+        const int first = MOE ? lists.seg_begin[seg] : 0;
+        const int n = MOE ? 2 * (lists.seg_begin[seg + 1] - first) : p.cols;
+        const uint32_t dst = base + static_cast<uint32_t>(p.ring.x_off + s * p.ring.x_bytes);
+        const T* X = static_cast<const T*>(p.X) + static_cast<int64_t>(kb) * stage_elems;
+        for (int i = lane; i < (n << row_shift); i += 32) {
+            const int c = i >> row_shift, o = (i - (c << row_shift)) * 8;
+            if (o < kv) {
+                const int64_t row = MOE ? 2 * static_cast<int64_t>(lists.slot[first + (c >> 1)]) + (c & 1) : c;
+                ptx::cp_async16(dst + static_cast<uint32_t>(c * pitch + o * 2), X + row * p.K + o);
             }
-            issue_x(i0 + i, s);
         }
-        if (!ok) {   // leave no copy in flight behind
-            for (int s = 0; s < NS; ++s)
-                for (uint32_t ph = 0; ph < 2; ++ph) wait_phase(full_bar(s), ph, p.status, kSiteStreamDrain, 1000000);
+        ptx::cp_async_arrive(full_bar(s));
+    };
+    // The group's stages, kg, kg + KW, ... of the CTA's list.
+    struct Place {
+        int left, seg, kb;
+    };
+    auto start = [&]() {
+        const int i = i0 + kg;
+        const int seg = MOE ? i / p.k_stages : 0;
+        return Place{mine_n - kg, seg, i - seg * p.k_stages};
+    };
+    auto advance = [&](Place& at) {
+        at.left -= KW;
+        at.kb += KW;
+        if constexpr (MOE) {
+            while (at.kb >= p.k_stages) {
+                at.kb -= p.k_stages;
+                ++at.seg;
+            }
         }
-    } else {
-        // ------------------------------------------------------------ consumers
-        ptx::griddep_wait();
-        const int mg = warp % p.mw, kg = warp / p.mw;
-        const int tiles = (rows + 15) >> 4;
+    };
+
+    // Before the wait for the kernel before this one: with experts the first
+    // slots' weights (they were complete before that kernel began); in the plain
+    // product only a prefetch into L2, which cannot expose stale data.
+    if (mg == 0) {
+        Place at = start();
+        for (int d = 0; d < own.depth && at.left > 0; ++d, advance(at)) {
+            if constexpr (MOE) {
+                issue_w(at.seg, at.kb, own.first + d);
+            } else {
+                if (lane < p.ring.atoms && (at.kb * p.ring.atoms + lane) * KE < p.K)
+                    ptx::tma_prefetch_2d(&tmW, (at.kb * p.ring.atoms + lane) * (W4 ? 128 : 64), row0);
+            }
+        }
+    }
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    Place ahead = start();   // the next stage to fetch (first warp of a group)
+    if (mg == 0) {
+        for (int d = 0; d < own.depth && ahead.left > 0; ++d, advance(ahead)) {
+            if constexpr (!MOE) issue_w(ahead.seg, ahead.kb, own.first + d);
+            issue_x(ahead.seg, ahead.kb, own.first + d);
+        }
+    }
+
+    {
         const int g = lane >> 2, t = lane & 3;
+        const int tile0 = mg * StreamWarp<T, W4, NT>::MT;               // this warp's tiles
+        const int tiles = max(0, ((rows + 15) >> 4) - tile0);
         float* mine = table + kg * table_size;
         StreamWarp<T, W4, NT> sw;
         sw.clear();
@@ -184,12 +192,11 @@ weight_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         auto flush = [&]() {
 #pragma unroll
             for (int jt = 0; jt < sw.MT; ++jt) {
-                const int tile = mg + jt * p.mw;
-                if (tile < tiles) {
-                    float* to = mine + tile * 16 + g;
+                if (jt < tiles) {
+                    float* to = mine + (tile0 + jt) * 16 + g;
 #pragma unroll
                     for (int q = 0; q < NT; ++q) {
-                        if (q < nt) {
+                        if (q == 0 || q < nt) {
                             if constexpr (MOE) {
                                 // columns 2t and 2t + 1 are the two parts of one slot's h
                                 const int c = q * 4 + t;
@@ -201,10 +208,10 @@ weight_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                                 }
                             } else {
                                 float* at = to + (q * 8 + 2 * t) * p.table_pitch;
-                                at[0] += sw.acc[jt][q][0];
-                                at[p.table_pitch] += sw.acc[jt][q][1];
-                                at[8] += sw.acc[jt][q][2];
-                                at[p.table_pitch + 8] += sw.acc[jt][q][3];
+                                at[0] = sw.acc[jt][q][0];
+                                at[p.table_pitch] = sw.acc[jt][q][1];
+                                at[8] = sw.acc[jt][q][2];
+                                at[p.table_pitch + 8] = sw.acc[jt][q][3];
                             }
                         }
                     }
@@ -213,36 +220,62 @@ weight_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
             sw.clear();
             __syncwarp();
         };
-        for (int i = kg; i < i1 - i0; i += KW) {
-            const int s = i % NS;
-            const int sg = MOE ? (i0 + i) / p.k_stages : 0;
-            const int kb = i0 + i - sg * p.k_stages;
-            if (sg != seg) {
+        int d = 0;
+        uint32_t phase = 0;
+        for (Place now = start(); now.left > 0; advance(now)) {
+            const int s = own.first + d;
+            if (now.seg != seg) {
                 if (seg >= 0) flush();
-                seg = sg;
-                first = MOE ? lists.seg_begin[sg] : 0;
-                n = MOE ? lists.seg_begin[sg + 1] - first : p.cols;
+                seg = now.seg;
+                first = MOE ? lists.seg_begin[seg] : 0;
+                n = MOE ? lists.seg_begin[seg + 1] - first : p.cols;
                 nt = MOE ? (n + 3) >> 2 : (n + 7) >> 3;
             }
-            if (!wait_phase_warp(full_bar(s), (i / NS) & 1, p.status, kSiteStreamFull, p.timeout_ns)) {
+            if (!wait_phase_warp(full_bar(s), phase, p.status, kSiteStreamFull, p.timeout_ns)) {
                 ok = false;
                 break;
             }
-            const int kv = min(kStageElems<W4>, p.K - kb * kStageElems<W4>);
-            const uint32_t w = base + static_cast<uint32_t>(s * p.ring.w_bytes);
-            const uint32_t x = base + static_cast<uint32_t>(p.ring.x_off + s * p.ring.x_bytes);
-            if constexpr (W4) {
-                const uint32_t sc = base + static_cast<uint32_t>(p.ring.side_off + s * p.ring.side_bytes);
-                const uint32_t zr = sc + static_cast<uint32_t>(p.ring.side_bytes / 2);
-                const SideView side{{sc, sc + 16u}, {zr, zr + 16u}, p.width, 16};
-                sw.stage4(w, x, side, p.has_zeros != 0, kv, p.chunks_per_group, tiles, mg, p.mw, nt, lane);
-            } else {
-                sw.stage16(w, x, kv, tiles, mg, p.mw, nt, lane);
+            const uint32_t there = base + ptx::stage_token();
+            const int kv = min(stage_elems, p.K - now.kb * stage_elems);
+            for (int a = 0; a * KE < kv; ++a) {
+                const uint32_t w = there + static_cast<uint32_t>(s * p.ring.w_bytes + a * p.ring.atom_bytes + tile0 * 2048);
+                const uint32_t x = there + static_cast<uint32_t>(p.ring.x_off + s * p.ring.x_bytes + a * KE * 2);
+                const int k = min(KE, kv - a * KE);
+                if constexpr (W4) {
+                    const uint32_t sc = there + static_cast<uint32_t>(p.ring.side_off + s * p.ring.side_bytes + (a * p.atom_groups * p.width + tile0 * 16) * 2);
+                    const SideView side{sc, sc + static_cast<uint32_t>(p.ring.side_bytes / 2), 16u, static_cast<uint32_t>(p.width * 2)};
+                    sw.template atom4<CPG, 2048, 32>(w, 1024u, x, pitch, side, p.has_zeros != 0, k, tiles, nt, lane);
+                } else {
+                    sw.template atom16<2048>(w, 1024u, x, pitch, k, tiles, nt, lane);
+                }
             }
+            sw.hold();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(empty_bar(s));
+            if (now.left > own.depth * KW) {   // another stage takes this slot
+                if (p.mw > 1) {
+                    if (lane == 0) ptx::mbar_arrive(empty_bar(s));
+                    if (mg == 0 && !wait_phase_warp(empty_bar(s), phase, p.status, kSiteStreamEmpty, p.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                }
+                if (mg == 0) {
+                    issue_w(ahead.seg, ahead.kb, s);
+                    issue_x(ahead.seg, ahead.kb, s);
+                    advance(ahead);
+                }
+            }
+            if (++d == own.depth) {
+                d = 0;
+                phase ^= 1u;
+            }
         }
         if (seg >= 0 && ok) flush();
+        if (!ok && mg == 0) {   // leave no copy in flight behind
+            for (int q = 0; q < own.depth; ++q)
+                for (uint32_t ph = 0; ph < 2; ++ph)
+                    wait_phase(full_bar(own.first + q), ph, p.status, kSiteStreamDrain, 1000000);
+        }
     }
 
     // ------------------------------------------------ the tables into the output
@@ -259,11 +292,13 @@ weight_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         }
         D[(MOE ? col : p.row0 + col) * static_cast<int64_t>(p.N) + n] = Elem<T>::from_float(v);
     };
+    const int used = MOE ? KW : min(KW, mine_n);   // groups that had a stage
     auto own_sum = [&](int e) {
+        if (used == 0) return 0.0f;
         const int col = e / p.width, row = e - col * p.width;
         const float* at = table + col * p.table_pitch + row;
         float v = at[0];
-        for (int q = 1; q < KW; ++q) v += at[q * table_size];
+        for (int q = 1; q < used; ++q) v += at[q * table_size];
         return v;
     };
     if (P == 1) {
@@ -298,21 +333,23 @@ struct RowsShape {
 
 inline int up_to(int a, int b) { return (a + b - 1) / b * b; }
 
-// The ring for `rows` rows and `cols` columns a stage, as deep as `budget`
-// bytes allow in multiples of `kw` stages (at least kw).
-inline RingLayout ring_layout(bool w4, int rows, int side_rows, int stage_groups, int cols, int budget, int kw) {
+// A ring for kw groups with `rows` rows and `cols` columns a stage, with as many
+// slots as `budget` bytes allow (at least one a group; the caller checks `end`).
+inline RingLayout ring_layout(bool w4, int atoms, int rows, int side_rows, int atom_groups, int cols, int budget, int kw) {
     RingLayout r;
-    r.w_bytes = up_to(rows, 16) * 128;
-    r.side_bytes = w4 ? 2 * up_to(side_rows * stage_groups * 2, 128) : 0;
-    const int pitch = w4 ? kColPitch<true> : kColPitch<false>;
+    r.atoms = atoms;
+    r.atom_bytes = up_to(rows, 16) * 128;
+    r.w_bytes = atoms * r.atom_bytes;
+    r.side_bytes = w4 ? 2 * up_to(side_rows * atom_groups * atoms * 2, 128) : 0;
+    const int pitch = col_pitch(w4, atoms);
     r.x_bytes = up_to(cols * pitch, 128);
     const int one = r.w_bytes + r.side_bytes + r.x_bytes;
-    // columns are read 8 at a time: the last stage's end in room of their own
+    // columns are read 8 at a time: the last slot's end in room of their own
     const int pad = up_to(cols, 8) * pitch - cols * pitch;
-    r.stages = std::max(kw, std::min(std::max(budget - pad, 0) / one, kMaxRing) / kw * kw);
-    r.side_off = r.stages * r.w_bytes;
-    r.x_off = r.side_off + r.stages * r.side_bytes;
-    r.end = up_to(r.x_off + r.stages * r.x_bytes + pad, 128);
+    r.slots = std::max(kw, std::min(std::max(budget - pad, 0) / one, kMaxRing));
+    r.side_off = r.slots * r.w_bytes;
+    r.x_off = r.side_off + r.slots * r.side_bytes;
+    r.end = up_to(r.x_off + r.slots * r.x_bytes + pad, 128);
     return r;
 }
 

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <algorithm>
+#include <cmath>
 #include <map>
 #include <mutex>
 
@@ -12,14 +13,16 @@ namespace gemm_gb300 {
 
 constexpr uint64_t kStreamTimeoutNs = 4000000000ull;
 constexpr int kMaxDynamicSmem = 226 * 1024;   // 227 KB less the barriers
+// dynamic shared memory of a launch, so that kCtasPerSm CTAs fit (1 KB of an SM's goes to each)
+template <int NT>
+constexpr int kSmemBudget = kCtasPerSm<NT> == 2 ? kSmemPerSm / 2 - 2048 : 200 * 1024;
 
 struct SideGroups {
-    int groups_k = 0, stage_groups = 0, chunks_per_group = 0;
+    int groups_k = 0, atom_groups = 0;
     SideGroups(const Weights& w, int64_t K) {
         if (w.scales == nullptr) return;
         groups_k = static_cast<int>(K / w.group);
-        stage_groups = 256 / w.group;
-        chunks_per_group = w.group / 32;
+        atom_groups = 256 / w.group;
     }
 };
 
@@ -29,21 +32,27 @@ inline int32_t stream_weights(bool w4, int64_t rows, int64_t K) { return (w4 ? r
 
 // Tensor maps of a stack: rows x K codes or 16-bit numbers in boxes of
 // box_rows x 128 bytes; scales and zero points [side_rows][N] in boxes of
-// stage_groups x side_box.
+// side_groups x side_box.
 inline bool encode_weights(const Weights& w, int64_t rows, int64_t side_rows, int64_t N, int64_t K, int box_rows,
-                           int side_box, int stage_groups, CUtensorMap* tw, CUtensorMap* ts, CUtensorMap* tz) {
+                           int side_box, int side_groups, CUtensorMap* tw, CUtensorMap* ts, CUtensorMap* tz) {
     if (w.scales == nullptr) {
         if (!encode_map(tw, w.data, 2, K, rows, 64, static_cast<uint32_t>(box_rows), true)) return false;
         *ts = *tz = *tw;   // not used
         return true;
     }
     if (!encode_map(tw, w.data, 1, K / 2, rows, 128, static_cast<uint32_t>(box_rows), true)) return false;
-    if (!encode_map(ts, w.scales, 2, N, side_rows, static_cast<uint32_t>(side_box), static_cast<uint32_t>(stage_groups), false)) return false;
+    if (!encode_map(ts, w.scales, 2, N, side_rows, static_cast<uint32_t>(side_box), static_cast<uint32_t>(side_groups), false)) return false;
     if (w.zeros == nullptr) {
         *tz = *ts;
         return true;
     }
-    return encode_map(tz, w.zeros, 2, N, side_rows, static_cast<uint32_t>(side_box), static_cast<uint32_t>(stage_groups), false);
+    return encode_map(tz, w.zeros, 2, N, side_rows, static_cast<uint32_t>(side_box), static_cast<uint32_t>(side_groups), false);
+}
+
+// The same rows in boxes of another height.
+inline bool encode_weights_box(const Weights& w, int64_t rows, int64_t K, int box_rows, CUtensorMap* t) {
+    return w.scales == nullptr ? encode_map(t, w.data, 2, K, rows, 64, static_cast<uint32_t>(box_rows), true)
+                               : encode_map(t, w.data, 1, K / 2, rows, 128, static_cast<uint32_t>(box_rows), true);
 }
 
 // Lifts a kernel's shared-memory limit, once per kernel and device.
@@ -90,52 +99,67 @@ gemm_status_t launch_stream(Kernel kernel, int dev, int grid, int cluster, int s
     return GEMM_OK;
 }
 
-// Fills the split and the shared-memory layout of `p` (N, K, k_stages set):
-// `tokens` outputs per row, `cols` columns per stage.  Returns the dynamic
-// shared memory of the launch, 0 when nothing fits.
-template <class T, bool W4, int NT, bool MOE>
-int plan_rows(RowsParams* p, int tokens, int cols, int stage_groups, int lists, int budget, const DeviceView& dev) {
-    constexpr int MT = kTilesPerWarp<NT>;
+// Fills the split and the shared-memory layout of `p` (N and K set): `tokens`
+// outputs per row, at most `cols` columns per stage, mostly typical_cols.  Returns the dynamic shared memory
+// of the launch, 0 when nothing fits.
+template <bool W4, int NT, bool MOE>
+int plan_rows(RowsParams* p, int tokens, int cols, int typical_cols, int atom_groups, int lists, const DeviceView& dev) {
+    constexpr int budget = kSmemBudget<NT>;
+    constexpr int MT = kTilesPerWarp<W4, NT>;
     const int table_cols = MOE ? tokens : 8 * NT;
+    const int k_atoms = (p->K + kAtomElems<W4> - 1) / kAtomElems<W4>;
+    const int nt = std::min(NT, (typical_cols + 7) / 8);
     int best = 0;
     double best_t = 0.0;
     RowsParams got = *p;
     for (int P = 1; P <= 8; P *= 2) {
-        const int clusters = dev.sms / P;
+        const int clusters = kCtasPerSm<NT> * dev.sms / P;
         // as few rounds of clusters as keep a range within a TMA box (256 rows)
         // and the consumers' registers
         const int most = std::min(256, kConsumers * MT * 16);
         const int rounds = (p->N + clusters * most - 1) / (clusters * most);
         const int width = up_to((p->N + clusters * rounds - 1) / (clusters * rounds), 8);
         const int tiles = (width + 15) / 16;
-        // As few warps per stage as the registers allow, more where the tables
-        // or a ring of KW stages would leave too little in flight.
         for (int mw = 1; mw <= kConsumers; mw *= 2) {
             if (mw * MT < tiles) continue;
             const int kw = kConsumers / mw;
-            RowsParams c = *p;
-            c.width = width;
-            c.ranges = (p->N + width - 1) / width;
-            c.pieces = P;
-            c.mw = mw;
-            c.table_pitch = up_to(tiles * 16, 32) + 8;
-            const int tables = kw * table_cols * c.table_pitch * 4;
-            const int recv = P > 1 ? up_to((tokens * width + P - 1) / P * P * 4, 128) : 0;
-            const int fixed = lists + tables + recv + 1024;
-            c.ring = ring_layout(W4, width, width, stage_groups, cols, budget - fixed, kw);
-            if (c.ring.end + fixed > kMaxDynamicSmem || c.ring.stages < 2) continue;
-            // bytes a CTA streams, slowed by a shallow ring, and the exchange
-            const double stages = static_cast<double>((p->k_stages + P - 1) / P);
-            const double flight = std::min(1.0, c.ring.stages * width * 128 / 65536.0);
-            const double t = rounds * stages * (width + (W4 ? 4 : 1) * cols * 0.5) * 128 / 45000.0 / flight +
-                             (P > 1 ? 1.0 : 0.0);
-            if (best == 0 || t < best_t) {
-                best_t = t;
-                c.list_off = c.ring.end;
-                c.table_off = c.list_off + lists;
-                c.recv_off = c.table_off + tables;
-                best = c.recv_off + recv + 1024;
-                got = c;
+            for (int atoms = 1; atoms <= kMaxAtoms; atoms *= 2) {
+                if (atoms > 1 && atoms * width * 128 > 16384) break;
+                RowsParams c = *p;
+                c.width = width;
+                c.ranges = (p->N + width - 1) / width;
+                c.pieces = P;
+                c.mw = mw;
+                c.k_stages = (k_atoms + atoms - 1) / atoms;
+                c.table_pitch = up_to(tiles * 16, 32) + 8;
+                const int tables = kw * table_cols * c.table_pitch * 4;
+                const int recv = P > 1 ? up_to((tokens * width + P - 1) / P * P * 4, 128) : 0;
+                const int fixed = lists + tables + recv + 1024;
+                c.ring = ring_layout(W4, atoms, width, width, atom_groups, cols, budget - fixed, kw);
+                if (c.ring.end + fixed > (best == 0 ? kMaxDynamicSmem : budget)) continue;
+                // Clocks per atom.  Arithmetic: a warp's instructions for its
+                // columns and tiles, about one per clock and SM.  Copies: the
+                // CTA's share of HBM for the weights and of L2 for the columns,
+                // slowed when less is in flight than their latency needs.
+                // Latency: what a group takes for a stage however small, with
+                // kw groups side by side; warps that share a stage wait for one
+                // another.
+                const int per_warp = (tiles + mw - 1) / mw;
+                const double work = W4 ? 8.0 * (10.0 * nt + per_warp * (22.0 + 6.0 * nt)) : 4.0 * (6.0 * nt + per_warp * (5.0 + 3.0 * nt));
+                const double arith = kCtasPerSm<NT> * (work + 200.0 / atoms) * mw / 2.0;
+                const double flight = std::min(1.0, c.ring.slots * atoms * width * 128 / (65536.0 / kCtasPerSm<NT>));
+                const double copies = kCtasPerSm<NT> * (width * 128 / 23.5 + typical_cols * (W4 ? 512 : 128) / 50.0) / flight;
+                const double latency = (1500.0 + 1500.0 * (mw - 1)) / (kw * atoms) + 2.0 * work / kw;
+                const double n_atoms = std::ceil(std::ceil(static_cast<double>(c.k_stages) / P) / kw) * kw * atoms;
+                const double t = rounds * n_atoms * std::max(std::max(arith, copies), latency) + (P > 1 ? 800.0 : 0.0) + tables / 100.0;
+                if (best == 0 || t < best_t) {
+                    best_t = t;
+                    c.list_off = c.ring.end;
+                    c.table_off = c.list_off + lists;
+                    c.recv_off = c.table_off + tables;
+                    best = c.recv_off + recv + 1024;
+                    got = c;
+                }
             }
         }
     }

@@ -7,21 +7,17 @@
 namespace gemm_gb300 {
 namespace {
 
-constexpr int kW4Smem = 200 * 1024;
-
-template <class T, int NT>
+template <class T, int CPG, int NT>
 gemm_status_t launch(const void* A, const Weights& w, void* D, int64_t row0, int M, int64_t N, int64_t K,
                      const EpiParams& epi, const DeviceView& dev, cudaStream_t s) {
     RowsParams p{};
     const SideGroups sg(w, K);
     p.N = static_cast<int32_t>(N);
     p.K = static_cast<int32_t>(K);
-    p.k_stages = static_cast<int32_t>((K + 255) / 256);
-    const int smem = plan_rows<T, true, NT, false>(&p, M, M, sg.stage_groups, 0, kW4Smem, dev);
+    const int smem = plan_rows<true, NT, false>(&p, M, M, M, sg.atom_groups, 0, dev);
     if (smem <= 0) return GEMM_ERR_CUDA;
     p.groups_k = sg.groups_k;
-    p.stage_groups = sg.stage_groups;
-    p.chunks_per_group = sg.chunks_per_group;
+    p.atom_groups = sg.atom_groups;
     p.has_zeros = w.zeros != nullptr;
     p.stream_w = stream_weights(true, N, K);
     p.cols = M;
@@ -32,22 +28,30 @@ gemm_status_t launch(const void* A, const Weights& w, void* D, int64_t row0, int
     p.status = dev.status;
     p.timeout_ns = kStreamTimeoutNs;
     CUtensorMap tw, ts, tz;
-    if (!encode_weights(w, N, sg.groups_k, N, K, p.width, p.width, sg.stage_groups, &tw, &ts, &tz)) return GEMM_ERR_INVALID_VALUE;
-    return launch_stream(weight_rows_kernel<T, true, NT, false>, dev.dev, p.ranges * p.pieces, p.pieces, smem, s, tw, ts, tz, p);
+    if (!encode_weights(w, N, sg.groups_k, N, K, p.width, p.width, p.ring.atoms * sg.atom_groups, &tw, &ts, &tz)) return GEMM_ERR_INVALID_VALUE;
+    return launch_stream(weight_rows_kernel<T, CPG, NT, false>, dev.dev, p.ranges * p.pieces, p.pieces, smem, s, tw, ts, tz, p);
 }
 
-template <class T>
+template <class T, int CPG>
 gemm_status_t run(const void* A, const Weights& w, void* D, int64_t M, int64_t N, int64_t K, const EpiParams& epi,
                   const DeviceView& dev, cudaStream_t s) {
     for (int64_t m0 = 0; m0 < M; m0 += 32) {
         const int m = static_cast<int>(std::min<int64_t>(32, M - m0));
         gemm_status_t st;
-        if (m <= 8) st = launch<T, 1>(A, w, D, m0, m, N, K, epi, dev, s);
-        else if (m <= 16) st = launch<T, 2>(A, w, D, m0, m, N, K, epi, dev, s);
-        else st = launch<T, 4>(A, w, D, m0, m, N, K, epi, dev, s);
+        if (m <= 8) st = launch<T, CPG, 1>(A, w, D, m0, m, N, K, epi, dev, s);
+        else if (m <= 16) st = launch<T, CPG, 2>(A, w, D, m0, m, N, K, epi, dev, s);
+        else st = launch<T, CPG, 4>(A, w, D, m0, m, N, K, epi, dev, s);
         if (st != GEMM_OK) return st;
     }
     return GEMM_OK;
+}
+
+template <class T>
+gemm_status_t by_group(const void* A, const Weights& w, void* D, int64_t M, int64_t N, int64_t K, const EpiParams& epi,
+                       const DeviceView& dev, cudaStream_t s) {
+    if (w.group == 32) return run<T, 1>(A, w, D, M, N, K, epi, dev, s);
+    if (w.group == 64) return run<T, 2>(A, w, D, M, N, K, epi, dev, s);
+    return run<T, 4>(A, w, D, M, N, K, epi, dev, s);
 }
 
 }  // namespace
@@ -55,7 +59,7 @@ gemm_status_t run(const void* A, const Weights& w, void* D, int64_t M, int64_t N
 gemm_status_t run_w4_gemm(bool bf16, const void* A, const Weights& w, void* D, int64_t M, int64_t N, int64_t K,
                           const EpiParams& epi, const DeviceView& dev, gemm_stream_t stream) {
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return bf16 ? run<__nv_bfloat16>(A, w, D, M, N, K, epi, dev, s) : run<__half>(A, w, D, M, N, K, epi, dev, s);
+    return bf16 ? by_group<__nv_bfloat16>(A, w, D, M, N, K, epi, dev, s) : by_group<__half>(A, w, D, M, N, K, epi, dev, s);
 }
 
 }  // namespace gemm_gb300
