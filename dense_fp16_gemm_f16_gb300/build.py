@@ -24,7 +24,8 @@ LIB_NAME = "libgemm_f16.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 
 SOURCES = ["api.cu", "tiled_2cta.cu", "tiled_2cta512.cu", "tiled_1cta.cu", "skinny.cu", "streamk.cu",
-           "llm/llm_api.cu", "llm/w4_codes.cu", "llm/w4_gemm.cu", "llm/moe_route.cu", "llm/moe_ffn.cu"]
+           "llm/llm_api.cu", "llm/w4_codes.cu", "llm/w4_gemm.cu", "llm/w4_tiles.cu",
+           "llm/moe_route.cu", "llm/moe_ffn.cu"]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH_FLAGS + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
                            "-I", INCLUDE, "-I", CSRC]

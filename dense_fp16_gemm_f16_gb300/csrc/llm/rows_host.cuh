@@ -68,16 +68,16 @@ inline cudaError_t allow_smem(const void* kernel, int dev) {
 }
 
 // Programmatic stream serialisation, and clusters of `cluster` CTAs.
-template <class Kernel, class Params>
-gemm_status_t launch_stream(Kernel kernel, int dev, int grid, int cluster, int smem, cudaStream_t s, const CUtensorMap& w,
-                            const CUtensorMap& sc, const CUtensorMap& zr, const Params& p) {
+template <class Kernel, class... Args>
+gemm_status_t launch_clusters(Kernel kernel, int dev, int grid, int threads, int cluster, int smem, cudaStream_t s,
+                              const Args&... args) {
     if (allow_smem(reinterpret_cast<const void*>(kernel), dev) != cudaSuccess) {
         cudaGetLastError();
         return GEMM_ERR_CUDA;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-    cfg.blockDim = dim3(kStreamThreads, 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -92,11 +92,17 @@ gemm_status_t launch_stream(Kernel kernel, int dev, int grid, int cluster, int s
         cfg.numAttrs = 2;
     }
     cfg.attrs = attr;
-    if (cudaLaunchKernelEx(&cfg, kernel, w, sc, zr, p) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
         cudaGetLastError();
         return GEMM_ERR_LAUNCH;
     }
     return GEMM_OK;
+}
+
+template <class Kernel, class Params>
+gemm_status_t launch_stream(Kernel kernel, int dev, int grid, int cluster, int smem, cudaStream_t s, const CUtensorMap& w,
+                            const CUtensorMap& sc, const CUtensorMap& zr, const Params& p) {
+    return launch_clusters(kernel, dev, grid, kStreamThreads, cluster, smem, s, w, sc, zr, p);
 }
 
 // Fills the split and the shared-memory layout of `p` (N and K set): `tokens`

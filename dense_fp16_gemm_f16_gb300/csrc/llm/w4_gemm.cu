@@ -54,11 +54,18 @@ gemm_status_t by_group(const void* A, const Weights& w, void* D, int64_t M, int6
     return run<T, 4>(A, w, D, M, N, K, epi, dev, s);
 }
 
+// Clocks of the streaming kernel for 17 to 64 rows of A, in passes of up to 32.
+double rows_clocks(int64_t M, int64_t N, int64_t K) {
+    return static_cast<double>((M + 31) / 32) * (9000.0 + static_cast<double>(N) * static_cast<double>(K) / 1100.0);
+}
+
 }  // namespace
 
 gemm_status_t run_w4_gemm(bool bf16, const void* A, const Weights& w, void* D, int64_t M, int64_t N, int64_t K,
                           const EpiParams& epi, const DeviceView& dev, gemm_stream_t stream) {
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (M > 64 || (M > 16 && w4_tiles_clocks(M, N, K, dev.sms) < rows_clocks(M, N, K)))
+        return run_w4_tiles(bf16, A, w, D, M, N, K, epi, dev, s);
     return bf16 ? by_group<__nv_bfloat16>(A, w, D, M, N, K, epi, dev, s) : by_group<__half>(A, w, D, M, N, K, epi, dev, s);
 }
 
