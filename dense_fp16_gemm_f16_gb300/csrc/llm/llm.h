@@ -51,7 +51,7 @@ cudaError_t launch_w4_dequantize(bool bf16, const Weights& w, int64_t batch, int
                                  cudaStream_t s);
 
 // The product on tcgen05, for more than a few rows of A, and its estimated clocks.
-double w4_tiles_clocks(int64_t M, int64_t N, int64_t K, int sms);
+double w4_tiles_clocks(int64_t M, int64_t N, int64_t K, const DeviceView& dev);
 gemm_status_t run_w4_tiles(bool bf16, const void* A, const Weights& w, void* D, int64_t M, int64_t N, int64_t K,
                            const EpiParams& epi, const DeviceView& dev, cudaStream_t s);
 

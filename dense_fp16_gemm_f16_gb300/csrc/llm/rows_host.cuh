@@ -6,6 +6,7 @@
 #include <cmath>
 #include <map>
 #include <mutex>
+#include <tuple>
 
 #include "llm/rows.cuh"
 
@@ -67,6 +68,36 @@ inline cudaError_t allow_smem(const void* kernel, int dev) {
     return e;
 }
 
+// Clusters of `cluster` CTAs that run at one time (0: none), looked up once.
+inline int active_clusters(const void* kernel, const DeviceView& dev, int threads, int smem, int cluster) {
+    static std::mutex mu;
+    static std::map<std::tuple<const void*, int, int, int>, int> known;
+    std::lock_guard<std::mutex> lock(mu);
+    const auto key = std::make_tuple(kernel, dev.dev, smem, cluster);
+    const auto it = known.find(key);
+    if (it != known.end()) return it->second;
+    int n = 0;
+    if (allow_smem(kernel, dev.dev) == cudaSuccess) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(cluster), 1, 1);
+        cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+        cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            n = 0;
+        }
+    }
+    known[key] = n;
+    return n;
+}
+
 // Programmatic stream serialisation, and clusters of `cluster` CTAs.
 template <class Kernel, class... Args>
 gemm_status_t launch_clusters(Kernel kernel, int dev, int grid, int threads, int cluster, int smem, cudaStream_t s,
@@ -109,7 +140,8 @@ gemm_status_t launch_stream(Kernel kernel, int dev, int grid, int cluster, int s
 // outputs per row, at most `cols` columns per stage, mostly typical_cols.  Returns the dynamic shared memory
 // of the launch, 0 when nothing fits.
 template <bool W4, int NT, bool MOE>
-int plan_rows(RowsParams* p, int tokens, int cols, int typical_cols, int atom_groups, int lists, const DeviceView& dev) {
+int plan_rows(const void* kernel, RowsParams* p, int tokens, int cols, int typical_cols, int atom_groups, int lists,
+              const DeviceView& dev) {
     constexpr int budget = kSmemBudget<NT>;
     constexpr int MT = kTilesPerWarp<W4, NT>;
     const int table_cols = MOE ? tokens : 8 * NT;
@@ -119,7 +151,8 @@ int plan_rows(RowsParams* p, int tokens, int cols, int typical_cols, int atom_gr
     double best_t = 0.0;
     RowsParams got = *p;
     for (int P = 1; P <= 8; P *= 2) {
-        const int clusters = kCtasPerSm<NT> * dev.sms / P;
+        const int clusters = active_clusters(kernel, dev, kStreamThreads, budget, P);
+        if (clusters < 1) continue;
         // as few rounds of clusters as keep a range within a TMA box (256 rows)
         // and the consumers' registers
         const int most = std::min(256, kConsumers * MT * 16);

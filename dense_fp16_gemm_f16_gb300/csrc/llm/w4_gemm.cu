@@ -14,7 +14,7 @@ gemm_status_t launch(const void* A, const Weights& w, void* D, int64_t row0, int
     const SideGroups sg(w, K);
     p.N = static_cast<int32_t>(N);
     p.K = static_cast<int32_t>(K);
-    const int smem = plan_rows<true, NT, false>(&p, M, M, M, sg.atom_groups, 0, dev);
+    const int smem = plan_rows<true, NT, false>(reinterpret_cast<const void*>(weight_rows_kernel<T, CPG, NT, false>), &p, M, M, M, sg.atom_groups, 0, dev);
     if (smem <= 0) return GEMM_ERR_CUDA;
     p.groups_k = sg.groups_k;
     p.atom_groups = sg.atom_groups;
@@ -64,7 +64,7 @@ double rows_clocks(int64_t M, int64_t N, int64_t K) {
 gemm_status_t run_w4_gemm(bool bf16, const void* A, const Weights& w, void* D, int64_t M, int64_t N, int64_t K,
                           const EpiParams& epi, const DeviceView& dev, gemm_stream_t stream) {
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (M > 64 || (M > 16 && w4_tiles_clocks(M, N, K, dev.sms) < rows_clocks(M, N, K)))
+    if (M > 64 || (M > 16 && w4_tiles_clocks(M, N, K, dev) < rows_clocks(M, N, K)))
         return run_w4_tiles(bf16, A, w, D, M, N, K, epi, dev, s);
     return bf16 ? by_group<__nv_bfloat16>(A, w, D, M, N, K, epi, dev, s) : by_group<__half>(A, w, D, M, N, K, epi, dev, s);
 }

@@ -14,21 +14,25 @@ struct TileShape {
     double clocks;
 };
 
-// A K block of 64 takes the MMA 2 clocks per row of A (128 weight rows), and
-// decoding it about kDecodeClocks; a CTA's start and end, and an exchange
-// between split parts, are added.
-constexpr double kDecodeClocks = 230.0, kTileFixedClocks = 7000.0, kTileExchangeClocks = 2500.0;
+// Clocks of a K block of 64: what decoding and handing it over takes, or its
+// MMAs; then a CTA's start and end, and an exchange between split parts.
+constexpr double kDecodeClocks = 600.0, kMmaClocksPerRow = 3.0, kTileFixedClocks = 9000.0, kTileExchangeClocks = 3000.0;
 
-TileShape tile_shape(int64_t M, int64_t N, int64_t K, int sms) {
+int tile_code_slot(int rows_b, int atom_groups) { return rows_b * 128 + 2 * up_to(rows_b * atom_groups * 2, 128); }
+
+template <class T, bool PAIRS>
+TileShape tile_shape(int64_t M, int64_t N, int64_t K, const DeviceView& dev) {
     TileShape t{};
-    t.rows_b = M <= 64 ? 64 : 128;
+    t.rows_b = PAIRS ? 64 : 128;
     t.m_tiles = static_cast<int>((M + 255) / 256);
     t.rows_a = up_to(static_cast<int>((M + t.m_tiles - 1) / t.m_tiles), 16);
     t.n_tiles = static_cast<int>((N + t.rows_b - 1) / t.rows_b);
     const int64_t atoms = (K + 255) / 256, tiles = static_cast<int64_t>(t.m_tiles) * t.n_tiles;
-    const double block = std::max(2.0 * t.rows_a, kDecodeClocks);
+    const double block = std::max(kMmaClocksPerRow * t.rows_a, kDecodeClocks);
     for (int s = 1; s <= 8 && s <= atoms; s *= 2) {
-        const double rounds = static_cast<double>((tiles * s + sms - 1) / sms);
+        const int at_once = active_clusters(reinterpret_cast<const void*>(w4_tiles_kernel<T, PAIRS, 2>), dev, kTileThreads, kMaxDynamicSmem, s);
+        if (at_once < 1) continue;
+        const double rounds = static_cast<double>((tiles + at_once - 1) / at_once);
         const double c = rounds * (4.0 * static_cast<double>((atoms + s - 1) / s) * block + kTileFixedClocks) + (s > 1 ? kTileExchangeClocks : 0.0);
         if (t.split == 0 || c < t.clocks) {
             t.split = s;
@@ -38,7 +42,7 @@ TileShape tile_shape(int64_t M, int64_t N, int64_t K, int sms) {
     return t;
 }
 
-template <class T, bool PAIRS>
+template <class T, bool PAIRS, int KB>
 gemm_status_t launch(const void* A, const Weights& w, void* D, int64_t M, int64_t N, int64_t K, const EpiParams& epi,
                      const TileShape& t, const DeviceView& dev, cudaStream_t s) {
     const SideGroups sg(w, K);
@@ -56,10 +60,10 @@ gemm_status_t launch(const void* A, const Weights& w, void* D, int64_t M, int64_
     p.has_zeros = w.zeros != nullptr;
     p.stream_w = stream_weights(true, N, K);
     p.side_bytes = up_to(t.rows_b * sg.atom_groups * 2, 128);
-    p.stages = t.rows_a <= 128 ? kTileStages : kTileStages / 2;   // 32 KB of A each at 256 rows
-    p.codes_off = p.stages * t.rows_a * 128;
-    const int code_slot = t.rows_b * 128 + 2 * p.side_bytes;
-    p.codes = std::min(kTileCodes, (kMaxDynamicSmem - 1024 - p.codes_off) / code_slot);
+    p.codes_off = kTileStages * KB * t.rows_a * 128;
+    const int code_slot = tile_code_slot(t.rows_b, sg.atom_groups);
+    p.codes = std::min(kTileCodes, (kMaxDynamicSmem - 1024 - p.codes_off) / code_slot) / 2 * 2;
+    if (p.codes < 2) return GEMM_ERR_CUDA;
     p.side_off = p.codes_off + p.codes * t.rows_b * 128;
     p.end = p.side_off + p.codes * 2 * p.side_bytes;
     // the output's exchange lies over the operands
@@ -79,19 +83,23 @@ gemm_status_t launch(const void* A, const Weights& w, void* D, int64_t M, int64_
         return GEMM_ERR_INVALID_VALUE;
     const int64_t ctas = static_cast<int64_t>(t.m_tiles) * t.n_tiles * t.split;
     if (ctas > INT32_MAX) return GEMM_ERR_INVALID_VALUE;
-    return launch_clusters(w4_tiles_kernel<T, PAIRS>, dev.dev, static_cast<int>(ctas), kTileThreads, t.split, smem, s, tw, ts, tz, ta, p);
+    return launch_clusters(w4_tiles_kernel<T, PAIRS, KB>, dev.dev, static_cast<int>(ctas), kTileThreads, t.split, smem, s, tw, ts, tz, ta, p);
 }
 
 template <class T>
 gemm_status_t run(const void* A, const Weights& w, void* D, int64_t M, int64_t N, int64_t K, const EpiParams& epi,
                   const DeviceView& dev, cudaStream_t s) {
-    const TileShape t = tile_shape(M, N, K, dev.sms);
-    return M <= 64 ? launch<T, true>(A, w, D, M, N, K, epi, t, dev, s) : launch<T, false>(A, w, D, M, N, K, epi, t, dev, s);
+    const TileShape t = M <= 64 ? tile_shape<T, true>(M, N, K, dev) : tile_shape<T, false>(M, N, K, dev);
+    if (t.split == 0) return GEMM_ERR_CUDA;
+    if (M <= 64) return launch<T, true, 2>(A, w, D, M, N, K, epi, t, dev, s);
+    return t.rows_a <= 128 ? launch<T, false, 2>(A, w, D, M, N, K, epi, t, dev, s) : launch<T, false, 1>(A, w, D, M, N, K, epi, t, dev, s);
 }
 
 }  // namespace
 
-double w4_tiles_clocks(int64_t M, int64_t N, int64_t K, int sms) { return tile_shape(M, N, K, sms).clocks; }
+double w4_tiles_clocks(int64_t M, int64_t N, int64_t K, const DeviceView& dev) {
+    return M <= 64 ? tile_shape<__half, true>(M, N, K, dev).clocks : tile_shape<__half, false>(M, N, K, dev).clocks;
+}
 
 gemm_status_t run_w4_tiles(bool bf16, const void* A, const Weights& w, void* D, int64_t M, int64_t N, int64_t K,
                            const EpiParams& epi, const DeviceView& dev, cudaStream_t s) {

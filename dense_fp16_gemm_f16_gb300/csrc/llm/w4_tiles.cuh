@@ -7,10 +7,19 @@
 // operand needs (A rows, staged by TMA, K-major, 128-byte swizzle).  TMEM lane
 // = weight row, so a decoding thread owns one row: its codes are 32
 // contiguous bytes per K block of 64, its scale one number per group.
-//   warps 0-15  four warpgroups: group g decodes every fourth K block, in
-//               registers while the MMAs catch up, then into one of its two TMEM
-//               stages (tcgen05.st); later they read the accumulator out
-//   warp 16     TMA: codes and scales in atoms of 256 k, A in K blocks of 64
+// The K loop runs in steps of KB blocks of 64 k.  Waiting, fencing and committing
+// cost the issuing thread some 350 clocks a step, as much as the MMAs of a K block
+// with few rows of A, so up to 128 rows a step is two blocks (M = 48, 8192 x 8192:
+// 45 us against 48; with a commit per block for A and one per step for the weights
+// 58).  With more rows the MMAs take longer and shared memory holds four single
+// blocks (M = 512: 52 us; two double ones 60).
+//   warps 0-15  four warpgroups: group g decodes every fourth step, in registers
+//               while the MMAs catch up, then into TMEM (tcgen05.st); later they
+//               read the accumulator out
+//   warp 16     TMA: A
+//   warp 18     TMA: codes and scales in atoms of 256 k, as far ahead as their
+//               slots allow (behind the A loads of one producer they came too late:
+//               512 x 8192 x 8192 57 us)
 //   warp 17     issues tcgen05.mma (M = 128, N = A rows, K = 16)
 // A weight is s * (code - z): code - z and the product each one rounded step in
 // the activations' type (the first exact for whole and half zero points).
@@ -37,16 +46,21 @@ namespace gemm_gb300 {
 
 constexpr int kTileGroups = 4;          // decoding warpgroups
 constexpr int kDecodeWarps = 4 * kTileGroups;
-constexpr int kTileThreads = 32 * (kDecodeWarps + 2);
-constexpr int kTileStages = 8;          // K blocks in flight, at most: weights in TMEM, A in shared memory
+constexpr int kTileThreads = 32 * (kDecodeWarps + 3);
+// Steps in flight: weights in TMEM, A in shared memory, one stage per group.  Every
+// wait here is by parity, which tells a slot's uses apart only for a waiter that
+// has seen each of them complete, so a slot's uses always belong to the same
+// waiters; the code slots are even in number because with KB = 2 a group reads
+// every second atom.
+constexpr int kTileStages = kTileGroups;
 constexpr int kTileCodes = 8;           // code atoms in flight, at most
-constexpr int kTileTmemCols = 512;      // accumulator: columns 0-255; weight stage s: 32 columns at 256 + 32 s
+constexpr int kTileTmemCols = 512;      // accumulator: columns 0-255; weights of stage s: 32 KB columns at 256 + 32 KB s
 constexpr uint32_t kSiteTileA = 12, kSiteTileCodes = 13, kSiteTileMma = 14, kSiteTileDone = 15, kSiteTileEmpty = 16;
 
 struct TileParams {
     int32_t M, N, K;
     int32_t rows_a;          // rows of A per tile: MMA N, a multiple of 16, <= 256
-    int32_t stages, codes;   // K blocks and code atoms in flight
+    int32_t codes;           // code atoms in flight
     int32_t rows_b;          // weight rows per tile: 64 with PAIRS, else 128
     int32_t m_tiles, split;
     int32_t atoms;           // code atoms over K
@@ -145,7 +159,7 @@ struct Pair<__nv_bfloat16> {
     }
 };
 
-template <class T, bool PAIRS>
+template <class T, bool PAIRS, int KB>
 __global__ void __launch_bounds__(kTileThreads, 1)
 w4_tiles_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmS,
                 const __grid_constant__ CUtensorMap tmZ, const __grid_constant__ CUtensorMap tmA, const TileParams p) {
@@ -167,12 +181,12 @@ w4_tiles_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         ptx::prefetch_tensormap(&tmW);
         ptx::prefetch_tensormap(&tmA);
         for (int s = 0; s < kTileStages; ++s) {
-            ptx::mbar_init(full(s), 5);    // four warps of a group, and the byte count of A
+            ptx::mbar_init(full(s), 5);   // the group's warps, and the byte count of A
             ptx::mbar_init(empty(s), 1);
         }
         for (int c = 0; c < kTileCodes; ++c) {
             ptx::mbar_init(c_full(c), 1);
-            ptx::mbar_init(c_empty(c), kDecodeWarps);
+            ptx::mbar_init(c_empty(c), 16 / KB);   // an atom is 4 / KB steps of 4 warps each
         }
         ptx::mbar_init(done, 1);
         ptx::fence_mbar_init();
@@ -188,7 +202,8 @@ w4_tiles_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     const int n0 = static_cast<int>(tile / p.m_tiles) * p.rows_b;
     const int at0 = static_cast<int>(static_cast<int64_t>(j) * p.atoms / S);
     const int at1 = static_cast<int>(static_cast<int64_t>(j + 1) * p.atoms / S);
-    const int blocks = (min(at1 * 256, p.K) - at0 * 256 + 63) / 64;   // this CTA's K blocks
+    const int blocks = (min(at1 * 256, p.K) - at0 * 256 + 63) / 64;   // this CTA's K blocks, KB to a step
+    const int steps = (blocks + KB - 1) / KB;
     ptx::tc_fence_before();
     if (S > 1) ptx::cluster_sync(); else __syncthreads();
     ptx::tc_fence_after();
@@ -198,49 +213,58 @@ w4_tiles_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     const uint32_t a_bytes = static_cast<uint32_t>(p.rows_a) * 128u;
     bool ok = true;
 
-    const int NS = p.stages;
     if (warp == kDecodeWarps) {
         // ------------------------------------------------------------ producer (one thread)
         if (lane == 0) {
-            const uint64_t pol_w = p.stream_w ? ptx::policy_evict_first() : ptx::policy_evict_normal();
             const uint64_t pol_a = ptx::policy_evict_last();
-            const uint32_t code_tx = static_cast<uint32_t>(p.rows_b) * 128u +
-                                     static_cast<uint32_t>(p.rows_b * p.atom_groups * 2) * (p.has_zeros ? 2u : 1u);
-            int s = 0, c = 0;
-            uint32_t ph = 1, c_ph = 1;   // a slot's first use waits for nothing
-            for (int b = 0; b < blocks; ++b) {
-                if ((b & 3) == 0) {   // the next code atom
-                    if (!wait_phase(c_empty(c), c_ph, p.status, kSiteTileCodes, p.timeout_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    const int at = at0 + (b >> 2);
-                    const uint32_t side = base + static_cast<uint32_t>(p.side_off + c * 2 * p.side_bytes);
-                    ptx::mbar_arrive_expect_tx(c_full(c), code_tx);
-                    ptx::tma_load_2d_hint(base + static_cast<uint32_t>(p.codes_off + c * p.rows_b * 128), &tmW, c_full(c), at * 128, n0, pol_w);
-                    ptx::tma_load_2d(side, &tmS, c_full(c), n0, at * p.atom_groups);
-                    if (p.has_zeros) ptx::tma_load_2d(side + static_cast<uint32_t>(p.side_bytes), &tmZ, c_full(c), n0, at * p.atom_groups);
-                    if (++c == p.codes) {
-                        c = 0;
-                        c_ph ^= 1u;
-                    }
-                }
+            int s = 0;
+            uint32_t ph = 1;   // a slot's first use waits for nothing
+            for (int b = 0; b < blocks; b += KB) {
                 if (!wait_phase(empty(s), ph, p.status, kSiteTileEmpty, p.timeout_ns)) {
                     ok = false;
                     break;
                 }
-                ptx::mbar_arrive_expect_tx(full(s), a_bytes);
-                ptx::tma_load_2d_hint(base + s * a_bytes, &tmA, full(s), at0 * 256 + b * 64, m0, pol_a);
-                if (++s == NS) {
+                const int n = min(KB, blocks - b);
+                ptx::mbar_arrive_expect_tx(full(s), n * a_bytes);
+                for (int i = 0; i < n; ++i)
+                    ptx::tma_load_2d_hint(base + (KB * s + i) * a_bytes, &tmA, full(s), at0 * 256 + (b + i) * 64, m0, pol_a);
+                if (++s == kTileStages) {
                     s = 0;
                     ph ^= 1u;
                 }
             }
             if (!ok) {   // leave no copy in flight behind
-                for (uint32_t q = 0; q < 2; ++q) {
-                    for (int i = 0; i < NS; ++i) wait_phase(full(i), q, p.status, kSiteStreamDrain, 1000000);
-                    for (int i = 0; i < p.codes; ++i) wait_phase(c_full(i), q, p.status, kSiteStreamDrain, 1000000);
+                for (uint32_t q = 0; q < 2; ++q)
+                    for (int i = 0; i < kTileStages; ++i) wait_phase(full(i), q, p.status, kSiteStreamDrain, 1000000);
+            }
+        }
+        __syncwarp();
+    } else if (warp == kDecodeWarps + 2) {
+        // ------------------------------------------------------------ codes and scales (one thread)
+        if (lane == 0) {
+            const uint64_t pol_w = p.stream_w ? ptx::policy_evict_first() : ptx::policy_evict_normal();
+            const uint32_t tx = static_cast<uint32_t>(p.rows_b) * 128u +
+                                static_cast<uint32_t>(p.rows_b * p.atom_groups * 2) * (p.has_zeros ? 2u : 1u);
+            int c = 0;
+            uint32_t ph = 1;
+            for (int at = at0; at < at1; ++at) {
+                if (!wait_phase(c_empty(c), ph, p.status, kSiteTileCodes, p.timeout_ns)) {
+                    ok = false;
+                    break;
                 }
+                const uint32_t side = base + static_cast<uint32_t>(p.side_off + c * 2 * p.side_bytes);
+                ptx::mbar_arrive_expect_tx(c_full(c), tx);
+                ptx::tma_load_2d_hint(base + static_cast<uint32_t>(p.codes_off + c * p.rows_b * 128), &tmW, c_full(c), at * 128, n0, pol_w);
+                ptx::tma_load_2d(side, &tmS, c_full(c), n0, at * p.atom_groups);
+                if (p.has_zeros) ptx::tma_load_2d(side + static_cast<uint32_t>(p.side_bytes), &tmZ, c_full(c), n0, at * p.atom_groups);
+                if (++c == p.codes) {
+                    c = 0;
+                    ph ^= 1u;
+                }
+            }
+            if (!ok) {
+                for (uint32_t q = 0; q < 2; ++q)
+                    for (int i = 0; i < p.codes; ++i) wait_phase(c_full(i), q, p.status, kSiteStreamDrain, 1000000);
             }
         }
         __syncwarp();
@@ -250,18 +274,24 @@ w4_tiles_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
             const uint32_t idesc = ptx::instr_desc(128, p.rows_a, p.ab_format);
             int s = 0;
             uint32_t ph = 0;
-            for (int b = 0; b < blocks; ++b) {
+            for (int b = 0; b < blocks; b += KB) {
                 if (!wait_phase(full(s), ph, p.status, kSiteTileMma, p.timeout_ns)) {
                     ok = false;
                     break;
                 }
                 ptx::tc_fence_after();
-                const uint64_t x = ptx::sw128_kmajor_desc(base + s * a_bytes);
-                const uint32_t w = tmem + 256u + 32u * s;
+                const uint32_t a = base + KB * s * a_bytes, w = tmem + 256u + 32u * KB * s;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) ptx::mma_f16_ts(tmem, w + 8u * k, x + 2u * k, idesc, (b != 0 || k != 0) ? 1u : 0u);
+                for (int i = 0; i < KB; ++i) {
+                    if (b + i < blocks) {
+                        const uint64_t x = ptx::sw128_kmajor_desc(a + i * a_bytes);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            ptx::mma_f16_ts(tmem, w + 32u * i + 8u * k, x + 2u * k, idesc, (b != 0 || i != 0 || k != 0) ? 1u : 0u);
+                    }
+                }
                 ptx::mma_commit(empty(s));
-                if (++s == NS) {
+                if (++s == kTileStages) {
                     s = 0;
                     ph ^= 1u;
                 }
@@ -278,69 +308,73 @@ w4_tiles_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q * 32) << 16);
         const uint32_t mask = ptx::opaque(0x000f000fu), kb = ptx::opaque(Pair<T>::kBase);
         const int g_shift = p.group == 32 ? 5 : (p.group == 64 ? 6 : 7);
-        for (int b = wg; b < blocks; b += kTileGroups) {
-            const int i = b >> 2, c_use = i / p.codes, c = i - c_use * p.codes, use = b / NS, s = b - use * NS;
+        for (int t = wg; t < steps; t += kTileGroups) {
+            const int i = t / (4 / KB), c_use = i / p.codes, c = i - c_use * p.codes, use = t / kTileStages, s = wg;
+            const int part = t % (4 / KB);   // of the atom
             if (!wait_phase_warp(c_full(c), c_use & 1, p.status, kSiteTileCodes, p.timeout_ns)) {
                 ok = false;
                 break;
             }
             const uint32_t there = base + ptx::stage_token();
             const uint32_t codes = there + static_cast<uint32_t>(p.codes_off + (c * p.rows_b + row) * 128);
-            uint32_t w[8];
-            {
-                uint32_t lo[4], hi[4];
-                const int ch = (b & 3) * 2;
-                ptx::ld_shared_u4<0>(codes + static_cast<uint32_t>((ch ^ (row & 7)) << 4), lo);
-                ptx::ld_shared_u4<0>(codes + static_cast<uint32_t>(((ch + 1) ^ (row & 7)) << 4), hi);
+            uint32_t w[8 * KB];
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    w[v] = lo[v];
-                    w[4 + v] = hi[v];
-                }
+            for (int v = 0; v < 2 * KB; ++v) {
+                uint32_t x[4];
+                ptx::ld_shared_u4<0>(codes + static_cast<uint32_t>(((part * 2 * KB + v) ^ (row & 7)) << 4), x);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) w[4 * v + u] = x[u];
             }
-            // scale (and zero point) of each 32 k
-            uint32_t sc[2], zr[2];
+            // scale and minus zero point of each 32 k, in both halves of a register
+            uint32_t sc[2 * KB], zr[2 * KB];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int grp = ((b & 3) * 64 + h * 32) >> g_shift;
+            for (int h = 0; h < 2 * KB; ++h) {
+                const int grp = (part * 64 * KB + h * 32) >> g_shift;
                 const uint32_t at = there + static_cast<uint32_t>(p.side_off + c * 2 * p.side_bytes + (grp * p.rows_b + row) * 2);
                 sc[h] = ptx::ld_shared_u16<0>(at) * 0x10001u;
                 zr[h] = p.has_zeros ? ((ptx::ld_shared_u16<0>(at + static_cast<uint32_t>(p.side_bytes)) * 0x10001u) ^ 0x80008000u) : 0u;
             }
-            uint32_t r[32];
-            // code words and scales are in registers: the atom may be refilled (it is one K block of every group)
+            // code words and scales are in registers: the atom may be refilled
 #pragma unroll
-            for (int v = 0; v < 8; ++v) asm volatile("" : "+r"(w[v]) :: "memory");
-            asm volatile("" : "+r"(sc[0]), "+r"(sc[1]), "+r"(zr[0]), "+r"(zr[1]) :: "memory");
+            for (int v = 0; v < 8 * KB; ++v) asm volatile("" : "+r"(w[v]) :: "memory");
+#pragma unroll
+            for (int h = 0; h < 2 * KB; ++h) asm volatile("" : "+r"(sc[h]), "+r"(zr[h]) :: "memory");
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(c_empty(c));
 #pragma unroll
-            for (int v = 0; v < 8; ++v) {
-                const uint32_t odd = w[v] >> 4;
-                uint32_t x[4] = {__byte_perm(w[v], odd, 0x0400), __byte_perm(w[v], odd, 0x0501), __byte_perm(w[v], odd, 0x0602),
-                                 __byte_perm(w[v], odd, 0x0703)};   // codes 2 u and 2 u + 1 in the low bits of each half
+            for (int blk = 0; blk < KB; ++blk) {
+                if (KB * t + blk >= blocks) break;
+                uint32_t r[32];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    uint32_t d = ptx::and_or(x[u], mask, kb);
-                    if (p.has_zeros) d = Pair<T>::add(Pair<T>::add(d, Pair<T>::kMinusBase), zr[v >> 2]);
-                    else d = Pair<T>::add(d, Pair<T>::kMinusBase8);
-                    const uint32_t prod = Pair<T>::mul(d, sc[v >> 2]);
-                    if (PAIRS && q >= 2) r[4 * v + u] = Pair<T>::fma(d, sc[v >> 2], Pair<T>::neg(prod));
-                    else r[4 * v + u] = prod;
+                for (int v = 0; v < 8; ++v) {
+                    const uint32_t word = w[8 * blk + v], odd = word >> 4, sv = sc[2 * blk + (v >> 2)];
+                    // codes 2 u and 2 u + 1 in the low bits of each half
+                    const uint32_t x[4] = {__byte_perm(word, odd, 0x0400), __byte_perm(word, odd, 0x0501),
+                                           __byte_perm(word, odd, 0x0602), __byte_perm(word, odd, 0x0703)};
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        uint32_t d = ptx::and_or(x[u], mask, kb);
+                        if (p.has_zeros) d = Pair<T>::add(Pair<T>::add(d, Pair<T>::kMinusBase), zr[2 * blk + (v >> 2)]);
+                        else d = Pair<T>::add(d, Pair<T>::kMinusBase8);
+                        const uint32_t prod = Pair<T>::mul(d, sv);
+                        if (PAIRS && q >= 2) r[4 * v + u] = Pair<T>::fma(d, sv, Pair<T>::neg(prod));
+                        else r[4 * v + u] = prod;
+                    }
                 }
+                if (blk == 0) {
+                    if (use > 0 && !wait_phase_warp(empty(s), (use & 1) ^ 1u, p.status, kSiteTileEmpty, p.timeout_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                }
+                ptx::tmem_st_x32(lane_addr + 256u + 32u * (KB * s + blk), r);
             }
-            if (use > 0 && !wait_phase_warp(empty(s), (use & 1) ^ 1u, p.status, kSiteTileEmpty, p.timeout_ns)) {
-                ok = false;
-                break;
-            }
-            ptx::tc_fence_after();
-            ptx::tmem_st_x32(lane_addr + 256u + 32u * s, r);
+            if (!ok) break;
             ptx::tmem_wait_st();
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-                ptx::mbar_arrive(full(s));
-            }
+            if (lane == 0) ptx::mbar_arrive(full(s));
         }
     }
 
