@@ -65,7 +65,7 @@ gemm_status_t launch_down(const FfnParams& f, const void* h, const DeviceView& d
     const int lists = list_offsets(f.T * f.k, f.E).end;
     p.N = f.H;
     p.K = f.I;
-    const int smem = plan_rows<W4, NT, true>(reinterpret_cast<const void*>(weight_rows_kernel<T, CPG, NT, true>), &p, f.T, std::min(8 * NT, 2 * f.T), std::min(8 * NT, 2 * typical_slots(f)), sg.atom_groups, lists, dev);
+    const int smem = plan_rows<W4, NT, true>(reinterpret_cast<const void*>(weight_rows_kernel<T, CPG, NT, true>), &p, f.T, std::min(8 * NT, 2 * f.T), std::min(8 * NT, 2 * typical_slots(f)), std::min(f.E, f.T * f.k), sg.atom_groups, lists, dev);
     if (smem <= 0) return GEMM_ERR_CUDA;
     p.groups_k = sg.groups_k;
     p.atom_groups = sg.atom_groups;

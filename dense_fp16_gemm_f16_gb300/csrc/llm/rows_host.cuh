@@ -136,12 +136,60 @@ gemm_status_t launch_stream(Kernel kernel, int dev, int grid, int cluster, int s
     return launch_clusters(kernel, dev, grid, kStreamThreads, cluster, smem, s, w, sc, zr, p);
 }
 
+// What plan_rows decides from, and the decision.  A thread keeps its last few: a
+// model's calls repeat a handful of shapes, and deciding takes microseconds.
+struct RowsPlan {
+    const void* kernel = nullptr;
+    int dev = 0, N = 0, K = 0, tokens = 0, cols = 0, typical_cols = 0, segments = 0, atom_groups = 0, lists = 0;
+    RowsParams p;
+    int smem = 0;
+    bool same(const RowsPlan& o) const {
+        return kernel == o.kernel && dev == o.dev && N == o.N && K == o.K && tokens == o.tokens && cols == o.cols &&
+               typical_cols == o.typical_cols && segments == o.segments && atom_groups == o.atom_groups && lists == o.lists;
+    }
+};
+
+template <bool W4, int NT, bool MOE>
+int plan_rows_anew(const void* kernel, RowsParams* p, int tokens, int cols, int typical_cols, int segments,
+                   int atom_groups, int lists, const DeviceView& dev);
+
+template <bool W4, int NT, bool MOE>
+int plan_rows(const void* kernel, RowsParams* p, int tokens, int cols, int typical_cols, int segments, int atom_groups,
+              int lists, const DeviceView& dev) {
+    thread_local RowsPlan known[8];
+    thread_local int next = 0;
+    RowsPlan want;
+    want.kernel = kernel;
+    want.dev = dev.dev;
+    want.N = p->N;
+    want.K = p->K;
+    want.tokens = tokens;
+    want.cols = cols;
+    want.typical_cols = typical_cols;
+    want.segments = segments;
+    want.atom_groups = atom_groups;
+    want.lists = lists;
+    for (const RowsPlan& k : known)
+        if (k.same(want)) {
+            *p = k.p;
+            return k.smem;
+        }
+    want.smem = plan_rows_anew<W4, NT, MOE>(kernel, p, tokens, cols, typical_cols, segments, atom_groups, lists, dev);
+    want.p = *p;
+    if (want.smem > 0) {
+        known[next] = want;
+        next = (next + 1) % 8;
+    }
+    return want.smem;
+}
+
 // Fills the split and the shared-memory layout of `p` (N and K set): `tokens`
-// outputs per row, at most `cols` columns per stage, mostly typical_cols.  Returns the dynamic shared memory
+// outputs per row, at most `cols` columns per stage, mostly typical_cols, about `segments`
+// matrices.  Returns the dynamic shared memory
 // of the launch, 0 when nothing fits.
 template <bool W4, int NT, bool MOE>
-int plan_rows(const void* kernel, RowsParams* p, int tokens, int cols, int typical_cols, int atom_groups, int lists,
-              const DeviceView& dev) {
+int plan_rows_anew(const void* kernel, RowsParams* p, int tokens, int cols, int typical_cols, int segments,
+                   int atom_groups, int lists, const DeviceView& dev) {
     constexpr int budget = kSmemBudget<NT>;
     constexpr int MT = kTilesPerWarp<W4, NT>;
     const int table_cols = MOE ? tokens : 8 * NT;
@@ -185,11 +233,11 @@ int plan_rows(const void* kernel, RowsParams* p, int tokens, int cols, int typic
                 // another.
                 const int per_warp = (tiles + mw - 1) / mw;
                 const double work = W4 ? 8.0 * (10.0 * nt + per_warp * (22.0 + 6.0 * nt)) : 4.0 * (6.0 * nt + per_warp * (5.0 + 3.0 * nt));
-                const double arith = kCtasPerSm<NT> * (work + 200.0 / atoms) * mw / 2.0;
+                const double arith = kCtasPerSm<NT> * (work + 200.0 / atoms) * mw * (0.9 + 0.1 * mw) / 2.0;
                 const double flight = std::min(1.0, c.ring.slots * atoms * width * 128 / (65536.0 / kCtasPerSm<NT>));
                 const double copies = kCtasPerSm<NT> * (width * 128 / 23.5 + typical_cols * (W4 ? 512 : 128) / 50.0) / flight;
                 const double latency = (1500.0 + 1500.0 * (mw - 1)) / (kw * atoms) + 2.0 * work / kw;
-                const double n_atoms = std::ceil(std::ceil(static_cast<double>(c.k_stages) / P) / kw) * kw * atoms;
+                const double n_atoms = std::ceil(std::ceil(static_cast<double>(segments) * c.k_stages / P) / kw) * kw * atoms;
                 const double t = rounds * n_atoms * std::max(std::max(arith, copies), latency) + (P > 1 ? 800.0 : 0.0) + tables / 100.0;
                 if (best == 0 || t < best_t) {
                     best_t = t;

@@ -14,7 +14,7 @@ gemm_status_t launch(const void* A, const Weights& w, void* D, int64_t row0, int
     const SideGroups sg(w, K);
     p.N = static_cast<int32_t>(N);
     p.K = static_cast<int32_t>(K);
-    const int smem = plan_rows<true, NT, false>(reinterpret_cast<const void*>(weight_rows_kernel<T, CPG, NT, false>), &p, M, M, M, sg.atom_groups, 0, dev);
+    const int smem = plan_rows<true, NT, false>(reinterpret_cast<const void*>(weight_rows_kernel<T, CPG, NT, false>), &p, M, M, M, 1, sg.atom_groups, 0, dev);
     if (smem <= 0) return GEMM_ERR_CUDA;
     p.groups_k = sg.groups_k;
     p.atom_groups = sg.atom_groups;

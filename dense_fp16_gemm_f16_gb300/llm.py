@@ -60,17 +60,24 @@ def declare(lib) -> None:
 
 
 _torch = None
+_lib = None
 _dtypes: dict = {}
+_raw_stream = None
+_current_device = None
 
 
 def _setup():
     """torch and the library, once; returns the library."""
-    global _torch
-    lib = _g._lib or _g.load()
-    if _torch is None:
-        import torch
-        _dtypes.update({torch.float16: int(_g.Dtype.F16), torch.bfloat16: int(_g.Dtype.BF16)})
-        _torch = torch
+    global _torch, _lib, _raw_stream, _current_device
+    lib = _g.load()
+    import torch
+    _dtypes.update({torch.float16: int(_g.Dtype.F16), torch.bfloat16: int(_g.Dtype.BF16)})
+    # the current stream's handle without a Stream object around it, which
+    # costs 2 us of the 8 that a small call takes
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _current_device = torch.cuda.current_device
+    _torch, _lib = torch, lib
     return lib
 
 
@@ -81,55 +88,63 @@ def _type16(t, name: str) -> int:
         raise TypeError(f"{name} must be a float16 or bfloat16 tensor, got {getattr(t, 'dtype', type(t))}") from None
 
 
-def _check(t, name: str, dtype, shape, device) -> int:
-    """The address of a contiguous tensor of this type and shape on `device`."""
+def _check(t, name: str, dtype, shape, index: int) -> int:
+    """The address of a contiguous tensor of this type and shape on CUDA device `index`."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not _g._is_tensor(t):
         raise TypeError(f"{name} must be a tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
+    if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _cuda(t, name: str):
+def _cuda(t, name: str) -> int:
+    """The CUDA device index of a contiguous tensor."""
     if not _g._is_tensor(t):
         raise TypeError(f"{name} must be a tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t.device
+    return t.get_device()
 
 
-def _weights(w, name: str, dtype, lead: tuple, N: int, K: int, device) -> Weights:
+def _weights(w, name: str, dtype, lead: tuple, N: int, K: int, index: int) -> Weights:
     """A W4 or a 16-bit tensor [*lead, N, K] as the library takes it."""
-    if not isinstance(w, W4):
-        return Weights(_check(w, name, dtype, (*lead, N, K), device), None, None, 0, 0)
+    if type(w) is not W4:
+        return Weights(_check(w, name, dtype, (*lead, N, K), index), None, None, 0, 0)
     group = w.group
     if group not in (32, 64, 128):
         raise ValueError(f"{name}: group must be 32, 64 or 128, got {group}")
     if K % group:
         raise ValueError(f"{name}: K = {K} is not a multiple of the group ({group})")
     side = (*lead, K // group, N)
-    return Weights(_check(w.codes, name + ".codes", _torch.uint8, (*lead, N, K // 2), device),
-                   _check(w.scales, name + ".scales", dtype, side, device),
-                   None if w.zeros is None else _check(w.zeros, name + ".zeros", dtype, side, device), group, 0)
+    return Weights(_check(w.codes, name + ".codes", _torch.uint8, (*lead, N, K // 2), index),
+                   _check(w.scales, name + ".scales", dtype, side, index),
+                   None if w.zeros is None else _check(w.zeros, name + ".zeros", dtype, side, index), group, 0)
 
 
-def _run(fn_name: str, fn, device, stream, args) -> None:
+def _run(fn, index: int, stream, args) -> None:
     """fn(*args, stream) with the tensors' device current."""
-    if device.index == _torch.cuda.current_device():
-        st = fn(*args, _g._stream_handle(stream, device))
+    if stream is None:
+        handle = _raw_stream(index) or None
     else:
-        with _torch.cuda.device(device):
-            st = fn(*args, _g._stream_handle(stream, device))
+        handle = stream.cuda_stream or None if hasattr(stream, "cuda_stream") else int(stream) or None
+    if index == _current_device():
+        st = fn(*args, handle)
+    else:
+        with _torch.cuda.device(index):
+            st = fn(*args, handle)
     if st:
-        raise _g.GemmError(st, fn_name)
+        raise _g.GemmError(st, fn.__name__)
 
 
 def gemm_w4_quantize(W, group: int = 128, codes=None, scales=None, zeros=None, symmetric: bool | None = None,
@@ -138,8 +153,8 @@ def gemm_w4_quantize(W, group: int = 128, codes=None, scales=None, zeros=None, s
 
     ``symmetric`` (default: True unless ``zeros`` is given) uses the fixed zero
     point 8; otherwise every group gets its own.  Outputs are allocated unless given."""
-    lib = _setup()
-    device = _cuda(W, "W")
+    lib = _lib or _setup()
+    index = _cuda(W, "W")
     dt = _type16(W, "W")
     if W.dim() not in (2, 3):
         raise ValueError(f"W must be [N, K] or [E, N, K], got {tuple(W.shape)}")
@@ -154,33 +169,33 @@ def gemm_w4_quantize(W, group: int = 128, codes=None, scales=None, zeros=None, s
         raise ValueError("symmetric weights have no zero points")
     side = (*lead, K // group, N)
     if codes is None:
-        codes = _torch.empty((*lead, N, K // 2), dtype=_torch.uint8, device=device)
+        codes = _torch.empty((*lead, N, K // 2), dtype=_torch.uint8, device=W.device)
     if scales is None:
-        scales = _torch.empty(side, dtype=W.dtype, device=device)
+        scales = _torch.empty(side, dtype=W.dtype, device=W.device)
     if zeros is None and not symmetric:
-        zeros = _torch.empty(side, dtype=W.dtype, device=device)
+        zeros = _torch.empty(side, dtype=W.dtype, device=W.device)
     out = W4(codes, scales, zeros, group)
-    w = _weights(out, "output", W.dtype, tuple(lead), N, K, device)
-    _run("gemm_w4_quantize", lib.gemm_w4_quantize, device, stream,
+    w = _weights(out, "output", W.dtype, tuple(lead), N, K, index)
+    _run(lib.gemm_w4_quantize, index, stream,
          (dt, W.data_ptr(), lead[0] if lead else 1, N, K, group, w.data, w.scales, w.zeros))
     return out
 
 
 def gemm_w4_dequantize(W: W4, out=None, stream=None):
     """The float16 / bfloat16 matrices that `W` stands for, in ``out`` (allocated unless given)."""
-    lib = _setup()
+    lib = _lib or _setup()
     if not isinstance(W, W4):
         raise TypeError("W must be a W4")
-    device = _cuda(W.codes, "W.codes")
+    index = _cuda(W.codes, "W.codes")
     dt = _type16(W.scales, "W.scales")
     if W.codes.dim() not in (2, 3):
         raise ValueError(f"W.codes must be [N, K/2] or [E, N, K/2], got {tuple(W.codes.shape)}")
     *lead, N, K = W.shape
-    w = _weights(W, "W", W.scales.dtype, tuple(lead), N, K, device)
+    w = _weights(W, "W", W.scales.dtype, tuple(lead), N, K, index)
     if out is None:
-        out = _torch.empty(W.shape, dtype=W.scales.dtype, device=device)
-    ptr = _check(out, "out", W.scales.dtype, W.shape, device)
-    _run("gemm_w4_dequantize", lib.gemm_w4_dequantize, device, stream,
+        out = _torch.empty(W.shape, dtype=W.scales.dtype, device=W.codes.device)
+    ptr = _check(out, "out", W.scales.dtype, W.shape, index)
+    _run(lib.gemm_w4_dequantize, index, stream,
          (dt, ctypes.byref(w), lead[0] if lead else 1, N, K, ptr))
     return out
 
@@ -188,8 +203,8 @@ def gemm_w4_dequantize(W: W4, out=None, stream=None):
 def gemm_w4_nt(A, B: W4, D, alpha=1.0, beta=0.0, C=None, bias=None, activation=_g.Activation.NONE, stream=None,
                scale_n=None) -> None:
     """D = act(alpha·scale_n[n]·A·Bᵀ + beta·C + bias[n]) with the weights B [N, K] in 4 bits."""
-    lib = _setup()
-    device = _cuda(A, "A")
+    lib = _lib or _setup()
+    index = _cuda(A, "A")
     dt = _type16(A, "A")
     if not isinstance(B, W4):
         raise TypeError("B must be a W4")
@@ -198,27 +213,27 @@ def gemm_w4_nt(A, B: W4, D, alpha=1.0, beta=0.0, C=None, bias=None, activation=_
     M, K = A.shape
     N = B.codes.shape[0]
     dtype = A.dtype
-    w = _weights(B, "B", dtype, (), N, K, device)
-    d = _check(D, "D", dtype, (M, N), device)
+    w = _weights(B, "B", dtype, (), N, K, index)
+    d = _check(D, "D", dtype, (M, N), index)
     epi = None
     if alpha != 1.0 or beta != 0.0 or bias is not None or scale_n is not None or activation:
         epi = ctypes.byref(_g.Epilogue(
-            float(alpha), float(beta), None if C is None else _check(C, "C", dtype, (M, N), device),
-            None if bias is None else _check(bias, "bias", dtype, (N,), device), int(activation), 0,
-            None if scale_n is None else _check(scale_n, "scale_n", _torch.float32, (N,), device)))
-    _run("gemm_w4_nt", lib.gemm_w4_nt, device, stream, (dt, A.data_ptr(), ctypes.byref(w), d, M, N, K, epi))
+            float(alpha), float(beta), None if C is None else _check(C, "C", dtype, (M, N), index),
+            None if bias is None else _check(bias, "bias", dtype, (N,), index), int(activation), 0,
+            None if scale_n is None else _check(scale_n, "scale_n", _torch.float32, (N,), index)))
+    _run(lib.gemm_w4_nt, index, stream, (dt, A.data_ptr(), ctypes.byref(w), d, M, N, K, epi))
 
 
 def _tokens(X, Wr, bias):
-    device = _cuda(X, "X")
+    index = _cuda(X, "X")
     dt = _type16(X, "X")
     if X.dim() != 2 or not _g._is_tensor(Wr) or Wr.dim() != 2:
         raise ValueError("X must be [T, H] and Wr [E, H]")
     T, H = X.shape
     E = Wr.shape[0]
-    wr = _check(Wr, "Wr", X.dtype, (E, H), device)
-    b = None if bias is None else _check(bias, "bias", _torch.float32, (E,), device)
-    return device, dt, T, H, E, wr, b
+    wr = _check(Wr, "Wr", X.dtype, (E, H), index)
+    b = None if bias is None else _check(bias, "bias", _torch.float32, (E,), index)
+    return index, dt, T, H, E, wr, b
 
 
 def gemm_moe_route(X, Wr, ids=None, weights=None, k: int | None = None, bias=None, scoring=MoeScoring.SOFTMAX,
@@ -230,30 +245,30 @@ def gemm_moe_route(X, Wr, ids=None, weights=None, k: int | None = None, bias=Non
     lower expert first where equal.  An id of -1 beside a weight of 0 means that
     no further expert is allowed (bias of minus infinity).  ``k`` is taken from
     ``ids`` where that is given."""
-    lib = _setup()
-    device, dt, T, H, E, wr, b = _tokens(X, Wr, bias)
+    lib = _lib or _setup()
+    index, dt, T, H, E, wr, b = _tokens(X, Wr, bias)
     if k is None:
         if ids is None:
             raise ValueError("give k or ids")
         k = ids.shape[-1]
     if ids is None:
-        ids = _torch.empty((T, k), dtype=_torch.int32, device=device)
+        ids = _torch.empty((T, k), dtype=_torch.int32, device=X.device)
     if weights is None:
-        weights = _torch.empty((T, k), dtype=_torch.float32, device=device)
-    _run("gemm_moe_route", lib.gemm_moe_route, device, stream,
+        weights = _torch.empty((T, k), dtype=_torch.float32, device=X.device)
+    _run(lib.gemm_moe_route, index, stream,
          (dt, X.data_ptr(), wr, b, T, H, E, k, int(scoring), 1 if renormalize else 0,
-          _check(ids, "ids", _torch.int32, (T, k), device),
-          _check(weights, "weights", _torch.float32, (T, k), device)))
+          _check(ids, "ids", _torch.int32, (T, k), index),
+          _check(weights, "weights", _torch.float32, (T, k), index)))
     return ids, weights
 
 
-def _experts(W13, W2, dtype, H, E, device):
+def _experts(W13, W2, dtype, H, E, index):
     """(w13, w2, I) of E experts as the library takes them."""
     rows = W13.codes if isinstance(W13, W4) else W13
     if not _g._is_tensor(rows) or rows.dim() != 3 or rows.shape[0] != E or rows.shape[1] % 2:
         raise ValueError(f"W13 must be [{E}, 2 I, {H}]")
     I = rows.shape[1] // 2
-    return (_weights(W13, "W13", dtype, (E,), 2 * I, H, device), _weights(W2, "W2", dtype, (E,), H, I, device), I)
+    return (_weights(W13, "W13", dtype, (E,), 2 * I, H, index), _weights(W2, "W2", dtype, (E,), H, I, index), I)
 
 
 def gemm_moe_ffn(X, ids, weights, W13, W2, Y, stream=None) -> None:
@@ -261,27 +276,27 @@ def gemm_moe_ffn(X, ids, weights, W13, W2, Y, stream=None) -> None:
 
     W13 [E, 2 I, H] (gate rows, then up rows) and W2 [E, H, I] are tensors of X's
     type or ``W4`` stacks.  Ids outside [0, E) are skipped.  At most 64 tokens."""
-    lib = _setup()
-    device = _cuda(X, "X")
+    lib = _lib or _setup()
+    index = _cuda(X, "X")
     dt = _type16(X, "X")
     if X.dim() != 2 or not _g._is_tensor(ids) or ids.dim() != 2:
         raise ValueError("X must be [T, H] and ids [T, k]")
     T, H = X.shape
     k = ids.shape[1]
     E = (W13.codes if isinstance(W13, W4) else W13).shape[0]
-    w13, w2, I = _experts(W13, W2, X.dtype, H, E, device)
-    _run("gemm_moe_ffn", lib.gemm_moe_ffn, device, stream,
-         (dt, X.data_ptr(), _check(ids, "ids", _torch.int32, (T, k), device),
-          _check(weights, "weights", _torch.float32, (T, k), device), ctypes.byref(w13), ctypes.byref(w2),
-          _check(Y, "Y", X.dtype, (T, H), device), T, H, I, E, k))
+    w13, w2, I = _experts(W13, W2, X.dtype, H, E, index)
+    _run(lib.gemm_moe_ffn, index, stream,
+         (dt, X.data_ptr(), _check(ids, "ids", _torch.int32, (T, k), index),
+          _check(weights, "weights", _torch.float32, (T, k), index), ctypes.byref(w13), ctypes.byref(w2),
+          _check(Y, "Y", X.dtype, (T, H), index), T, H, I, E, k))
 
 
 def gemm_moe_layer(X, Wr, W13, W2, Y, k: int, bias=None, scoring=MoeScoring.SOFTMAX, renormalize: bool = True,
                    stream=None) -> None:
     """A whole mixture-of-experts layer for at most 64 tokens: gemm_moe_route, then gemm_moe_ffn on its choice."""
-    lib = _setup()
-    device, dt, T, H, E, wr, b = _tokens(X, Wr, bias)
-    w13, w2, I = _experts(W13, W2, X.dtype, H, E, device)
-    _run("gemm_moe_layer", lib.gemm_moe_layer, device, stream,
-         (dt, X.data_ptr(), wr, b, ctypes.byref(w13), ctypes.byref(w2), _check(Y, "Y", X.dtype, (T, H), device),
+    lib = _lib or _setup()
+    index, dt, T, H, E, wr, b = _tokens(X, Wr, bias)
+    w13, w2, I = _experts(W13, W2, X.dtype, H, E, index)
+    _run(lib.gemm_moe_layer, index, stream,
+         (dt, X.data_ptr(), wr, b, ctypes.byref(w13), ctypes.byref(w2), _check(Y, "Y", X.dtype, (T, H), index),
           T, H, I, E, k, int(scoring), 1 if renormalize else 0))
