@@ -42,11 +42,20 @@ gemm_status_t launch_up(const FfnParams& f, void* h, const DeviceView& dev, cuda
         const int kw = kConsumers / mw;
         const int sums = kw * 8 * NT * kUpPitch * 4;
         p.mw = mw;
-        p.ring = ring_layout(W4, 1, kUpRows, 2 * kUpGranules * 8, sg.atom_groups, cols, kSmemBudget<NT> - 1024 - lists - sums, kw);
-        p.list_off = p.ring.end;
+        // 4-bit weights: a segment's columns stay in shared memory over all its
+        // pieces if they take at most half of it; a stage of columns would be as
+        // large as the weights beside it
+        const int fixed = 1024 + lists + sums;
+        p.x_pitch = up_to(f.H * 2, 128) + 64;
+        const int resident = W4 ? up_to(up_to(cols, 8) * p.x_pitch, 128) : 0;
+        p.x_resident = W4 && resident <= kSmemBudget<W4, NT> / 2 && fixed + resident + kw * 12 * 1024 <= kSmemBudget<W4, NT>;
+        p.ring = ring_layout(W4, 1, kUpRows, 2 * kUpGranules * 8, sg.atom_groups, p.x_resident ? 0 : cols,
+                             kSmemBudget<W4, NT> - fixed - (p.x_resident ? resident : 0), kw);
+        p.x_off = p.ring.end;
+        p.list_off = p.x_off + (p.x_resident ? resident : 0);
         p.sums_off = p.list_off + lists;
         smem = p.sums_off + sums + 1024;
-        if (smem <= kSmemBudget<NT> && p.ring.slots >= 8) break;
+        if (smem <= kSmemBudget<W4, NT> && p.ring.slots >= 8) break;
     }
     if (smem > kMaxDynamicSmem) return GEMM_ERR_CUDA;
     p.k_stages = (f.H + kAtomElems<W4> - 1) / kAtomElems<W4>;
@@ -54,7 +63,7 @@ gemm_status_t launch_up(const FfnParams& f, void* h, const DeviceView& dev, cuda
     if (!encode_weights(f.w13, rows, static_cast<int64_t>(f.E) * sg.groups_k, 2 * f.I, f.H, 8, kUpGranules * 8, sg.atom_groups, &w, &sc, &zr) ||
         !encode_weights_box(f.w13, rows, f.H, 8 * kUpGranules, &p.tm_piece))
         return GEMM_ERR_INVALID_VALUE;
-    return launch_stream(moe_up_kernel<T, CPG, NT>, dev.dev, kCtasPerSm<NT> * dev.sms, 1, smem, s, w, sc, zr, p);
+    return launch_stream(moe_up_kernel<T, CPG, NT>, dev.dev, kCtasPerSm<W4, NT> * dev.sms, 1, smem, s, w, sc, zr, p);
 }
 
 template <class T, int CPG, int NT>

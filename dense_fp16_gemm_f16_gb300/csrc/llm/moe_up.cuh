@@ -29,6 +29,7 @@ struct UpParams {
     CUtensorMap tm_piece;         // the weights in boxes of kUpGranules granules (tmW: of one)
     RingLayout ring;
     int32_t list_off, sums_off;
+    int32_t x_resident, x_off, x_pitch;   // 4-bit weights: a segment's columns, all K
     int32_t H, I, k_stages, mw;
     int32_t groups_k, atom_groups, has_zeros;
     int32_t stream_w;
@@ -58,7 +59,7 @@ struct UpPieces {
 };
 
 template <class T, int CPG, int NT>
-__global__ void __launch_bounds__(kStreamThreads, kCtasPerSm<NT>)
+__global__ void __launch_bounds__(kStreamThreads, kCtasPerSm<(CPG != 0), NT>)
 moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmS,
               const __grid_constant__ CUtensorMap tmZ, const __grid_constant__ UpParams p) {
     constexpr bool W4 = CPG != 0;
@@ -77,7 +78,7 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
         ptx::prefetch_tensormap(&p.tm_piece);
     }
     if (static_cast<int>(threadIdx.x) < p.ring.slots) {
-        ptx::mbar_init(full_bar(threadIdx.x), kFullArrivals);
+        ptx::mbar_init(full_bar(threadIdx.x), p.x_resident ? 1u : full_arrivals(p.mw));
         ptx::mbar_init(empty_bar(threadIdx.x), static_cast<uint32_t>(p.mw));
         ptx::fence_mbar_init();
     }
@@ -91,7 +92,7 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
     const UpPieces all{total * blockIdx.x / gridDim.x, total * (blockIdx.x + 1) / gridDim.x, per_seg};
 
     constexpr int KE = kAtomElems<W4>;
-    const int pitch = col_pitch(W4, 1);
+    const int pitch = p.x_resident ? p.x_pitch : col_pitch(W4, 1);
     const int mg = warp % p.mw, kg = warp / p.mw;
     const GroupSlots own(p.ring.slots, KW, kg);
     const uint64_t pol_w = p.stream_w ? ptx::policy_evict_first() : ptx::policy_evict_normal();
@@ -103,27 +104,30 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
         const int first = lists.seg_begin[seg], n = lists.seg_begin[seg + 1] - first;
         const int e = lists.seg_e[seg];
         const int kv = min(KE, p.H - kb * KE);
-        if (lane == 0)
-            ptx::mbar_arrive_expect_tx(full_bar(s), static_cast<uint32_t>(count) * 2048u +
-                                                        (W4 ? 2u * side_half * (p.has_zeros ? 2u : 1u) : 0u));
-        __syncwarp();
-        const int32_t y = e * 2 * p.I + at * 8 + ((lane & 1) ? p.I : 0);   // even lanes: gate rows, odd lanes: up rows
-        const uint32_t dst = base + static_cast<uint32_t>(s * p.ring.w_bytes) + (lane & 1) * kHalf;
-        if (count == kUpGranules) {
-            if (lane < 2) ptx::tma_load_2d_hint(dst, &p.tm_piece, full_bar(s), kb * (W4 ? 128 : 64), y, pol_w);
-        } else if (lane < 2 * count) {
-            ptx::tma_load_2d_hint(dst + (lane >> 1) * 1024u, &tmW, full_bar(s), kb * (W4 ? 128 : 64), y + (lane >> 1) * 8, pol_w);
+        if (mg == 0) {
+            if (lane == 0)
+                ptx::mbar_arrive_expect_tx(full_bar(s), static_cast<uint32_t>(count) * 2048u +
+                                                            (W4 ? 2u * side_half * (p.has_zeros ? 2u : 1u) : 0u));
+            __syncwarp();
+            const int32_t y = e * 2 * p.I + at * 8 + ((lane & 1) ? p.I : 0);   // even lanes: gate rows, odd lanes: up rows
+            const uint32_t dst = base + static_cast<uint32_t>(s * p.ring.w_bytes) + (lane & 1) * kHalf;
+            if (count == kUpGranules) {
+                if (lane < 2) ptx::tma_load_2d_hint(dst, &p.tm_piece, full_bar(s), kb * (W4 ? 128 : 64), y, pol_w);
+            } else if (lane < 2 * count) {
+                ptx::tma_load_2d_hint(dst + (lane >> 1) * 1024u, &tmW, full_bar(s), kb * (W4 ? 128 : 64), y + (lane >> 1) * 8, pol_w);
+            }
+            if constexpr (W4) {
+                // [scales | zero points] x [gate | up] x [groups][32 rows]
+                const int q = lane - 8;
+                if (q >= 0 && q < (p.has_zeros ? 4 : 2))
+                    ptx::tma_load_2d(base + static_cast<uint32_t>(p.ring.side_off + s * p.ring.side_bytes + (q >> 1) * (p.ring.side_bytes / 2)) + (q & 1) * side_half,
+                                     (q >> 1) ? &tmZ : &tmS, full_bar(s), at * 8 + ((q & 1) ? p.I : 0), e * p.groups_k + kb * p.atom_groups);
         }
-        if constexpr (W4) {
-            // [scales | zero points] x [gate | up] x [groups][32 rows]
-            const int q = lane - 8;
-            if (q >= 0 && q < (p.has_zeros ? 4 : 2))
-                ptx::tma_load_2d(base + static_cast<uint32_t>(p.ring.side_off + s * p.ring.side_bytes + (q >> 1) * (p.ring.side_bytes / 2)) + (q & 1) * side_half,
-                                 (q >> 1) ? &tmZ : &tmS, full_bar(s), at * 8 + ((q & 1) ? p.I : 0), e * p.groups_k + kb * p.atom_groups);
         }
+        if (p.x_resident) return;
         const uint32_t x = base + static_cast<uint32_t>(p.ring.x_off + s * p.ring.x_bytes);
         constexpr int kShift = W4 ? 5 : 3;   // 32 or 8 pieces of 16 bytes per column
-        for (int i = lane; i < n << kShift; i += 32) {
+        for (int i = mg * 32 + lane; i < (n << kShift); i += 32 * p.mw) {   // the group's warps share them
             const int c = i >> kShift, o = (i - (c << kShift)) * 8;
             if (o < kv)
                 ptx::cp_async16(x + static_cast<uint32_t>(c * pitch + o * 2),
@@ -151,18 +155,30 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
         const int tile0 = mg * StreamWarp<T, W4, NT>::MT;   // this warp's tiles
         float* sums = reinterpret_cast<float*>(smem + p.sums_off);
         T* h = static_cast<T*>(p.h);
-        if (mg == 0)
-            for (int d = 0; d < own.depth; ++d)
-                if (!fetch_next(own.first + d)) break;
+        for (int d = 0; d < own.depth; ++d)
+            if (!fetch_next(own.first + d)) break;
         StreamWarp<T, W4, NT> sw;
         bool ok = true;
         int d = 0, kb = kg;
         uint32_t phase = 0;
         UpPieces pieces = all;
-        int seg, at, count;
+        int seg, at, count, x_seg = -1;
         while (pieces.next(seg, at, count)) {
             const int first = lists.seg_begin[seg], n = lists.seg_begin[seg + 1] - first;
             const int nt = (n + 7) >> 3;
+            if (p.x_resident && seg != x_seg) {
+                // nobody reads the last segment's columns any more: the sums'
+                // barriers are behind every warp
+                x_seg = seg;
+                const int pieces16 = p.H >> 3;
+                for (int c = warp; c < n; c += kConsumers) {
+                    const T* src = static_cast<const T*>(p.X) + static_cast<int64_t>(lists.slot[first + c] / p.k) * p.H;
+                    const uint32_t dst = base + static_cast<uint32_t>(p.x_off + c * p.x_pitch);
+                    for (int o = lane; o < pieces16; o += 32) ptx::cp_async16(dst + o * 16u, src + o * 8);
+                }
+                ptx::cp_async_wait_all();
+                __syncthreads();
+            }
             sw.clear();
             for (; ok && kb < p.k_stages; kb += KW) {
                 const int s = own.first + d;
@@ -173,7 +189,7 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 const int kv = min(KE, p.H - kb * KE);
                 const uint32_t there = base + ptx::stage_token();
                 const uint32_t w = there + static_cast<uint32_t>(s * p.ring.w_bytes + tile0 * 1024);
-                const uint32_t x = there + static_cast<uint32_t>(p.ring.x_off + s * p.ring.x_bytes);
+                const uint32_t x = there + static_cast<uint32_t>(p.x_resident ? p.x_off + kb * KE * 2 : p.ring.x_off + s * p.ring.x_bytes);
                 if constexpr (W4) {
                     const uint32_t sc = there + static_cast<uint32_t>(p.ring.side_off + s * p.ring.side_bytes + tile0 * 16);
                     const SideView side{sc, sc + static_cast<uint32_t>(p.ring.side_bytes / 2), side_half, kUpGranules * 16u};
@@ -185,12 +201,12 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 __syncwarp();
                 if (p.mw > 1) {
                     if (lane == 0) ptx::mbar_arrive(empty_bar(s));
-                    if (mg == 0 && f_more && !wait_phase_warp(empty_bar(s), phase, p.status, kSiteStreamEmpty, p.timeout_ns)) {
+                    if (f_more && !wait_phase_warp(empty_bar(s), phase, p.status, kSiteStreamEmpty, p.timeout_ns)) {
                         ok = false;
                         break;
                     }
                 }
-                if (mg == 0 && f_more) fetch_next(s);
+                if (f_more) fetch_next(s);
                 if (++d == own.depth) {
                     d = 0;
                     phase ^= 1u;

@@ -47,7 +47,7 @@ struct RowsParams {
 
 // CPG: 32-k chunks per group of 4-bit weights, 0 for 16-bit weights
 template <class T, int CPG, int NT, bool MOE>
-__global__ void __launch_bounds__(kStreamThreads, kCtasPerSm<NT>)
+__global__ void __launch_bounds__(kStreamThreads, kCtasPerSm<(CPG != 0), NT>)
 weight_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmS,
                    const __grid_constant__ CUtensorMap tmZ, const RowsParams p) {
     constexpr bool W4 = CPG != 0;
@@ -66,7 +66,7 @@ weight_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         ptx::prefetch_tensormap(&tmW);
     }
     if (static_cast<int>(threadIdx.x) < p.ring.slots) {
-        ptx::mbar_init(full_bar(threadIdx.x), kFullArrivals);
+        ptx::mbar_init(full_bar(threadIdx.x), full_arrivals(p.mw));
         ptx::mbar_init(empty_bar(threadIdx.x), static_cast<uint32_t>(p.mw));
         ptx::fence_mbar_init();
     }
@@ -126,7 +126,7 @@ weight_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         const int n = MOE ? 2 * (lists.seg_begin[seg + 1] - first) : p.cols;
         const uint32_t dst = base + static_cast<uint32_t>(p.ring.x_off + s * p.ring.x_bytes);
         const T* X = static_cast<const T*>(p.X) + static_cast<int64_t>(kb) * stage_elems;
-        for (int i = lane; i < (n << row_shift); i += 32) {
+        for (int i = mg * 32 + lane; i < (n << row_shift); i += 32 * p.mw) {   // the group's warps share them
             const int c = i >> row_shift, o = (i - (c << row_shift)) * 8;
             if (o < kv) {
                 const int64_t row = MOE ? 2 * static_cast<int64_t>(lists.slot[first + (c >> 1)]) + (c & 1) : c;
@@ -171,12 +171,12 @@ weight_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     }
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    Place ahead = start();   // the next stage to fetch (first warp of a group)
-    if (mg == 0) {
-        for (int d = 0; d < own.depth && ahead.left > 0; ++d, advance(ahead)) {
-            if constexpr (!MOE) issue_w(ahead.seg, ahead.kb, own.first + d);
-            issue_x(ahead.seg, ahead.kb, own.first + d);
+    Place ahead = start();   // the next stage to fetch: the first warp its rows, all of the group its columns
+    for (int d = 0; d < own.depth && ahead.left > 0; ++d, advance(ahead)) {
+        if constexpr (!MOE) {
+            if (mg == 0) issue_w(ahead.seg, ahead.kb, own.first + d);
         }
+        issue_x(ahead.seg, ahead.kb, own.first + d);
     }
 
     {
@@ -254,16 +254,14 @@ weight_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
             if (now.left > own.depth * KW) {   // another stage takes this slot
                 if (p.mw > 1) {
                     if (lane == 0) ptx::mbar_arrive(empty_bar(s));
-                    if (mg == 0 && !wait_phase_warp(empty_bar(s), phase, p.status, kSiteStreamEmpty, p.timeout_ns)) {
+                    if (!wait_phase_warp(empty_bar(s), phase, p.status, kSiteStreamEmpty, p.timeout_ns)) {
                         ok = false;
                         break;
                     }
                 }
-                if (mg == 0) {
-                    issue_w(ahead.seg, ahead.kb, s);
-                    issue_x(ahead.seg, ahead.kb, s);
-                    advance(ahead);
-                }
+                if (mg == 0) issue_w(ahead.seg, ahead.kb, s);
+                issue_x(ahead.seg, ahead.kb, s);
+                advance(ahead);
             }
             if (++d == own.depth) {
                 d = 0;

@@ -56,15 +56,18 @@ constexpr int kMaxAtoms = 4;                        // atoms per stage
 
 constexpr int kConsumers = 8;                       // warps
 constexpr int kStreamThreads = 32 * kConsumers;
-// CTAs per SM for NT groups of 8 columns.  Up to 16 columns the sums take few
-// registers and two CTAs fit: 16 warps to cover the decoding's chains of short
-// latencies, and one CTA's start and end beside the other's middle.
-template <int NT>
-constexpr int kCtasPerSm = NT <= 2 ? 2 : 1;
+// CTAs per SM for NT groups of 8 columns.  With few columns the sums take few
+// registers and two CTAs fit: 16 warps to cover the chains of short latencies,
+// and one CTA's start and end beside the other's middle.  With 4-bit weights and
+// more than 8 columns, registers for 4 tiles a warp and shared memory for the
+// columns (4 times a stage's weights, byte for byte) are worth more.
+template <bool W4, int NT>
+constexpr int kCtasPerSm = NT == 1 || (NT == 2 && !W4) ? 2 : 1;
 constexpr int kSmemPerSm = 226 * 1024;              // 228 KB less what the CTAs' static parts take
 
-// arrivals on a slot's full barrier: the byte count and every lane's columns
-constexpr uint32_t kFullArrivals = 33;
+// arrivals on a slot's full barrier: the byte count, and the columns of every
+// lane of the mw warps that share the slot
+__device__ __forceinline__ uint32_t full_arrivals(int mw) { return 1u + 32u * mw; }
 
 constexpr uint32_t kSiteStreamEmpty = 9, kSiteStreamFull = 10, kSiteStreamDrain = 11;
 
@@ -77,7 +80,7 @@ constexpr int kAtomElems = W4 ? 256 : 64;
 __host__ __device__ constexpr int col_pitch(bool w4, int ka) { return w4 ? ka * 512 + 64 : ka * 128 + 16; }
 // 16-row tiles per warp: the fp32 sums of tiles x columns stay in registers
 template <bool W4, int NT>
-constexpr int kTilesPerWarp = NT == 8 || (W4 && NT >= 2) ? 2 : 4;
+constexpr int kTilesPerWarp = NT == 8 || (W4 && NT == 4) ? 2 : 4;
 
 namespace ptx {
 
@@ -140,6 +143,8 @@ __device__ __forceinline__ void keep(float (&v)[4]) {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
 }
+
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // An arrival on `bar` once this thread's copies so far have landed (one of the
 // arrivals that the barrier was set up for).
