@@ -36,7 +36,7 @@ gemm_status_t launch_up(const FfnParams& f, void* h, const DeviceView& dev, cuda
     const int lists = list_offsets(f.T * f.k, f.E).end;
     const int cols = std::min(8 * NT, f.T);
     int smem = 0;
-    for (int mw = kUpGranules / kTilesPerWarp<W4, NT>; mw <= kUpGranules; mw *= 2) {
+    for (int mw = kUpGranules / kTilesPerWarp<W4, NT, true>; mw <= kUpGranules; mw *= 2) {
         // as few warps per stage as the registers allow, more where the sums
         // would leave too little in flight
         const int kw = kConsumers / mw;
@@ -48,14 +48,14 @@ gemm_status_t launch_up(const FfnParams& f, void* h, const DeviceView& dev, cuda
         const int fixed = 1024 + lists + sums;
         p.x_pitch = up_to(f.H * 2, 128) + 64;
         const int resident = W4 ? up_to(up_to(cols, 8) * p.x_pitch, 128) : 0;
-        p.x_resident = W4 && resident <= kSmemBudget<W4, NT> / 2 && fixed + resident + kw * 12 * 1024 <= kSmemBudget<W4, NT>;
+        p.x_resident = W4 && resident <= kSmemBudget<W4, NT, true> / 2 && fixed + resident + kw * 12 * 1024 <= kSmemBudget<W4, NT, true>;
         p.ring = ring_layout(W4, 1, kUpRows, 2 * kUpGranules * 8, sg.atom_groups, p.x_resident ? 0 : cols,
-                             kSmemBudget<W4, NT> - fixed - (p.x_resident ? resident : 0), kw);
+                             kSmemBudget<W4, NT, true> - fixed - (p.x_resident ? resident : 0), kw);
         p.x_off = p.ring.end;
         p.list_off = p.x_off + (p.x_resident ? resident : 0);
         p.sums_off = p.list_off + lists;
         smem = p.sums_off + sums + 1024;
-        if (smem <= kSmemBudget<W4, NT> && p.ring.slots >= 8) break;
+        if (smem <= kSmemBudget<W4, NT, true> && p.ring.slots >= 8) break;
     }
     if (smem > kMaxDynamicSmem) return GEMM_ERR_CUDA;
     p.k_stages = (f.H + kAtomElems<W4> - 1) / kAtomElems<W4>;
@@ -63,7 +63,7 @@ gemm_status_t launch_up(const FfnParams& f, void* h, const DeviceView& dev, cuda
     if (!encode_weights(f.w13, rows, static_cast<int64_t>(f.E) * sg.groups_k, 2 * f.I, f.H, 8, kUpGranules * 8, sg.atom_groups, &w, &sc, &zr) ||
         !encode_weights_box(f.w13, rows, f.H, 8 * kUpGranules, &p.tm_piece))
         return GEMM_ERR_INVALID_VALUE;
-    return launch_stream(moe_up_kernel<T, CPG, NT>, dev.dev, kCtasPerSm<W4, NT> * dev.sms, 1, smem, s, w, sc, zr, p);
+    return launch_stream(moe_up_kernel<T, CPG, NT>, dev.dev, kCtasPerSm<W4, NT, true> * dev.sms, 1, smem, s, w, sc, zr, p);
 }
 
 template <class T, int CPG, int NT>

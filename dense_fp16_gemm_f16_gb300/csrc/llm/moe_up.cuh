@@ -59,7 +59,7 @@ struct UpPieces {
 };
 
 template <class T, int CPG, int NT>
-__global__ void __launch_bounds__(kStreamThreads, kCtasPerSm<(CPG != 0), NT>)
+__global__ void __launch_bounds__(kStreamThreads, kCtasPerSm<(CPG != 0), NT, true>)
 moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmS,
               const __grid_constant__ CUtensorMap tmZ, const __grid_constant__ UpParams p) {
     constexpr bool W4 = CPG != 0;
@@ -152,12 +152,12 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
     {
         const int g = lane >> 2, t = lane & 3;
         constexpr int kCols = 8 * NT;
-        const int tile0 = mg * StreamWarp<T, W4, NT>::MT;   // this warp's tiles
+        const int tile0 = mg * StreamWarp<T, W4, NT, true>::MT;   // this warp's tiles
         float* sums = reinterpret_cast<float*>(smem + p.sums_off);
         T* h = static_cast<T*>(p.h);
         for (int d = 0; d < own.depth; ++d)
             if (!fetch_next(own.first + d)) break;
-        StreamWarp<T, W4, NT> sw;
+        StreamWarp<T, W4, NT, true> sw;
         bool ok = true;
         int d = 0, kb = kg;
         uint32_t phase = 0;

@@ -47,7 +47,7 @@ struct RowsParams {
 
 // CPG: 32-k chunks per group of 4-bit weights, 0 for 16-bit weights
 template <class T, int CPG, int NT, bool MOE>
-__global__ void __launch_bounds__(kStreamThreads, kCtasPerSm<(CPG != 0), NT>)
+__global__ void __launch_bounds__(kStreamThreads, kCtasPerSm<(CPG != 0), NT, MOE>)
 weight_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmS,
                    const __grid_constant__ CUtensorMap tmZ, const RowsParams p) {
     constexpr bool W4 = CPG != 0;
@@ -181,10 +181,10 @@ weight_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
 
     {
         const int g = lane >> 2, t = lane & 3;
-        const int tile0 = mg * StreamWarp<T, W4, NT>::MT;               // this warp's tiles
+        const int tile0 = mg * StreamWarp<T, W4, NT, MOE>::MT;               // this warp's tiles
         const int tiles = max(0, ((rows + 15) >> 4) - tile0);
         float* mine = table + kg * table_size;
-        StreamWarp<T, W4, NT> sw;
+        StreamWarp<T, W4, NT, MOE> sw;
         sw.clear();
         int seg = -1, nt = 0, first = 0, n = 0;
         bool ok = true;

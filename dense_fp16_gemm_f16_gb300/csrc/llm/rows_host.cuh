@@ -15,8 +15,8 @@ namespace gemm_gb300 {
 constexpr uint64_t kStreamTimeoutNs = 4000000000ull;
 constexpr int kMaxDynamicSmem = 226 * 1024;   // 227 KB less the barriers
 // dynamic shared memory of a launch, so that kCtasPerSm CTAs fit (1 KB of an SM's goes to each)
-template <bool W4, int NT>
-constexpr int kSmemBudget = kCtasPerSm<W4, NT> == 2 ? kSmemPerSm / 2 - 2048 : 210 * 1024;
+template <bool W4, int NT, bool MOE>
+constexpr int kSmemBudget = kCtasPerSm<W4, NT, MOE> == 2 ? kSmemPerSm / 2 - 2048 : 210 * 1024;
 
 struct SideGroups {
     int groups_k = 0, atom_groups = 0;
@@ -190,8 +190,8 @@ int plan_rows(const void* kernel, RowsParams* p, int tokens, int cols, int typic
 template <bool W4, int NT, bool MOE>
 int plan_rows_anew(const void* kernel, RowsParams* p, int tokens, int cols, int typical_cols, int segments,
                    int atom_groups, int lists, const DeviceView& dev) {
-    constexpr int budget = kSmemBudget<W4, NT>;
-    constexpr int MT = kTilesPerWarp<W4, NT>;
+    constexpr int budget = kSmemBudget<W4, NT, MOE>;
+    constexpr int MT = kTilesPerWarp<W4, NT, MOE>;
     const int table_cols = MOE ? tokens : 8 * NT;
     const int k_atoms = (p->K + kAtomElems<W4> - 1) / kAtomElems<W4>;
     const int nt = std::min(NT, (typical_cols + 7) / 8);
@@ -233,9 +233,9 @@ int plan_rows_anew(const void* kernel, RowsParams* p, int tokens, int cols, int 
                 // another.
                 const int per_warp = (tiles + mw - 1) / mw;
                 const double work = W4 ? 8.0 * (10.0 * nt + per_warp * (22.0 + 6.0 * nt)) : 4.0 * (6.0 * nt + per_warp * (5.0 + 3.0 * nt));
-                const double arith = kCtasPerSm<W4, NT> * (work + 200.0 / atoms) * mw * (0.9 + 0.1 * mw) / 2.0;
-                const double flight = std::min(1.0, c.ring.slots * atoms * width * 128 / (65536.0 / kCtasPerSm<W4, NT>));
-                const double copies = kCtasPerSm<W4, NT> * (width * 128 / 23.5 + typical_cols * (W4 ? 512 : 128) / 50.0) / flight;
+                const double arith = kCtasPerSm<W4, NT, MOE> * (work + 200.0 / atoms) * mw * (0.9 + 0.1 * mw) / 2.0;
+                const double flight = std::min(1.0, c.ring.slots * atoms * width * 128 / (65536.0 / kCtasPerSm<W4, NT, MOE>));
+                const double copies = kCtasPerSm<W4, NT, MOE> * (width * 128 / 23.5 + typical_cols * (W4 ? 512 : 128) / 50.0) / flight;
                 const double latency = (1500.0 + 1500.0 * (mw - 1)) / (kw * atoms) + 2.0 * work / kw;
                 const double n_atoms = std::ceil(std::ceil(static_cast<double>(segments) * c.k_stages / P) / kw) * kw * atoms;
                 const double t = rounds * n_atoms * std::max(std::max(arith, copies), latency) + (P > 1 ? 800.0 : 0.0) + tables / 100.0;

@@ -58,11 +58,13 @@ constexpr int kConsumers = 8;                       // warps
 constexpr int kStreamThreads = 32 * kConsumers;
 // CTAs per SM for NT groups of 8 columns.  With few columns the sums take few
 // registers and two CTAs fit: 16 warps to cover the chains of short latencies,
-// and one CTA's start and end beside the other's middle.  With 4-bit weights and
+// and one CTA's start and end beside the other's middle.  For 4-bit experts with
 // more than 8 columns, registers for 4 tiles a warp and shared memory for the
-// columns (4 times a stage's weights, byte for byte) are worth more.
-template <bool W4, int NT>
-constexpr int kCtasPerSm = NT == 1 || (NT == 2 && !W4) ? 2 : 1;
+// columns (as many bytes per K as 4 times the weights) are worth more; for the
+// plain product, which has exactly its columns, they are not (13 rows of A,
+// 11000 x 4128: 22 us against 24).
+template <bool W4, int NT, bool MOE>
+constexpr int kCtasPerSm = NT == 1 || (NT == 2 && !(W4 && MOE)) ? 2 : 1;
 constexpr int kSmemPerSm = 226 * 1024;              // 228 KB less what the CTAs' static parts take
 
 // arrivals on a slot's full barrier: the byte count, and the columns of every
@@ -79,8 +81,8 @@ constexpr int kAtomElems = W4 ? 256 : 64;
 // columns at a time.  Both pitches spread those over all banks.
 __host__ __device__ constexpr int col_pitch(bool w4, int ka) { return w4 ? ka * 512 + 64 : ka * 128 + 16; }
 // 16-row tiles per warp: the fp32 sums of tiles x columns stay in registers
-template <bool W4, int NT>
-constexpr int kTilesPerWarp = NT == 8 || (W4 && NT == 4) ? 2 : 4;
+template <bool W4, int NT, bool MOE>
+constexpr int kTilesPerWarp = NT == 8 || (W4 && NT == 4) || (W4 && NT == 2 && !MOE) ? 2 : 4;
 
 namespace ptx {
 
@@ -225,9 +227,9 @@ __device__ __forceinline__ void unrolled(F&& f) {
 }
 
 // The consumer's state for one warp: fp32 sums of its tiles.
-template <class T, bool W4, int NT>
+template <class T, bool W4, int NT, bool MOE>
 struct StreamWarp {
-    static constexpr int MT = kTilesPerWarp<W4, NT>;
+    static constexpr int MT = kTilesPerWarp<W4, NT, MOE>;
     float acc[MT][NT][4];
 
     __device__ __forceinline__ void hold() {
