@@ -46,9 +46,9 @@ struct FfnParams {
 };
 
 cudaError_t launch_w4_quantize(bool bf16, const void* W, int64_t batch, int64_t N, int64_t K, int group, void* codes,
-                               void* scales, void* zeros, cudaStream_t s);
+                               void* scales, void* zeros, int sms, cudaStream_t s);
 cudaError_t launch_w4_dequantize(bool bf16, const Weights& w, int64_t batch, int64_t N, int64_t K, void* W,
-                                 cudaStream_t s);
+                                 int sms, cudaStream_t s);
 
 // The product on tcgen05, for more than a few rows of A, and its estimated clocks.
 double w4_tiles_clocks(int64_t M, int64_t N, int64_t K, const DeviceView& dev);

@@ -137,7 +137,7 @@ gemm_status_t quantize(int dtype, const void* W, int64_t batch, int64_t N, int64
     const gemm_status_t st = device_view(&dev);
     if (st != GEMM_OK) return st;
     return from_launch(launch_w4_quantize(dtype == GEMM_DTYPE_BF16, W, batch, N, K, group, codes, scales, zeros,
-                                          reinterpret_cast<cudaStream_t>(stream)));
+                                          dev.sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 gemm_status_t dequantize(int dtype, const gemm_weights_t* weights, int64_t batch, int64_t N, int64_t K, void* W,
@@ -156,7 +156,7 @@ gemm_status_t dequantize(int dtype, const gemm_weights_t* weights, int64_t batch
     st = device_view(&dev);
     if (st != GEMM_OK) return st;
     return from_launch(launch_w4_dequantize(dtype == GEMM_DTYPE_BF16, w, batch, N, K, W,
-                                            reinterpret_cast<cudaStream_t>(stream)));
+                                            dev.sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 gemm_status_t w4_nt(int dtype, const void* A, const gemm_weights_t* B, void* D, int64_t M, int64_t N, int64_t K,
