@@ -10,7 +10,7 @@ namespace {
 
 // The split of one product over tiles and clusters, and its time in clocks.
 struct TileShape {
-    int rows_a, rows_b, m_tiles, n_tiles, split;
+    int rows_a, m_tiles, n_tiles, split;
     double clocks;
 };
 
@@ -18,19 +18,16 @@ struct TileShape {
 // MMAs; then a CTA's start and end, and an exchange between split parts.
 constexpr double kDecodeClocks = 600.0, kMmaClocksPerRow = 3.0, kTileFixedClocks = 9000.0, kTileExchangeClocks = 3000.0;
 
-int tile_code_slot(int rows_b, int atom_groups) { return rows_b * 128 + 2 * up_to(rows_b * atom_groups * 2, 128); }
-
 template <class T, bool PAIRS>
 TileShape tile_shape(int64_t M, int64_t N, int64_t K, const DeviceView& dev) {
     TileShape t{};
-    t.rows_b = PAIRS ? 64 : 128;
     t.m_tiles = static_cast<int>((M + 255) / 256);
     t.rows_a = up_to(static_cast<int>((M + t.m_tiles - 1) / t.m_tiles), 16);
-    t.n_tiles = static_cast<int>((N + t.rows_b - 1) / t.rows_b);
+    t.n_tiles = static_cast<int>((N + kTileRows - 1) / kTileRows);
     const int64_t atoms = (K + 255) / 256, tiles = static_cast<int64_t>(t.m_tiles) * t.n_tiles;
     const double block = std::max(kMmaClocksPerRow * t.rows_a, kDecodeClocks);
     for (int s = 1; s <= 8 && s <= atoms; s *= 2) {
-        const int at_once = active_clusters(reinterpret_cast<const void*>(w4_tiles_kernel<T, PAIRS, 2>), dev, kTileThreads, kMaxDynamicSmem, s);
+        const int at_once = active_clusters(reinterpret_cast<const void*>(w4_tiles_kernel<T, PAIRS, 1>), dev, kTileThreads, kMaxDynamicSmem, s);
         if (at_once < 1) continue;
         const double rounds = static_cast<double>((tiles + at_once - 1) / at_once);
         const double c = rounds * (4.0 * static_cast<double>((atoms + s - 1) / s) * block + kTileFixedClocks) + (s > 1 ? kTileExchangeClocks : 0.0);
@@ -51,7 +48,6 @@ gemm_status_t launch(const void* A, const Weights& w, void* D, int64_t M, int64_
     p.N = static_cast<int32_t>(N);
     p.K = static_cast<int32_t>(K);
     p.rows_a = t.rows_a;
-    p.rows_b = t.rows_b;
     p.m_tiles = t.m_tiles;
     p.split = t.split;
     p.atoms = static_cast<int32_t>((K + 255) / 256);
@@ -59,16 +55,16 @@ gemm_status_t launch(const void* A, const Weights& w, void* D, int64_t M, int64_
     p.group = w.group;
     p.has_zeros = w.zeros != nullptr;
     p.stream_w = stream_weights(true, N, K);
-    p.side_bytes = up_to(t.rows_b * sg.atom_groups * 2, 128);
+    p.side_bytes = kTileRows * sg.atom_groups * 2;
     p.codes_off = kTileStages * KB * t.rows_a * 128;
-    const int code_slot = tile_code_slot(t.rows_b, sg.atom_groups);
+    const int code_slot = kTileRows * 128 + 2 * p.side_bytes;
     p.codes = std::min(kTileCodes, (kMaxDynamicSmem - 1024 - p.codes_off) / code_slot) / 2 * 2;
     if (p.codes < 2) return GEMM_ERR_CUDA;
-    p.side_off = p.codes_off + p.codes * t.rows_b * 128;
+    p.side_off = p.codes_off + p.codes * kTileRows * 128;
     p.end = p.side_off + p.codes * 2 * p.side_bytes;
     // the output's exchange lies over the operands
     const int per = (t.rows_a / 16 + t.split - 1) / t.split * 16;
-    if (PAIRS || t.split > 1) p.end = std::max(p.end, t.split * per * 512);
+    if (t.split > 1) p.end = std::max(p.end, t.split * per * 512);
     // more than half an SM's: a CTA takes all of an SM's TMEM, so it shares none
     const int smem = std::max(p.end + 1024, 116 * 1024);
     if (smem > kMaxDynamicSmem) return GEMM_ERR_CUDA;
@@ -78,7 +74,7 @@ gemm_status_t launch(const void* A, const Weights& w, void* D, int64_t M, int64_
     p.status = dev.status;
     p.timeout_ns = kStreamTimeoutNs;
     CUtensorMap tw, ts, tz, ta;
-    if (!encode_weights(w, N, sg.groups_k, N, K, t.rows_b, t.rows_b, sg.atom_groups, &tw, &ts, &tz) ||
+    if (!encode_weights(w, N, sg.groups_k, N, K, kTileRows, kTileRows, sg.atom_groups, &tw, &ts, &tz) ||
         !encode_map(&ta, A, 2, K, M, 64, static_cast<uint32_t>(t.rows_a), true))
         return GEMM_ERR_INVALID_VALUE;
     const int64_t ctas = static_cast<int64_t>(t.m_tiles) * t.n_tiles * t.split;
@@ -91,7 +87,7 @@ gemm_status_t run(const void* A, const Weights& w, void* D, int64_t M, int64_t N
                   const DeviceView& dev, cudaStream_t s) {
     const TileShape t = M <= 64 ? tile_shape<T, true>(M, N, K, dev) : tile_shape<T, false>(M, N, K, dev);
     if (t.split == 0) return GEMM_ERR_CUDA;
-    if (M <= 64) return launch<T, true, 2>(A, w, D, M, N, K, epi, t, dev, s);
+    if (M <= 64) return launch<T, true, 1>(A, w, D, M, N, K, epi, t, dev, s);
     return t.rows_a <= 128 ? launch<T, false, 2>(A, w, D, M, N, K, epi, t, dev, s) : launch<T, false, 1>(A, w, D, M, N, K, epi, t, dev, s);
 }
 

@@ -7,12 +7,9 @@
 // operand needs (A rows, staged by TMA, K-major, 128-byte swizzle).  TMEM lane
 // = weight row, so a decoding thread owns one row: its codes are 32
 // contiguous bytes per K block of 64, its scale one number per group.
-// The K loop runs in steps of KB blocks of 64 k.  Waiting, fencing and committing
-// cost the issuing thread some 350 clocks a step, as much as the MMAs of a K block
-// with few rows of A, so up to 128 rows a step is two blocks (M = 48, 8192 x 8192:
-// 45 us against 48; with a commit per block for A and one per step for the weights
-// 58).  With more rows the MMAs take longer and shared memory holds four single
-// blocks (M = 512: 52 us; two double ones 60).
+// The K loop runs in steps of KB blocks of 64 k: two up to 128 rows, where the
+// MMAs of one are shorter than what a step costs besides; with more rows shared
+// memory holds four single blocks (M = 512: 46 us; two double ones 60).
 //   warps 0-15  four warpgroups: group g decodes every fourth step, in registers
 //               while the MMAs catch up, then into TMEM (tcgen05.st); later they
 //               read the accumulator out
@@ -20,13 +17,17 @@
 //   warp 18     TMA: codes and scales in atoms of 256 k, as far ahead as their
 //               slots allow (behind the A loads of one producer they came too late:
 //               512 x 8192 x 8192 57 us)
-//   warp 17     issues tcgen05.mma (M = 128, N = A rows, K = 16)
+//   warp 17     issues tcgen05.mma (M = 128, N = A rows, K = 16): the whole warp
+//               walks the loop and one elected lane issues, so that descriptors stay
+//               in uniform registers (from a loop in one thread's branch an MMA took
+//               57 clocks to issue: M = 48, 8192 x 8192 35 us instead of 24)
 // A weight is s * (code - z): code - z and the product each one rounded step in
 // the activations' type (the first exact for whole and half zero points).
 // For M > 64 that product is the operand.  For fewer rows, where the MMA is not
-// what bounds, PAIRS makes the products exact: a CTA takes 64 weight rows, TMEM
-// lanes 0-63 hold the rounded products and lanes 64-127 what the rounding left
-// (one fma), and the two halves of the sum are added at the end.
+// what bounds, PAIRS makes the products exact: what the rounding left (one fma)
+// is a second operand beside the first, and both are multiplied with the same A
+// (with the two parts in lanes 0-63 and 64-127 of one operand every weight was
+// decoded twice: 40 us).
 // Split K.  With fewer tiles than SMs a cluster of S CTAs shares a tile's K
 // loop; the fp32 partial sums meet in distributed shared memory and are added
 // in ascending order, so results are reproducible.
@@ -53,6 +54,7 @@ constexpr int kTileThreads = 32 * (kDecodeWarps + 3);
 // waiters; the code slots are even in number because with KB = 2 a group reads
 // every second atom.
 constexpr int kTileStages = kTileGroups;
+constexpr int kTileRows = 128;          // weight rows per tile, one per TMEM lane
 constexpr int kTileCodes = 8;           // code atoms in flight, at most
 constexpr int kTileTmemCols = 512;      // accumulator: columns 0-255; weights of stage s: 32 KB columns at 256 + 32 KB s
 constexpr uint32_t kSiteTileA = 12, kSiteTileCodes = 13, kSiteTileMma = 14, kSiteTileDone = 15, kSiteTileEmpty = 16;
@@ -61,7 +63,6 @@ struct TileParams {
     int32_t M, N, K;
     int32_t rows_a;          // rows of A per tile: MMA N, a multiple of 16, <= 256
     int32_t codes;           // code atoms in flight
-    int32_t rows_b;          // weight rows per tile: 64 with PAIRS, else 128
     int32_t m_tiles, split;
     int32_t atoms;           // code atoms over K
     int32_t atom_groups;     // 256 / group
@@ -163,6 +164,8 @@ template <class T, bool PAIRS, int KB>
 __global__ void __launch_bounds__(kTileThreads, 1)
 w4_tiles_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmS,
                 const __grid_constant__ CUtensorMap tmZ, const __grid_constant__ CUtensorMap tmA, const TileParams p) {
+    static_assert(!PAIRS || KB == 1, "a stage has 64 columns of TMEM at most");
+    constexpr uint32_t kStageCols = PAIRS ? 64 : 32 * KB;   // PAIRS: the remainders behind the products
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_u32(smem_raw);
     uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -199,7 +202,7 @@ w4_tiles_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     const int j = static_cast<int>(blockIdx.x % S);
     const int64_t tile = blockIdx.x / S;
     const int m0 = static_cast<int>(tile % p.m_tiles) * p.rows_a;
-    const int n0 = static_cast<int>(tile / p.m_tiles) * p.rows_b;
+    const int n0 = static_cast<int>(tile / p.m_tiles) * kTileRows;
     const int at0 = static_cast<int>(static_cast<int64_t>(j) * p.atoms / S);
     const int at1 = static_cast<int>(static_cast<int64_t>(j + 1) * p.atoms / S);
     const int blocks = (min(at1 * 256, p.K) - at0 * 256 + 63) / 64;   // this CTA's K blocks, KB to a step
@@ -243,8 +246,8 @@ w4_tiles_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         // ------------------------------------------------------------ codes and scales (one thread)
         if (lane == 0) {
             const uint64_t pol_w = p.stream_w ? ptx::policy_evict_first() : ptx::policy_evict_normal();
-            const uint32_t tx = static_cast<uint32_t>(p.rows_b) * 128u +
-                                static_cast<uint32_t>(p.rows_b * p.atom_groups * 2) * (p.has_zeros ? 2u : 1u);
+            const uint32_t tx = static_cast<uint32_t>(kTileRows) * 128u +
+                                static_cast<uint32_t>(kTileRows * p.atom_groups * 2) * (p.has_zeros ? 2u : 1u);
             int c = 0;
             uint32_t ph = 1;
             for (int at = at0; at < at1; ++at) {
@@ -254,7 +257,7 @@ w4_tiles_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                 }
                 const uint32_t side = base + static_cast<uint32_t>(p.side_off + c * 2 * p.side_bytes);
                 ptx::mbar_arrive_expect_tx(c_full(c), tx);
-                ptx::tma_load_2d_hint(base + static_cast<uint32_t>(p.codes_off + c * p.rows_b * 128), &tmW, c_full(c), at * 128, n0, pol_w);
+                ptx::tma_load_2d_hint(base + static_cast<uint32_t>(p.codes_off + c * kTileRows * 128), &tmW, c_full(c), at * 128, n0, pol_w);
                 ptx::tma_load_2d(side, &tmS, c_full(c), n0, at * p.atom_groups);
                 if (p.has_zeros) ptx::tma_load_2d(side + static_cast<uint32_t>(p.side_bytes), &tmZ, c_full(c), n0, at * p.atom_groups);
                 if (++c == p.codes) {
@@ -269,18 +272,20 @@ w4_tiles_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         }
         __syncwarp();
     } else if (warp == kDecodeWarps + 1) {
-        // ------------------------------------------------------------ MMA issue (one thread)
-        if (lane == 0) {
-            const uint32_t idesc = ptx::instr_desc(128, p.rows_a, p.ab_format);
-            int s = 0;
-            uint32_t ph = 0;
-            for (int b = 0; b < blocks; b += KB) {
-                if (!wait_phase(full(s), ph, p.status, kSiteTileMma, p.timeout_ns)) {
-                    ok = false;
-                    break;
-                }
-                ptx::tc_fence_after();
-                const uint32_t a = base + KB * s * a_bytes, w = tmem + 256u + 32u * KB * s;
+        // ------------------------------------------------------------ MMA issue
+        // (whole warp, one elected lane issues: with the loop in one thread's branch
+        // the descriptors go through vector registers)
+        const uint32_t idesc = ptx::instr_desc(128, p.rows_a, p.ab_format);
+        int s = 0;
+        uint32_t ph = 0;
+        for (int b = 0; b < blocks; b += KB) {
+            if (!wait_phase_warp(full(s), ph, p.status, kSiteTileMma, p.timeout_ns)) {
+                ok = false;
+                break;
+            }
+            ptx::tc_fence_after();
+            const uint32_t a = base + KB * s * a_bytes, w = tmem + 256u + kStageCols * s;
+            if (ptx::elect_one()) {
 #pragma unroll
                 for (int i = 0; i < KB; ++i) {
                     if (b + i < blocks) {
@@ -288,23 +293,28 @@ w4_tiles_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             ptx::mma_f16_ts(tmem, w + 32u * i + 8u * k, x + 2u * k, idesc, (b != 0 || i != 0 || k != 0) ? 1u : 0u);
+                        if constexpr (PAIRS) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) ptx::mma_f16_ts(tmem, w + 32u + 8u * k, x + 2u * k, idesc, 1u);
+                        }
                     }
                 }
                 ptx::mma_commit(empty(s));
-                if (++s == kTileStages) {
-                    s = 0;
-                    ph ^= 1u;
-                }
             }
-            ptx::mma_commit(done);   // also after a wait that gave up: the MMAs issued so far
-            wait_phase(done, 0, p.status, kSiteTileDone, p.timeout_ns);
+            __syncwarp();
+            if (++s == kTileStages) {
+                s = 0;
+                ph ^= 1u;
+            }
         }
+        // also after a wait that gave up: the MMAs issued so far
+        if (ptx::elect_one()) ptx::mma_commit(done);
         __syncwarp();
+        wait_phase_warp(done, 0, p.status, kSiteTileDone, p.timeout_ns);
     } else {
         // ------------------------------------------------------------ decode
         const int wg = warp >> 2, q = warp & 3;
-        const int l = q * 32 + lane;                        // TMEM lane
-        const int row = PAIRS ? (l & 63) : l;               // weight row within the tile
+        const int row = q * 32 + lane;                      // weight row within the tile, and TMEM lane
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q * 32) << 16);
         const uint32_t mask = ptx::opaque(0x000f000fu), kb = ptx::opaque(Pair<T>::kBase);
         const int g_shift = p.group == 32 ? 5 : (p.group == 64 ? 6 : 7);
@@ -316,7 +326,7 @@ w4_tiles_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                 break;
             }
             const uint32_t there = base + ptx::stage_token();
-            const uint32_t codes = there + static_cast<uint32_t>(p.codes_off + (c * p.rows_b + row) * 128);
+            const uint32_t codes = there + static_cast<uint32_t>(p.codes_off + (c * kTileRows + row) * 128);
             uint32_t w[8 * KB];
 #pragma unroll
             for (int v = 0; v < 2 * KB; ++v) {
@@ -330,7 +340,7 @@ w4_tiles_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
 #pragma unroll
             for (int h = 0; h < 2 * KB; ++h) {
                 const int grp = (part * 64 * KB + h * 32) >> g_shift;
-                const uint32_t at = there + static_cast<uint32_t>(p.side_off + c * 2 * p.side_bytes + (grp * p.rows_b + row) * 2);
+                const uint32_t at = there + static_cast<uint32_t>(p.side_off + c * 2 * p.side_bytes + (grp * kTileRows + row) * 2);
                 sc[h] = ptx::ld_shared_u16<0>(at) * 0x10001u;
                 zr[h] = p.has_zeros ? ((ptx::ld_shared_u16<0>(at + static_cast<uint32_t>(p.side_bytes)) * 0x10001u) ^ 0x80008000u) : 0u;
             }
@@ -345,6 +355,7 @@ w4_tiles_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
             for (int blk = 0; blk < KB; ++blk) {
                 if (KB * t + blk >= blocks) break;
                 uint32_t r[32];
+                [[maybe_unused]] uint32_t rest[PAIRS ? 32 : 1];   // what rounding the products left
 #pragma unroll
                 for (int v = 0; v < 8; ++v) {
                     const uint32_t word = w[8 * blk + v], odd = word >> 4, sv = sc[2 * blk + (v >> 2)];
@@ -357,8 +368,8 @@ w4_tiles_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                         if (p.has_zeros) d = Pair<T>::add(Pair<T>::add(d, Pair<T>::kMinusBase), zr[2 * blk + (v >> 2)]);
                         else d = Pair<T>::add(d, Pair<T>::kMinusBase8);
                         const uint32_t prod = Pair<T>::mul(d, sv);
-                        if (PAIRS && q >= 2) r[4 * v + u] = Pair<T>::fma(d, sv, Pair<T>::neg(prod));
-                        else r[4 * v + u] = prod;
+                        r[4 * v + u] = prod;
+                        if constexpr (PAIRS) rest[4 * v + u] = Pair<T>::fma(d, sv, Pair<T>::neg(prod));
                     }
                 }
                 if (blk == 0) {
@@ -368,7 +379,9 @@ w4_tiles_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                     }
                     ptx::tc_fence_after();
                 }
-                ptx::tmem_st_x32(lane_addr + 256u + 32u * (KB * s + blk), r);
+                const uint32_t to = lane_addr + 256u + kStageCols * s + 32u * blk;
+                ptx::tmem_st_x32(to, r);
+                if constexpr (PAIRS) ptx::tmem_st_x32(to + 32u, rest);
             }
             if (!ok) break;
             ptx::tmem_wait_st();
@@ -381,14 +394,13 @@ w4_tiles_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     // ---------------------------------------------------------------- output
     T* D = static_cast<T*>(p.D);
     const int cols = p.rows_a;
-    const bool through_smem = PAIRS || S > 1;
     if (warp < kDecodeWarps) {
         if (!wait_phase_warp(done, 0, p.status, kSiteTileDone, p.timeout_ns)) ok = false;
         ptx::tc_fence_after();
     }
     const int wg = warp >> 2, q = warp & 3, l = q * 32 + lane;
     const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16);
-    if (!through_smem) {
+    if (S == 1) {
         if (warp < kDecodeWarps) {
             const int64_t n = n0 + l;
             const bool in = n < p.N;
@@ -418,7 +430,7 @@ w4_tiles_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         // [S][per / 4][128 lanes][4 columns].
         const int per = (cols / 16 + S - 1) / S * 16;
         __syncwarp();
-        if (S > 1) ptx::cluster_sync(); else __syncthreads();   // every MMA and copy of the cluster is done
+        ptx::cluster_sync();   // every MMA and copy of the cluster is done
         if (warp < kDecodeWarps) {
             for (int c0 = wg * 16; c0 < cols; c0 += 16 * kTileGroups) {
                 uint32_t v[16];
@@ -431,11 +443,10 @@ w4_tiles_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                 for (int i = 0; i < 16; i += 4) ptx::st_cluster_v4(peer + static_cast<uint32_t>(i * 512), v[i], v[i + 1], v[i + 2], v[i + 3]);
             }
         }
-        if (S > 1) ptx::cluster_sync(); else __syncthreads();
-        const int rows = p.rows_b;
+        ptx::cluster_sync();
         const int mine = min(per, cols - j * per);
-        for (int e = threadIdx.x; e < (mine >> 2) * rows; e += kTileThreads) {
-            const int c = e / rows * 4, r = e - (c >> 2) * rows;
+        for (int e = threadIdx.x; e < (mine >> 2) * kTileRows; e += kTileThreads) {
+            const int c = e / kTileRows * 4, r = e % kTileRows;
             const int64_t m = m0 + j * per + c, n = n0 + r;
             if (n >= p.N) continue;
             float x[4] = {};
@@ -445,11 +456,6 @@ w4_tiles_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                 ptx::ld_shared_v4(at, t);
 #pragma unroll
                 for (int q2 = 0; q2 < 4; ++q2) x[q2] += t[q2];
-                if constexpr (PAIRS) {
-                    ptx::ld_shared_v4(at + 64u * 16u, t);
-#pragma unroll
-                    for (int q2 = 0; q2 < 4; ++q2) x[q2] += t[q2];
-                }
             }
 #pragma unroll
             for (int q2 = 0; q2 < 4; ++q2) {
