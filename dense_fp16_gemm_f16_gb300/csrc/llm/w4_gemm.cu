@@ -54,9 +54,13 @@ gemm_status_t by_group(const void* A, const Weights& w, void* D, int64_t M, int6
     return run<T, 4>(A, w, D, M, N, K, epi, dev, s);
 }
 
-// Clocks of the streaming kernel for 17 to 64 rows of A, in passes of up to 32.
+// Clocks of the streaming kernel for 17 to 64 rows of A, in passes of up to 32,
+// fitted to measured times.  Against the tiles of w4_tiles.cuh (us): 8192 x 8192,
+// 17 rows 29.5 / 22.5, 48 rows 69 / 24; 2048 x 8192, 17 rows 10.9 / 13.2, 48 rows
+// 24.6 / 13.6; 1024 x 4096, 17 rows 7.0 / 7.3, 32 rows 8.3 / 7.3.
 double rows_clocks(int64_t M, int64_t N, int64_t K) {
-    return static_cast<double>((M + 31) / 32) * (9000.0 + static_cast<double>(N) * static_cast<double>(K) / 1100.0);
+    const double passes = static_cast<double>((M + 31) / 32), weights = static_cast<double>(N) * static_cast<double>(K);
+    return passes * 10500.0 + weights * (4.4e-4 * passes + 1.5e-5 * static_cast<double>(M));
 }
 
 }  // namespace

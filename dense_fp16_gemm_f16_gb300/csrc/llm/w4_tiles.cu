@@ -14,9 +14,11 @@ struct TileShape {
     double clocks;
 };
 
-// Clocks of a K block of 64: what decoding and handing it over takes, or its
-// MMAs; then a CTA's start and end, and an exchange between split parts.
-constexpr double kDecodeClocks = 600.0, kMmaClocksPerRow = 3.0, kTileFixedClocks = 9000.0, kTileExchangeClocks = 3000.0;
+// Clocks of a K block of 64, fitted to measured times: what decoding and handing
+// it over takes (with and without remainders), or its MMAs; then a CTA's start and
+// end, and an exchange between split parts.
+constexpr double kPairClocks = 520.0, kDecodeClocks = 400.0, kMmaClocksPerRow = 2.1;
+constexpr double kTileFixedClocks = 8000.0, kTileExchangeClocks = 2000.0;
 
 template <class T, bool PAIRS>
 TileShape tile_shape(int64_t M, int64_t N, int64_t K, const DeviceView& dev) {
@@ -25,7 +27,7 @@ TileShape tile_shape(int64_t M, int64_t N, int64_t K, const DeviceView& dev) {
     t.rows_a = up_to(static_cast<int>((M + t.m_tiles - 1) / t.m_tiles), 16);
     t.n_tiles = static_cast<int>((N + kTileRows - 1) / kTileRows);
     const int64_t atoms = (K + 255) / 256, tiles = static_cast<int64_t>(t.m_tiles) * t.n_tiles;
-    const double block = std::max(kMmaClocksPerRow * t.rows_a, kDecodeClocks);
+    const double block = std::max(kMmaClocksPerRow * t.rows_a, PAIRS ? kPairClocks : kDecodeClocks);
     for (int s = 1; s <= 8 && s <= atoms; s *= 2) {
         const int at_once = active_clusters(reinterpret_cast<const void*>(w4_tiles_kernel<T, PAIRS, 1>), dev, kTileThreads, kMaxDynamicSmem, s);
         if (at_once < 1) continue;
