@@ -196,6 +196,7 @@ int plan_rows_anew(const void* kernel, RowsParams* p, int tokens, int cols, int 
     const int k_atoms = (p->K + kAtomElems<W4> - 1) / kAtomElems<W4>;
     const int nt = std::min(NT, (typical_cols + 7) / 8);
     int best = 0;
+    bool best_fits = false;
     double best_t = 0.0;
     RowsParams got = *p;
     for (int P = 1; P <= 8; P *= 2) {
@@ -223,7 +224,9 @@ int plan_rows_anew(const void* kernel, RowsParams* p, int tokens, int cols, int 
                 const int recv = P > 1 ? up_to((tokens * width + P - 1) / P * P * 4, 128) : 0;
                 const int fixed = lists + tables + recv + 1024;
                 c.ring = ring_layout(W4, atoms, width, width, atom_groups, cols, budget - fixed, kw);
-                if (c.ring.end + fixed > (best == 0 ? kMaxDynamicSmem : budget)) continue;
+                // more than the budget (fewer CTAs per SM than planned) only where nothing fits it
+                const bool fits = c.ring.end + fixed <= budget;
+                if (c.ring.end + fixed > kMaxDynamicSmem || (best != 0 && best_fits && !fits)) continue;
                 // Clocks per atom.  Arithmetic: a warp's instructions for its
                 // columns and tiles, about one per clock and SM.  Copies: the
                 // CTA's share of HBM for the weights and of L2 for the columns,
@@ -239,8 +242,9 @@ int plan_rows_anew(const void* kernel, RowsParams* p, int tokens, int cols, int 
                 const double latency = (1500.0 + 1500.0 * (mw - 1)) / (kw * atoms) + 2.0 * work / kw;
                 const double n_atoms = std::ceil(std::ceil(static_cast<double>(segments) * c.k_stages / P) / kw) * kw * atoms;
                 const double t = rounds * n_atoms * std::max(std::max(arith, copies), latency) + (P > 1 ? 800.0 : 0.0) + tables / 100.0;
-                if (best == 0 || t < best_t) {
+                if (best == 0 || t < best_t || (fits && !best_fits)) {
                     best_t = t;
+                    best_fits = fits;
                     c.list_off = c.ring.end;
                     c.table_off = c.list_off + lists;
                     c.recv_off = c.table_off + tables;
