@@ -4,9 +4,9 @@
 
 #include <algorithm>
 #include <cmath>
+#include <functional>
 #include <map>
 #include <mutex>
-#include <tuple>
 
 #include "llm/rows.cuh"
 
@@ -56,12 +56,25 @@ inline bool encode_weights_box(const Weights& w, int64_t rows, int64_t K, int bo
                                : encode_map(t, w.data, 1, K / 2, rows, 128, static_cast<uint32_t>(box_rows), true);
 }
 
+// What the facts about a kernel's launches are known by.  A type of this
+// namespace also keeps the maps' symbols out of the library's exports.
+struct LaunchKey {
+    const void* kernel;
+    int dev, smem, cluster;
+    bool operator<(const LaunchKey& o) const {
+        if (kernel != o.kernel) return std::less<const void*>()(kernel, o.kernel);
+        if (dev != o.dev) return dev < o.dev;
+        if (smem != o.smem) return smem < o.smem;
+        return cluster < o.cluster;
+    }
+};
+
 // Lifts a kernel's shared-memory limit, once per kernel and device.
 inline cudaError_t allow_smem(const void* kernel, int dev) {
     static std::mutex mu;
-    static std::map<std::pair<const void*, int>, bool> done;
+    static std::map<LaunchKey, bool> done;
     std::lock_guard<std::mutex> lock(mu);
-    bool& ready = done[std::make_pair(kernel, dev)];
+    bool& ready = done[LaunchKey{kernel, dev, 0, 0}];
     if (ready) return cudaSuccess;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicSmem);
     ready = e == cudaSuccess;
@@ -71,9 +84,9 @@ inline cudaError_t allow_smem(const void* kernel, int dev) {
 // Clusters of `cluster` CTAs that run at one time (0: none), looked up once.
 inline int active_clusters(const void* kernel, const DeviceView& dev, int threads, int smem, int cluster) {
     static std::mutex mu;
-    static std::map<std::tuple<const void*, int, int, int>, int> known;
+    static std::map<LaunchKey, int> known;
     std::lock_guard<std::mutex> lock(mu);
-    const auto key = std::make_tuple(kernel, dev.dev, smem, cluster);
+    const LaunchKey key{kernel, dev.dev, smem, cluster};
     const auto it = known.find(key);
     if (it != known.end()) return it->second;
     int n = 0;
