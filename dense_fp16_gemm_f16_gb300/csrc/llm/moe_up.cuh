@@ -12,6 +12,10 @@
 // type, rows 2 s and 2 s + 1 for slot s: one rounding to 16 bits here would cost
 // as much accuracy as the output's own, and two columns instead of one are
 // nearly free where weights set the pace.
+// Measured: 8 experts of 2 x 8200 x 4096 in 16 bits (1.07 GB), 16 tokens: 167 us,
+// 6.4 TB/s, bound by HBM.  64 experts of 2 x 1408 x 2048 in 4 bits (185 MB), 64
+// tokens: 96 us, bound by the eight warps' chains from codes to sums (1.5 of 4
+// instructions per clock; 16 warps with half the registers: 107 us).
 #pragma once
 
 #include "llm/lists.cuh"
@@ -122,7 +126,7 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 if (q >= 0 && q < (p.has_zeros ? 4 : 2))
                     ptx::tma_load_2d(base + static_cast<uint32_t>(p.ring.side_off + s * p.ring.side_bytes + (q >> 1) * (p.ring.side_bytes / 2)) + (q & 1) * side_half,
                                      (q >> 1) ? &tmZ : &tmS, full_bar(s), at * 8 + ((q & 1) ? p.I : 0), e * p.groups_k + kb * p.atom_groups);
-        }
+            }
         }
         if (p.x_resident) return;
         const uint32_t x = base + static_cast<uint32_t>(p.ring.x_off + s * p.ring.x_bytes);

@@ -62,7 +62,7 @@ constexpr int kStreamThreads = 32 * kConsumers;
 // more than 8 columns, registers for 4 tiles a warp and shared memory for the
 // columns (as many bytes per K as 4 times the weights) are worth more; for the
 // plain product, which has exactly its columns, they are not (13 rows of A,
-// 11000 x 4128: 22 us against 24).
+// 11000 x 4128: 21 us against 24).
 template <bool W4, int NT, bool MOE>
 constexpr int kCtasPerSm = NT == 1 || (NT == 2 && !(W4 && MOE)) ? 2 : 1;
 constexpr int kSmemPerSm = 226 * 1024;              // 228 KB less what the CTAs' static parts take

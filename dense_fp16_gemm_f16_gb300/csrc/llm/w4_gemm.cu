@@ -1,4 +1,5 @@
-// w4_gemm.cu -- D = A·Bᵀ with the weights B in 4 bits (rows.cuh).
+// w4_gemm.cu -- D = A·Bᵀ with the weights B in 4 bits: few rows of A stream the
+// weights (rows.cuh), more go to the tensor cores (w4_tiles.cuh).
 #include <algorithm>
 
 #include "llm/rows.cuh"

@@ -283,7 +283,10 @@ def gemm_moe_ffn(X, ids, weights, W13, W2, Y, stream=None) -> None:
         raise ValueError("X must be [T, H] and ids [T, k]")
     T, H = X.shape
     k = ids.shape[1]
-    E = (W13.codes if isinstance(W13, W4) else W13).shape[0]
+    rows = W13.codes if isinstance(W13, W4) else W13
+    if not _g._is_tensor(rows) or rows.dim() != 3:
+        raise ValueError(f"W13 must be [E, 2 I, {H}]")
+    E = rows.shape[0]
     w13, w2, I = _experts(W13, W2, X.dtype, H, E, index)
     _run(lib.gemm_moe_ffn, index, stream,
          (dt, X.data_ptr(), _check(ids, "ids", _torch.int32, (T, k), index),

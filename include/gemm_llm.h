@@ -75,8 +75,16 @@ GEMM_API gemm_status_t gemm_w4_dequantize(gemm_dtype_t dtype, const gemm_weights
  * output transform of gemm_nt_ex (NULL: none).
  *   A [M][K], D [M][N] in dtype; N a multiple of 8, K of B's group.
  * M == 0 or N == 0 is a no-op; K == 0 gives act(beta * C + bias).
- * Up to M = 64 products are exact and summed in fp32 group by group; for
- * larger M each weight is rounded to dtype before it is multiplied.
+ * Precision; sums are fp32 throughout.
+ *   M <= 16: the products of codes and A are exact, scales and zero points
+ *     are applied to each group's sum in fp32.
+ *   17 <= M <= 64: as above, or, for larger N and K, code - zero rounded to dtype
+ *     (exact for whole and half zero points) and its product with the scale kept
+ *     as two numbers of dtype, exact but for what lies below dtype's smallest
+ *     number.  There a weight beyond dtype's largest number, or an infinity in
+ *     A, can give NaN where the sum would be infinite.
+ *   M > 64: code - zero, and its product with the scale, each rounded to dtype,
+ *     like the matrix that gemm_w4_dequantize writes but for one rounding.
  */
 GEMM_API gemm_status_t gemm_w4_nt(gemm_dtype_t dtype, const void* A, const gemm_weights_t* B, void* D, int64_t M,
                                   int64_t N, int64_t K, const gemm_epilogue_t* epilogue, gemm_stream_t stream);
