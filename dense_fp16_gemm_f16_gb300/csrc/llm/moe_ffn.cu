@@ -63,7 +63,7 @@ gemm_status_t launch_up(const FfnParams& f, void* h, const DeviceView& dev, cuda
     if (!encode_weights(f.w13, rows, static_cast<int64_t>(f.E) * sg.groups_k, 2 * f.I, f.H, 8, kUpGranules * 8, sg.atom_groups, &w, &sc, &zr) ||
         !encode_weights_box(f.w13, rows, f.H, 8 * kUpGranules, &p.tm_piece))
         return GEMM_ERR_INVALID_VALUE;
-    return launch_stream(moe_up_kernel<T, CPG, NT>, dev.dev, kCtasPerSm<W4, NT, true> * dev.sms, 1, smem, s, w, sc, zr, p);
+    return launch_stream(moe_up_kernel<T, CPG, NT>, dev.dev, kCtasPerSm<W4, NT, true> * dev.sms, 1, smem, true, s, w, sc, zr, p);
 }
 
 template <class T, int CPG, int NT>
@@ -93,32 +93,64 @@ gemm_status_t launch_down(const FfnParams& f, const void* h, const DeviceView& d
     CUtensorMap w, sc, zr;
     if (!encode_weights(f.w2, rows, static_cast<int64_t>(f.E) * sg.groups_k, f.H, f.I, p.width, p.width, p.ring.atoms * sg.atom_groups, &w, &sc, &zr))
         return GEMM_ERR_INVALID_VALUE;
-    return launch_stream(weight_rows_kernel<T, CPG, NT, true>, dev.dev, p.ranges * p.pieces, p.pieces, smem, s, w, sc, zr, p);
+    // Clusters of 8 that start while the CTAs of the first product end here and there
+    // are placed so that some are left for a second round: 64 tokens, 2 of 64
+    // experts of 2048 x 1408 in 4 bits 184 us, 134 if they wait for its end.  The
+    // smaller clusters gain 1 to 3 us by starting early.
+    return launch_stream(weight_rows_kernel<T, CPG, NT, true>, dev.dev, p.ranges * p.pieces, p.pieces, smem, p.pieces < 8, s, w, sc, zr, p);
 }
 
-// Columns a segment may have: twice what an expert gets when the choices are
-// even (an expert with more has its weights read again, mostly from L2), at most
-// 64 for 16-bit weights and 32 for 4-bit ones, whose group sums take registers
-// too.  Narrow kernels keep more tiles per warp and two CTAs per SM.
-int segment_slots(const FfnParams& f) { return std::min(f.T, 2 * typical_slots(f)); }
+// How many columns a kernel is built for (8 NT).  An expert with more slots than
+// that has its weights read again for the rest; few columns leave registers for
+// more tiles per warp or for two CTAs per SM, and shared memory for weights in
+// flight.  Matrices of up to kResident bytes are still in L2 when they are read again,
+// so for them the narrow kernels win well past the slots that an expert
+// usually gets.  Measured, E experts of H x I, T tokens with k choices (us):
+//   first product, 16 bits: 64 of 2048 x 1024, T = 64, k = 6: 8 columns 184, 16
+//     columns 202; k = 8: 226, 222.  8 of 4096 x 8200, k = 2, T = 16: 265, 275;
+//     T = 32: 390, 338; T = 64: 16 columns 550, 32 columns 564.
+//   first product, 4 bits: 64 of 2048 x 1408, k = 8, T = 4: 8 columns 56, 16 columns
+//     65; T = 8: 107, 85; T = 16: 147, 117; T = 64: 16 columns 206, 32 columns 397.
+//     16 of them, T = 64, k = 4: 128, 98, 32 columns 164.
+//   second product (two columns per slot), 16 bits: 64 of 2048 x 1024, T = 64, k = 6: 8
+//     columns 198, 16 columns 184, 32 columns 218; 8 of them, k = 4: 110, 98, 103, 64
+//     columns 126.  8 of 4096 x 8200, k = 2, T = 16: 290, 265; T = 64: 16 columns
+//     608, 32 columns 575, 64 columns 551.
+//   second product, 4 bits: 64 of 2048 x 1408, k = 8, T = 32: 8 columns 147, 16
+//     columns 165, 32 columns 171; T = 64: 246, 240, 206.
+constexpr int64_t kResident = 24ll << 20;
+
+bool resident(const Weights& w, int64_t rows, int64_t K) { return (w.scales != nullptr ? rows * K / 2 : rows * K * 2) <= kResident; }
+
+int up_columns(const FfnParams& f) {
+    const int usual = typical_slots(f);
+    if (f.w13.scales != nullptr) return f.T <= 4 || f.T * f.k <= 16 ? 8 : 16;
+    return std::min(f.T, resident(f.w13, 2ll * f.I, f.H) ? (usual <= 6 ? 8 : 16) : usual <= 4 ? 8 : usual <= 16 ? 16 : 32);
+}
+
+int down_columns(const FfnParams& f) {
+    const int usual = typical_slots(f);
+    const bool small = resident(f.w2, f.H, f.I);
+    if (f.w2.scales != nullptr) return std::min(2 * f.T, usual <= (small ? 4 : 2) ? 8 : 32);
+    return std::min(2 * f.T, small ? (usual <= 2 ? 8 : 16) : 4 * usual);
+}
 
 template <class T, int CPG>
 gemm_status_t up(const FfnParams& f, void* h, const DeviceView& dev, cudaStream_t s) {
-    const int cols = segment_slots(f);
+    const int cols = up_columns(f);
     if (cols <= 8) return launch_up<T, CPG, 1>(f, h, dev, s);
-    if (cols <= 16) return launch_up<T, CPG, 2>(f, h, dev, s);
     if constexpr (CPG == 0) {
-        if (cols > 32) return launch_up<T, CPG, 8>(f, h, dev, s);
+        if (cols > 16) return launch_up<T, CPG, 4>(f, h, dev, s);
     }
-    return launch_up<T, CPG, 4>(f, h, dev, s);
+    return launch_up<T, CPG, 2>(f, h, dev, s);
 }
 
 template <class T, int CPG>
 gemm_status_t down(const FfnParams& f, const void* h, const DeviceView& dev, cudaStream_t s) {
-    const int cols = 2 * segment_slots(f);
+    const int cols = down_columns(f);
     if (cols <= 8) return launch_down<T, CPG, 1>(f, h, dev, s);
-    if (cols <= 16) return launch_down<T, CPG, 2>(f, h, dev, s);
     if constexpr (CPG == 0) {
+        if (cols <= 16) return launch_down<T, CPG, 2>(f, h, dev, s);
         if (cols > 32) return launch_down<T, CPG, 8>(f, h, dev, s);
     }
     return launch_down<T, CPG, 4>(f, h, dev, s);

@@ -111,10 +111,10 @@ inline int active_clusters(const void* kernel, const DeviceView& dev, int thread
     return n;
 }
 
-// Programmatic stream serialisation, and clusters of `cluster` CTAs.
+// Programmatic stream serialisation (where `early`), and clusters of `cluster` CTAs.
 template <class Kernel, class... Args>
-gemm_status_t launch_clusters(Kernel kernel, int dev, int grid, int threads, int cluster, int smem, cudaStream_t s,
-                              const Args&... args) {
+gemm_status_t launch_clusters(Kernel kernel, int dev, int grid, int threads, int cluster, int smem, bool early,
+                              cudaStream_t s, const Args&... args) {
     if (allow_smem(reinterpret_cast<const void*>(kernel), dev) != cudaSuccess) {
         cudaGetLastError();
         return GEMM_ERR_CUDA;
@@ -126,7 +126,7 @@ gemm_status_t launch_clusters(Kernel kernel, int dev, int grid, int threads, int
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[0].val.programmaticStreamSerializationAllowed = early ? 1 : 0;
     cfg.numAttrs = 1;
     if (cluster > 1) {
         attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -144,9 +144,9 @@ gemm_status_t launch_clusters(Kernel kernel, int dev, int grid, int threads, int
 }
 
 template <class Kernel, class Params>
-gemm_status_t launch_stream(Kernel kernel, int dev, int grid, int cluster, int smem, cudaStream_t s, const CUtensorMap& w,
-                            const CUtensorMap& sc, const CUtensorMap& zr, const Params& p) {
-    return launch_clusters(kernel, dev, grid, kStreamThreads, cluster, smem, s, w, sc, zr, p);
+gemm_status_t launch_stream(Kernel kernel, int dev, int grid, int cluster, int smem, bool early, cudaStream_t s,
+                            const CUtensorMap& w, const CUtensorMap& sc, const CUtensorMap& zr, const Params& p) {
+    return launch_clusters(kernel, dev, grid, kStreamThreads, cluster, smem, early, s, w, sc, zr, p);
 }
 
 // What plan_rows decides from, and the decision.  A thread keeps its last few: a

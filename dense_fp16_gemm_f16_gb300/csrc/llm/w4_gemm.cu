@@ -30,7 +30,7 @@ gemm_status_t launch(const void* A, const Weights& w, void* D, int64_t row0, int
     p.timeout_ns = kStreamTimeoutNs;
     CUtensorMap tw, ts, tz;
     if (!encode_weights(w, N, sg.groups_k, N, K, p.width, p.width, p.ring.atoms * sg.atom_groups, &tw, &ts, &tz)) return GEMM_ERR_INVALID_VALUE;
-    return launch_stream(weight_rows_kernel<T, CPG, NT, false>, dev.dev, p.ranges * p.pieces, p.pieces, smem, s, tw, ts, tz, p);
+    return launch_stream(weight_rows_kernel<T, CPG, NT, false>, dev.dev, p.ranges * p.pieces, p.pieces, smem, true, s, tw, ts, tz, p);
 }
 
 template <class T, int CPG>

@@ -81,7 +81,7 @@ gemm_status_t launch(const void* A, const Weights& w, void* D, int64_t M, int64_
         return GEMM_ERR_INVALID_VALUE;
     const int64_t ctas = static_cast<int64_t>(t.m_tiles) * t.n_tiles * t.split;
     if (ctas > INT32_MAX) return GEMM_ERR_INVALID_VALUE;
-    return launch_clusters(w4_tiles_kernel<T, PAIRS, KB>, dev.dev, static_cast<int>(ctas), kTileThreads, t.split, smem, s, tw, ts, tz, ta, p);
+    return launch_clusters(w4_tiles_kernel<T, PAIRS, KB>, dev.dev, static_cast<int>(ctas), kTileThreads, t.split, smem, true, s, tw, ts, tz, ta, p);
 }
 
 template <class T>
