@@ -304,10 +304,13 @@ struct StreamWarp {
         constexpr float kOffset = kF16 ? 0.0f : 128.0f;
         // what a code of 1 counts in the even and in the odd places
         constexpr float kUnit = kF16 ? 16777216.0f : 1.0f, kUnitOdd = kF16 ? 1048576.0f : 1.0f;
-        // Groups of one chunk: even and odd places added up in one chain of MMAs, at
-        // the cost of shifts for fp16, leave a third less to do to the sums
-        // (13 rows of A, 11000 x 4128, groups of 32: 21.5 -> 20.7 us).
-        constexpr bool kMerge = CPG == 1 && NT >= 2;
+        // Even and odd places added up in one chain of MMAs leave a third less to do to
+        // the sums.  It costs fp16 its saved shifts, so there only groups of one chunk do
+        // it (13 rows of A, 11000 x 4128, groups of 32: 21.5 -> 20.7 us); bf16 does in the
+        // plain product (16 rows, 8192 x 8192, groups of 128: 21.1 -> 20.2 us).  Experts
+        // often have 8 columns or fewer in use, and then the longer chain is what counts
+        // (16 tokens, 8 of 64 experts, groups of 128: 123 us, merged 126).
+        constexpr bool kMerge = NT >= 2 && (CPG == 1 || (!kF16 && !MOE));
         constexpr uint32_t kOne = kF16 ? 0x3C003C00u : 0x3F803F80u;
         const uint32_t ones[4] = {kOne, kOne, kOne, kOne};
         const uint32_t mask = ptx::opaque(0x000f000fu), offset = ptx::opaque(0x43004300u);
@@ -394,7 +397,8 @@ struct StreamWarp {
                         for (int n = 0; n < NT; ++n) {
                             if (n == 0 || n < nt) {
                                 if constexpr (kMerge) {
-                                    ptx::mma16816_first<T>(p[n], even, b[c][n][0], b[c][n][1]);
+                                    if (c == 0) ptx::mma16816_first<T>(p[n], even, b[c][n][0], b[c][n][1]);
+                                    else ptx::mma16816<T>(p[n], even, b[c][n][0], b[c][n][1]);
                                     ptx::mma16816<T>(p[n], odd, b[c][n][2], b[c][n][3]);
                                 } else if (c == 0) {
                                     ptx::mma16816_first<T>(p[n], even, b[c][n][0], b[c][n][1]);
