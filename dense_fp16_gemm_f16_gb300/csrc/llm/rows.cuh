@@ -14,7 +14,7 @@
 // ever add to one number.  At the end the tables are added in a fixed order,
 // across the cluster through distributed shared memory, and each output is
 // rounded once.  Results are bitwise reproducible.
-// Measured: 8192 x 8192 4-bit weights (34.6 MB), M = 1 12.5 us, M = 8 13 us, M = 13
+// Measured: 8192 x 8192 4-bit weights (34.6 MB), M = 1 12.5 us, M = 8 13 us, M = 16
 // 20 us; 11000 x 4128 with zero points in groups of 32, M = 13 21 us, of which the
 // warps' instructions for decoding and scaling (2.2 of 4 issued per clock) are most;
 // 2 of 8 experts of 4096 x 8200 per token, 16 tokens (all 8 read, 537 MB): 105 us,
