@@ -73,6 +73,8 @@ std::mutex g_mu;
 std::map<int, DeviceState> g_devices;
 std::map<std::pair<int, void*>, Workspace> g_workspaces;
 EncodeTiledFn g_encode = nullptr;
+typedef CUresult (*CtxGetCurrentFn)(CUcontext*);
+CtxGetCurrentFn g_ctx_current = nullptr;
 
 constexpr int64_t kMaxDim = INT32_MAX;
 // Raster groups hold as many tile rows as keep the group's A rows (tile rows x
@@ -517,7 +519,14 @@ gemm_status_t get_device(DeviceState** out, int* dev_out) {
                 cudaGetLastError();
                 return GEMM_ERR_CUDA;
             }
-            g_encode = reinterpret_cast<EncodeTiledFn>(fn);
+            EncodeTiledFn encode = reinterpret_cast<EncodeTiledFn>(fn);
+            if (cudaGetDriverEntryPointByVersion("cuCtxGetCurrent", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+                q != cudaDriverEntryPointSuccess || fn == nullptr) {
+                cudaGetLastError();
+                return GEMM_ERR_CUDA;
+            }
+            g_ctx_current = reinterpret_cast<CtxGetCurrentFn>(fn);
+            g_encode = encode;
         }
         void* status = nullptr;
         if (cudaGetSymbolAddress(&status, g_status_word) != cudaSuccess) {
@@ -572,6 +581,13 @@ gemm_status_t get_device(DeviceState** out, int* dev_out) {
             }
         }
         d.ready = true;
+    }
+    // A thread that has made no CUDA call yet has no current context, and encoding
+    // a tensor map needs one but does not bring it.
+    CUcontext context = nullptr;
+    if (g_ctx_current(&context) != CUDA_SUCCESS || (context == nullptr && cudaSetDevice(dev) != cudaSuccess)) {
+        cudaGetLastError();
+        return GEMM_ERR_CUDA;
     }
     *out = &d;
     if (dev_out) *dev_out = dev;
