@@ -7,6 +7,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <mutex>
 
 #include "epilogue.cuh"
 #include "gemm_f16.h"
@@ -40,10 +41,20 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 
 // `bytes` of scratch for (device, stream), 256-byte aligned, and its counters:
 // kScratchCounters zeros that every kernel using them leaves at zero (llm/llm_api.cu).
+// The kernels of one call pass values to one another through it, so a Scratch keeps
+// other threads' calls on the pair waiting for as long as it lives: until the call's
+// last launch.
 constexpr int kScratchCounters = 1024;
 struct Scratch {
-    uint8_t* data;
-    uint32_t* counters;
+    uint8_t* data = nullptr;
+    uint32_t* counters = nullptr;
+    std::mutex* held = nullptr;
+    Scratch() = default;
+    Scratch(const Scratch&) = delete;
+    Scratch& operator=(const Scratch&) = delete;
+    ~Scratch() {
+        if (held != nullptr) held->unlock();
+    }
 };
 gemm_status_t get_scratch(int dev, gemm_stream_t stream, size_t bytes, Scratch* out);
 

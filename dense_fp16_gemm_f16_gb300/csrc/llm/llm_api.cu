@@ -16,6 +16,7 @@ namespace gemm_gb300 {
 
 namespace {
 struct StreamScratch {
+    std::mutex mu;   // held by the call whose launches use the buffer
     uint8_t* data = nullptr;
     size_t bytes = 0;
     uint32_t* counters = nullptr;
@@ -28,8 +29,14 @@ std::map<std::pair<int, void*>, StreamScratch> g_scratch;
 // or a captured graph, may still use it.  Buffers at least double, so the ones
 // left behind hold less than the one in use.
 gemm_status_t get_scratch(int dev, gemm_stream_t stream, size_t bytes, Scratch* out) {
-    std::lock_guard<std::mutex> lock(g_scratch_mu);
-    StreamScratch& w = g_scratch[std::make_pair(dev, static_cast<void*>(stream))];
+    StreamScratch* found = nullptr;
+    {
+        std::lock_guard<std::mutex> lock(g_scratch_mu);
+        found = &g_scratch[std::make_pair(dev, static_cast<void*>(stream))];   // stays where it is
+    }
+    StreamScratch& w = *found;
+    w.mu.lock();
+    out->held = &w.mu;
     if (w.counters == nullptr) {
         uint32_t* c = nullptr;
         if (cudaMalloc(&c, kScratchCounters * sizeof(uint32_t)) != cudaSuccess) {

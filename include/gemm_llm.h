@@ -14,7 +14,8 @@
  * allocates it with cudaMalloc; a larger problem gets a new buffer of at least
  * twice the size.  Buffers are kept until the process exits, so a captured
  * graph never outlives the one it was recorded with.  Calls on one stream
- * share it safely.  A call may be captured into a CUDA graph once an
+ * share it safely, from several host threads too: a call keeps the others on
+ * its stream waiting until its last kernel is enqueued.  A call may be captured into a CUDA graph once an
  * uncaptured call of the same sizes has run on that stream; a replay must be
  * ordered with the calls and the other replays that use that stream's scratch.
  */

@@ -1,0 +1,104 @@
+"""Mixture-of-experts calls from several host threads on a GB300.
+
+The kernels of one call pass logits, choices and the first product's result to one
+another through scratch memory of their stream.  Calls of two threads must never
+find each other's values there."""
+import sys
+import threading
+
+import pytest
+
+import dense_fp16_gemm_f16_gb300 as g
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from dense_fp16_gemm_f16_gb300 import build as gbuild
+    assert torch.cuda.is_available(), "this test needs a CUDA GPU"
+    gbuild.build()
+
+
+class Case:
+    """One operator on inputs of its own; call(stream) returns its outputs."""
+
+    def __init__(self, op, T, H, I, E, k, seed):
+        gen = torch.Generator().manual_seed(seed)
+        self.op, self.k = op, k
+        self.X = torch.randn((T, H), generator=gen).half().cuda()
+        self.Wr = (torch.randn((E, H), generator=gen) / 16).half().cuda()
+        self.W13 = (torch.randn((E, 2 * I, H), generator=gen) / H ** 0.5).half().cuda()
+        self.W2 = (torch.randn((E, H, I), generator=gen) / I ** 0.5).half().cuda()
+        self.ids = torch.randint(0, E, (T, k), generator=gen).to(torch.int32).cuda()
+        self.weights = torch.rand((T, k), generator=gen).cuda()
+
+    def outputs(self):
+        if self.op == "route":
+            return torch.full_like(self.ids, -7), torch.full_like(self.weights, -7.0)
+        return (torch.full_like(self.X, float("nan")),)
+
+    def call(self, out, stream):
+        if self.op == "route":
+            g.gemm_moe_route(self.X, self.Wr, out[0], out[1], stream=stream)
+        elif self.op == "ffn":
+            g.gemm_moe_ffn(self.X, self.ids, self.weights, self.W13, self.W2, out[0], stream=stream)
+        else:
+            g.gemm_moe_layer(self.X, self.Wr, self.W13, self.W2, out[0], self.k, stream=stream)
+
+    def alone(self):
+        out = self.outputs()
+        self.call(out, None)
+        torch.cuda.synchronize()
+        return out
+
+
+def _run_threads(cases, streams, calls):
+    """Every case from a thread of its own, `calls` times; all outputs against a call alone."""
+    want = [c.alone() for c in cases]
+    outs = [[c.outputs() for _ in range(calls)] for c in cases]
+    torch.cuda.synchronize()
+    gate = threading.Barrier(len(cases))
+    errors = []
+
+    def work(i):
+        try:
+            gate.wait(60)
+            for out in outs[i]:
+                cases[i].call(out, streams[i])
+        except BaseException as e:   # noqa: B902  (reported by the test's thread)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    before = sys.getswitchinterval()
+    sys.setswitchinterval(1e-5)
+    try:
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join(120)
+    finally:
+        sys.setswitchinterval(before)
+    assert not errors, errors
+    torch.cuda.synchronize()
+    g.gemm_f16_nt_check(device=cases[0].X.device)
+    for i, case in enumerate(cases):
+        wrong = sum(not all(torch.equal(a, b) for a, b in zip(out, want[i])) for out in outs[i])
+        assert wrong == 0, f"{case.op} {i}: {wrong} of {calls} calls differ from a call alone"
+
+
+@pytest.mark.parametrize("op", ["layer", "ffn", "route"])
+def test_two_threads_on_one_stream(op):
+    # the same sizes, so that values of the other thread would fit; 16 tokens: choice in a kernel of its own
+    cases = [Case(op, 16, 512, 256, 8, 2, seed) for seed in (1, 2)]
+    for stream in (None, torch.cuda.Stream()):
+        _run_threads(cases, [stream, stream], 200)
+
+
+def test_threads_with_different_operators_on_one_stream():
+    cases = [Case("layer", 4, 256, 128, 8, 2, 3), Case("layer", 64, 512, 384, 16, 4, 4), Case("ffn", 20, 256, 512, 4, 2, 5),
+             Case("route", 64, 512, 8, 32, 4, 6)]
+    stream = torch.cuda.Stream()
+    _run_threads(cases, [stream] * 4, 100)
