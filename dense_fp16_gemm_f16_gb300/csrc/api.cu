@@ -6,9 +6,11 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cstdint>
 #include <cstring>
+#include <functional>
 #include <map>
 #include <mutex>
 #include <utility>
@@ -75,6 +77,20 @@ std::map<std::pair<int, void*>, Workspace> g_workspaces;
 EncodeTiledFn g_encode = nullptr;
 typedef CUresult (*CtxGetCurrentFn)(CUcontext*);
 CtxGetCurrentFn g_ctx_current = nullptr;
+
+// What a thread calls a stream: cudaStreamPerThread is one handle for all threads.
+struct StreamName {
+    int dev;
+    const void* handle;
+    unsigned long long thread;   // cudaStreamPerThread: the calling thread, else 0
+    bool operator<(const StreamName& o) const {
+        if (dev != o.dev) return dev < o.dev;
+        if (handle != o.handle) return std::less<const void*>()(handle, o.handle);
+        return thread < o.thread;
+    }
+};
+std::mutex g_names_mu;
+std::map<StreamName, unsigned long long> g_names;   // the ids that uncaptured calls found
 
 constexpr int64_t kMaxDim = INT32_MAX;
 // Raster groups hold as many tile rows as keep the group's A rows (tile rows x
@@ -941,6 +957,32 @@ gemm_status_t device_view(DeviceView* out) {
     const gemm_status_t st = get_device(&d, &dev);
     if (st != GEMM_OK) return st;
     *out = DeviceView{dev, d->sms, d->status};
+    return GEMM_OK;
+}
+
+// A stream that is being captured does not tell its id, so there it is the one of the
+// last uncaptured call, which the capture rule of the header asks for.
+gemm_status_t stream_key(int dev, gemm_stream_t stream, StreamKey* out) {
+    static std::atomic<unsigned long long> threads{0};
+    thread_local const unsigned long long thread = ++threads;   // unlike a thread's id, not used again
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const StreamName name{dev, stream, s == cudaStreamPerThread ? thread : 0};
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    unsigned long long id = 0;
+    if (cudaStreamIsCapturing(s, &capture) != cudaSuccess ||
+        (capture == cudaStreamCaptureStatusNone && cudaStreamGetId(s, &id) != cudaSuccess)) {
+        cudaGetLastError();
+        return GEMM_ERR_CUDA;
+    }
+    std::lock_guard<std::mutex> lock(g_names_mu);
+    if (capture == cudaStreamCaptureStatusNone) {
+        g_names[name] = id;
+    } else {
+        const auto known = g_names.find(name);
+        if (known == g_names.end()) return GEMM_ERR_CUDA;
+        id = known->second;
+    }
+    *out = StreamKey{dev, id};
     return GEMM_OK;
 }
 

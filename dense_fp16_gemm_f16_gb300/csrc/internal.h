@@ -39,6 +39,16 @@ bool encode_map(CUtensorMap* map, const void* base, int elem_bytes, int64_t inne
 bool ranges_overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes);
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// What scratch memory belongs to: one stream of one device.  A handle does not tell
+// streams apart: cudaStreamPerThread is another stream in every thread, and a
+// destroyed stream's handle may come back while its work still runs.
+struct StreamKey {
+    int dev;
+    unsigned long long id;   // cudaStreamGetId: never used twice in a process
+    bool operator<(const StreamKey& o) const { return dev != o.dev ? dev < o.dev : id < o.id; }
+};
+gemm_status_t stream_key(int dev, gemm_stream_t stream, StreamKey* out);   // api.cu
+
 // `bytes` of scratch for (device, stream), 256-byte aligned, and its counters:
 // kScratchCounters zeros that every kernel using them leaves at zero (llm/llm_api.cu).
 // The kernels of one call pass values to one another through it, so a Scratch keeps

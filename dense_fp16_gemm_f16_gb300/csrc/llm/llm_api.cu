@@ -5,7 +5,6 @@
 #include <climits>
 #include <map>
 #include <mutex>
-#include <utility>
 #include <vector>
 
 #include "llm/llm.h"
@@ -22,17 +21,20 @@ struct StreamScratch {
     uint32_t* counters = nullptr;
 };
 std::mutex g_scratch_mu;
-std::map<std::pair<int, void*>, StreamScratch> g_scratch;
+std::map<StreamKey, StreamScratch> g_scratch;
 }  // namespace
 
 // A buffer that has become too small is not freed: work queued on the stream,
 // or a captured graph, may still use it.  Buffers at least double, so the ones
 // left behind hold less than the one in use.
 gemm_status_t get_scratch(int dev, gemm_stream_t stream, size_t bytes, Scratch* out) {
+    StreamKey key;
+    const gemm_status_t st = stream_key(dev, stream, &key);
+    if (st != GEMM_OK) return st;
     StreamScratch* found = nullptr;
     {
         std::lock_guard<std::mutex> lock(g_scratch_mu);
-        found = &g_scratch[std::make_pair(dev, static_cast<void*>(stream))];   // stays where it is
+        found = &g_scratch[key];   // stays where it is
     }
     StreamScratch& w = *found;
     w.mu.lock();

@@ -15,9 +15,14 @@
  * twice the size.  Buffers are kept until the process exits, so a captured
  * graph never outlives the one it was recorded with.  Calls on one stream
  * share it safely, from several host threads too: a call keeps the others on
- * its stream waiting until its last kernel is enqueued.  A call may be captured into a CUDA graph once an
- * uncaptured call of the same sizes has run on that stream; a replay must be
- * ordered with the calls and the other replays that use that stream's scratch.
+ * its stream waiting until its last kernel is enqueued.  Streams are told apart
+ * by cudaStreamGetId, not by their handles: cudaStreamPerThread has a buffer
+ * for every thread, and a stream that gets a destroyed one's handle gets a
+ * buffer of its own.  A caller that makes and destroys many streams or threads
+ * therefore keeps a buffer for each.  A call may be captured into a CUDA graph
+ * once an uncaptured call of the same sizes has run on that stream; a replay
+ * must be ordered with the calls and the other replays that use that stream's
+ * scratch.
  */
 #ifndef GEMM_LLM_H_
 #define GEMM_LLM_H_

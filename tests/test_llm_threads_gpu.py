@@ -102,3 +102,67 @@ def test_threads_with_different_operators_on_one_stream():
              Case("route", 64, 512, 8, 32, 4, 6)]
     stream = torch.cuda.Stream()
     _run_threads(cases, [stream] * 4, 100)
+
+
+PER_THREAD = 2   # the handle cudaStreamPerThread
+
+
+def test_the_per_thread_stream_is_another_stream_in_every_thread():
+    # long enough that the threads' kernels run side by side
+    cases = [Case("layer", 16, 2048, 1024, 8, 2, seed) for seed in (7, 8, 9)]
+    _run_threads(cases, [PER_THREAD] * 3, 60)
+    cases = [Case("route", T, 4096, 8, 64, 4, T) for T in (3, 8, 64)]   # up to 8 tokens a counter tells the last CTA
+    _run_threads(cases, [PER_THREAD] * 3, 60)
+
+
+def test_a_destroyed_stream_leaves_its_scratch_to_its_work():
+    """A stream that comes after a destroyed one, perhaps with its handle, while the old one's work still waits."""
+    a, b = Case("layer", 16, 1024, 512, 8, 2, 11), Case("layer", 16, 1024, 512, 8, 2, 12)
+    want = a.alone(), b.alone()
+    rt = torch.cuda.cudart()
+
+    def create():
+        handle = torch.zeros(1, dtype=torch.int64)
+        assert int(rt.cudaStreamCreate(handle.data_ptr())) == 0
+        return int(handle)
+
+    for _ in range(4):
+        outs = a.outputs(), b.outputs()
+        torch.cuda.synchronize()
+        first = create()
+        with torch.cuda.stream(torch.cuda.ExternalStream(first)):
+            torch.cuda._sleep(20_000_000)   # 10 ms: the layer below is still waiting when its stream goes
+        a.call(outs[0], first)
+        assert int(rt.cudaStreamDestroy(first)) == 0
+        second = create()
+        b.call(outs[1], second)
+        torch.cuda.synchronize()
+        assert int(rt.cudaStreamDestroy(second)) == 0
+        g.gemm_f16_nt_check(device=a.X.device)
+        assert torch.equal(outs[0][0], want[0][0]) and torch.equal(outs[1][0], want[1][0])
+
+
+def test_capture_before_and_after_the_first_call_on_a_stream():
+    a = Case("layer", 16, 512, 256, 8, 2, 13)
+    want = a.alone()[0]
+    rt = torch.cuda.cudart()
+    handle = torch.zeros(1, dtype=torch.int64)
+    assert int(rt.cudaStreamCreate(handle.data_ptr())) == 0
+    fresh = torch.cuda.ExternalStream(int(handle))
+    out = a.outputs()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with pytest.raises(g.GemmError):   # no scratch yet: refused, and the stream stays usable
+        with torch.cuda.graph(graph, stream=fresh):
+            a.call(out, fresh)
+    a.call(out, fresh)
+    torch.cuda.synchronize()
+    assert torch.equal(out[0], want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=fresh):
+        a.call(out, fresh)
+    out[0].zero_()
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out[0], want)
