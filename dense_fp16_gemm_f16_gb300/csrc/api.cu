@@ -646,45 +646,40 @@ bool encode_2d(CUtensorMap* map, const void* base, int64_t inner, int64_t outer,
     return r == CUDA_SUCCESS;
 }
 
+// A buffer that has become too small is not freed: work queued on the stream, a
+// captured graph or a call that another thread is about to launch may still use it.
+// Buffers at least double, so the ones left behind hold less than the one in use.
 gemm_status_t get_workspace(int dev, gemm_stream_t stream, size_t partial_bytes, size_t n_counters,
-                            Workspace** out) {
+                            Workspace* out) {
     std::lock_guard<std::mutex> lock(g_mu);
     Workspace& w = g_workspaces[std::make_pair(dev, static_cast<void*>(stream))];
     if (w.partial_bytes < partial_bytes) {
-        // growing: the old buffer may still be in use by work queued on this stream
-        if (w.partials) {
-            if (cudaStreamSynchronize(stream) != cudaSuccess) { cudaGetLastError(); return GEMM_ERR_CUDA; }
-            cudaFree(w.partials);
-            w.partials = nullptr;
-            w.partial_bytes = 0;
-        }
-        if (cudaMalloc(&w.partials, partial_bytes) != cudaSuccess) {
+        const size_t want = std::max(partial_bytes, 2 * w.partial_bytes);
+        float* partials = nullptr;
+        if (cudaMalloc(&partials, want) != cudaSuccess) {
             cudaGetLastError();
-            w.partials = nullptr;
             return GEMM_ERR_CUDA;
         }
-        w.partial_bytes = partial_bytes;
+        w.partials = partials;
+        w.partial_bytes = want;
     }
     if (w.n_counters < n_counters) {
-        if (w.counters) {
-            if (cudaStreamSynchronize(stream) != cudaSuccess) { cudaGetLastError(); return GEMM_ERR_CUDA; }
-            cudaFree(w.counters);
-            w.counters = nullptr;
-            w.n_counters = 0;
-        }
-        if (cudaMalloc(&w.counters, n_counters * sizeof(uint32_t)) != cudaSuccess) {
+        const size_t want = std::max(n_counters, 2 * w.n_counters);
+        uint32_t* counters = nullptr;
+        if (cudaMalloc(&counters, want * sizeof(uint32_t)) != cudaSuccess) {
             cudaGetLastError();
-            w.counters = nullptr;
             return GEMM_ERR_CUDA;
         }
         // counters start at zero; every call leaves them at zero again
-        if (cudaMemset(w.counters, 0, n_counters * sizeof(uint32_t)) != cudaSuccess) {
+        if (cudaMemset(counters, 0, want * sizeof(uint32_t)) != cudaSuccess) {
             cudaGetLastError();
+            cudaFree(counters);
             return GEMM_ERR_CUDA;
         }
-        w.n_counters = n_counters;
+        w.counters = counters;
+        w.n_counters = want;
     }
-    *out = &w;
+    *out = w;
     return GEMM_OK;
 }
 
@@ -778,14 +773,14 @@ gemm_status_t run(const void* A, const void* B, void* D, int64_t M, int64_t N, i
         if (!encode_2d(&tw, B, K, N, bk, 128, dtype) ||
             !encode_2d(&tx, A, K, M, bk, static_cast<uint32_t>(ops.mn), dtype))
             return GEMM_ERR_INVALID_VALUE;
-        Workspace* ws = nullptr;
+        Workspace ws;
         const size_t partial_bytes = static_cast<size_t>(pl.grid_ctas) * pl.max_tiles_per_cta * ops.mn * 128 * 4;
         st = get_workspace(dev_id, stream, partial_bytes, static_cast<size_t>(pl.n_tiles), &ws);
         if (st != GEMM_OK) return st;
         // Every completed call leaves the tile counters at zero, but one that
         // gave up waiting (a timeout) may not; clear them on the stream so a
         // later call never starts from counts an earlier one left behind.
-        if (cudaMemsetAsync(ws->counters, 0, static_cast<size_t>(pl.n_tiles) * sizeof(uint32_t), s) != cudaSuccess) {
+        if (cudaMemsetAsync(ws.counters, 0, static_cast<size_t>(pl.n_tiles) * sizeof(uint32_t), s) != cudaSuccess) {
             cudaGetLastError();
             return GEMM_ERR_CUDA;
         }
@@ -798,8 +793,8 @@ gemm_status_t run(const void* A, const void* B, void* D, int64_t M, int64_t N, i
         p.num_ctas = pl.grid_ctas;
         p.max_tiles_per_cta = pl.max_tiles_per_cta;
         p.units = pl.n_tiles * pl.k_blocks;
-        p.partials = ws->partials;
-        p.counters = ws->counters;
+        p.partials = ws.partials;
+        p.counters = ws.counters;
         p.D = D;
         p.epi = epi;
         p.status = dev->status;

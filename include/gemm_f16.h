@@ -26,24 +26,23 @@
  *   - Argument errors are returned synchronously and nothing is enqueued.
  *   - The library uses the CUDA device that is current on the calling thread.
  *
- * Scratch memory.  Two kernels keep fp32 partial sums and per-tile counters
- * in global memory: the 2-CTA tiles with a split K loop
- * (GEMM_VARIANT_TILE_2CTA_SPLITK) and the stream-K small-M kernel
- * (GEMM_VARIANT_SKINNY_STREAMK; the default small-M kernel sums its partials
- * on chip and needs none).  That workspace is allocated with cudaMalloc on
- * the first call that needs it for a given (device, stream) pair, grows when
- * a larger problem needs more, and is kept until the process exits: a caller
- * that runs these variants on many short-lived streams keeps one workspace
- * per stream (each as large as the largest problem it ran).  Calls on the
- * same stream are ordered and share that workspace safely; calls on
- * different streams get different workspaces.
+ * Scratch memory.  The stream-K small-M kernel (GEMM_VARIANT_SKINNY_STREAMK)
+ * keeps fp32 partial sums and per-tile counters in global memory; the others
+ * sum what they split on chip and need none.  That workspace is allocated with
+ * cudaMalloc on the first call that needs it for a given (device, stream) pair;
+ * a larger problem gets a new one of at least twice the size.  Workspaces are
+ * kept until the process exits, the outgrown ones too (queued work or a captured
+ * graph may use them): a caller that runs this variant on many short-lived
+ * streams keeps up to four times its largest problem's workspace per stream.
+ * Calls on the same stream are ordered and share that workspace safely; calls
+ * on different streams get different workspaces.
  *
  * CUDA graphs.  A call may be recorded by stream capture (and the graph
  * replayed on new contents of the same buffers) once one uncaptured call of
  * the same kind has run on that stream: the first call on a device sets the
- * device up, and a call that has to grow its stream's workspace allocates
- * (and may synchronise the stream), which a capture does not allow.  The
- * recorded kernels keep the pointers, sizes and scalars of the captured call.
+ * device up, and a call that has to grow its stream's workspace allocates,
+ * which a capture does not allow.  The recorded kernels keep the pointers, sizes
+ * and scalars of the captured call.
  */
 #ifndef GEMM_F16_H_
 #define GEMM_F16_H_
