@@ -13,7 +13,6 @@
 #include <functional>
 #include <map>
 #include <mutex>
-#include <utility>
 
 #include "config.h"
 #include "epilogue.cuh"
@@ -73,7 +72,7 @@ struct Workspace {
 
 std::mutex g_mu;
 std::map<int, DeviceState> g_devices;
-std::map<std::pair<int, void*>, Workspace> g_workspaces;
+std::map<StreamKey, Workspace> g_workspaces;
 EncodeTiledFn g_encode = nullptr;
 typedef CUresult (*CtxGetCurrentFn)(CUcontext*);
 CtxGetCurrentFn g_ctx_current = nullptr;
@@ -651,8 +650,11 @@ bool encode_2d(CUtensorMap* map, const void* base, int64_t inner, int64_t outer,
 // Buffers at least double, so the ones left behind hold less than the one in use.
 gemm_status_t get_workspace(int dev, gemm_stream_t stream, size_t partial_bytes, size_t n_counters,
                             Workspace* out) {
+    StreamKey key;
+    const gemm_status_t st = stream_key(dev, stream, &key);
+    if (st != GEMM_OK) return st;
     std::lock_guard<std::mutex> lock(g_mu);
-    Workspace& w = g_workspaces[std::make_pair(dev, static_cast<void*>(stream))];
+    Workspace& w = g_workspaces[key];
     if (w.partial_bytes < partial_bytes) {
         const size_t want = std::max(partial_bytes, 2 * w.partial_bytes);
         float* partials = nullptr;
@@ -1099,7 +1101,7 @@ GEMM_API gemm_status_t gemm_f16_nt_check(gemm_stream_t stream) {
     {
         std::lock_guard<std::mutex> lock(g_mu);
         for (auto& kv : g_workspaces)
-            if (kv.first.first == dev_id && kv.second.counters)
+            if (kv.first.dev == dev_id && kv.second.counters)
                 cudaMemset(kv.second.counters, 0, kv.second.n_counters * sizeof(uint32_t));
     }
     if (cudaDeviceSynchronize() != cudaSuccess) {

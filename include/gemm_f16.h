@@ -35,7 +35,9 @@
  * graph may use them): a caller that runs this variant on many short-lived
  * streams keeps up to four times its largest problem's workspace per stream.
  * Calls on the same stream are ordered and share that workspace safely; calls
- * on different streams get different workspaces.
+ * on different streams get different workspaces.  Streams are told apart by
+ * cudaStreamGetId, not by their handles (cudaStreamPerThread is a stream of its
+ * own in every thread).
  *
  * CUDA graphs.  A call may be recorded by stream capture (and the graph
  * replayed on new contents of the same buffers) once one uncaptured call of

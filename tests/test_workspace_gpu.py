@@ -83,3 +83,35 @@ def test_two_threads_grow_one_workspace():
     for ws, ds in zip(work, outs):
         for (_, _, want, shape), d in zip(ws, ds):
             assert torch.equal(d, want), shape
+
+
+PER_THREAD = 2   # the handle cudaStreamPerThread
+
+
+def test_the_per_thread_stream_has_a_workspace_in_every_thread():
+    torch.backends.cuda.matmul.allow_tf32 = False
+    shapes = [(16, 8192, 4096), (64, 8192, 4096), (33, 4096, 8192)]   # long enough to run side by side
+    work = [_operands(*shape, i) for i, shape in enumerate(shapes)]
+    outs = [[torch.empty_like(w[2]) for _ in range(40)] for w in work]
+    torch.cuda.synchronize()
+    gate = threading.Barrier(len(work))
+    errors = []
+
+    def run(i):
+        try:
+            gate.wait(60)
+            for d in outs[i]:
+                g.gemm_f16_nt_variant(work[i][0], work[i][1], d, variant=STREAMK, stream=PER_THREAD)
+        except BaseException as e:   # noqa: B902  (reported by the test's thread)
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(work))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(120)
+    assert not errors, errors
+    torch.cuda.synchronize()
+    g.gemm_f16_nt_check(device=work[0][0].device)
+    for w, ds, shape in zip(work, outs, shapes):
+        assert all(torch.equal(d, w[2]) for d in ds), shape
