@@ -46,13 +46,16 @@ gemm_status_t launch_up(const FfnParams& f, void* h, const DeviceView& dev, cuda
         // pieces if they take at most half of it; a stage of columns would be as
         // large as the weights beside it
         const int fixed = 1024 + lists + sums;
-        p.x_pitch = up_to(f.H * 2, 128) + 64;
-        const int resident = W4 ? up_to(up_to(cols, 8) * p.x_pitch, 128) : 0;
-        p.x_resident = W4 && resident <= kSmemBudget<W4, NT, true> / 2 && fixed + resident + kw * 12 * 1024 <= kSmemBudget<W4, NT, true>;
+        // in 64 bits: eight columns of 2^27 elements pass 2^31 bytes
+        const int64_t x_pitch = (2ll * f.H + 127) / 128 * 128 + 64;
+        const int64_t all_columns = W4 ? (up_to(cols, 8) * x_pitch + 127) / 128 * 128 : 0;
+        p.x_resident = W4 && all_columns <= kSmemBudget<W4, NT, true> / 2 && fixed + all_columns + kw * 12 * 1024 <= kSmemBudget<W4, NT, true>;
+        p.x_pitch = p.x_resident ? static_cast<int32_t>(x_pitch) : 0;
+        const int resident = p.x_resident ? static_cast<int>(all_columns) : 0;
         p.ring = ring_layout(W4, 1, kUpRows, 2 * kUpGranules * 8, sg.atom_groups, p.x_resident ? 0 : cols,
-                             kSmemBudget<W4, NT, true> - fixed - (p.x_resident ? resident : 0), kw);
+                             kSmemBudget<W4, NT, true> - fixed - resident, kw);
         p.x_off = p.ring.end;
-        p.list_off = p.x_off + (p.x_resident ? resident : 0);
+        p.list_off = p.x_off + resident;
         p.sums_off = p.list_off + lists;
         smem = p.sums_off + sums + 1024;
         if (smem <= kSmemBudget<W4, NT, true> && p.ring.slots >= 8) break;
