@@ -80,3 +80,31 @@ def _one_expert(H, I, group):
 def test_experts_with_columns_past_two_gigabytes():
     # eight columns of H pass 2^31 bytes: they do not fit shared memory, whatever 32 bits say
     _one_expert(1 << 27, 8, 128)
+
+
+def test_router_with_the_longest_rows():
+    H, E = 2 ** 31 - 8, 2
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    X = torch.zeros((1, H), dtype=torch.float16, device="cuda")
+    Wr = torch.ones((E, H), dtype=torch.float16, device="cuda")
+    for part in (slice(0, 64), slice(H - 64, H)):
+        X[:, part] = torch.randint(-2, 3, (1, 64), generator=gen, device="cuda").half()
+        Wr[:, part] = torch.randint(-2, 3, (E, 64), generator=gen, device="cuda").half()
+    ids, w = g.gemm_moe_route(X, Wr, k=E)
+    g.gemm_f16_nt_check(device=X.device)
+    x, r = (torch.cat((t[:, :64], t[:, -64:]), 1) for t in (X, Wr))
+    rid, rw = lc.route64(x, r, E)
+    assert torch.equal(ids, rid)
+    assert bool(((w.double() - rw).abs() <= 2.0 ** -19 * rw + 1e-37).all())
+
+
+def test_router_with_many_tokens():
+    # more tokens than have their logits in scratch at one time, and a few left over
+    T, H, E, k = 16389, 72, 40, 3
+    gen = torch.Generator().manual_seed(6)
+    X = torch.randint(-1, 2, (T, H), generator=gen).bfloat16().cuda()
+    Wr = torch.randint(-1, 2, (E, H), generator=gen).bfloat16().cuda()
+    ids, w = g.gemm_moe_route(X, Wr, k=k)
+    rid, rw = lc.route64(X, Wr, k)
+    assert torch.equal(ids, rid)
+    assert bool(((w.double() - rw).abs() <= 2.0 ** -19 * rw + 1e-37).all())
