@@ -61,7 +61,7 @@ gemm_status_t launch_up(const FfnParams& f, void* h, const DeviceView& dev, cuda
         if (smem <= kSmemBudget<W4, NT, true> && p.ring.slots >= 8) break;
     }
     if (smem > kMaxDynamicSmem) return GEMM_ERR_CUDA;
-    p.k_stages = (f.H + kAtomElems<W4> - 1) / kAtomElems<W4>;
+    p.k_stages = count_of(f.H, kAtomElems<W4>);
     CUtensorMap w, sc, zr;
     if (!encode_weights(f.w13, rows, static_cast<int64_t>(f.E) * sg.groups_k, 2 * f.I, f.H, 8, kUpGranules * 8, sg.atom_groups, &w, &sc, &zr) ||
         !encode_weights_box(f.w13, rows, f.H, 8 * kUpGranules, &p.tm_piece))

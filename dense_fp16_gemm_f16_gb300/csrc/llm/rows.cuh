@@ -169,7 +169,7 @@ weight_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
             if constexpr (MOE) {
                 issue_w(at.seg, at.kb, own.first + d);
             } else {
-                if (lane < p.ring.atoms && (at.kb * p.ring.atoms + lane) * KE < p.K)
+                if (lane < p.ring.atoms && static_cast<int64_t>(at.kb * p.ring.atoms + lane) * KE < p.K)
                     ptx::tma_prefetch_2d(&tmW, (at.kb * p.ring.atoms + lane) * (W4 ? 128 : 64), row0);
             }
         }

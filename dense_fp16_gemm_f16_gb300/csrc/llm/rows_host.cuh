@@ -27,6 +27,9 @@ struct SideGroups {
     }
 };
 
+// Parts of up to `part` that n falls into.  n may be all but 2^31, so nothing is added to it.
+inline int count_of(int n, int part) { return n / part + (n % part != 0); }
+
 // Weights that cannot stay in L2 (129 MB) from one call to the next anyway
 // are read with evict-first, so they do not push out what can.
 inline int32_t stream_weights(bool w4, int64_t rows, int64_t K) { return (w4 ? rows * K / 2 : rows * K * 2) > (48ll << 20); }
@@ -206,7 +209,7 @@ int plan_rows_anew(const void* kernel, RowsParams* p, int tokens, int cols, int 
     constexpr int budget = kSmemBudget<W4, NT, MOE>;
     constexpr int MT = kTilesPerWarp<W4, NT, MOE>;
     const int table_cols = MOE ? tokens : 8 * NT;
-    const int k_atoms = (p->K + kAtomElems<W4> - 1) / kAtomElems<W4>;
+    const int k_atoms = count_of(p->K, kAtomElems<W4>);
     const int nt = std::min(NT, (typical_cols + 7) / 8);
     int best = 0;
     bool best_fits = false;
@@ -218,8 +221,8 @@ int plan_rows_anew(const void* kernel, RowsParams* p, int tokens, int cols, int 
         // as few rounds of clusters as keep a range within a TMA box (256 rows)
         // and the consumers' registers
         const int most = std::min(256, kConsumers * MT * 16);
-        const int rounds = (p->N + clusters * most - 1) / (clusters * most);
-        const int width = up_to((p->N + clusters * rounds - 1) / (clusters * rounds), 8);
+        const int rounds = count_of(p->N, clusters * most);
+        const int width = up_to(count_of(p->N, clusters * rounds), 8);
         const int tiles = (width + 15) / 16;
         for (int mw = 1; mw <= kConsumers; mw *= 2) {
             if (mw * MT < tiles) continue;
@@ -228,7 +231,7 @@ int plan_rows_anew(const void* kernel, RowsParams* p, int tokens, int cols, int 
                 if (atoms > 1 && atoms * width * 128 > 16384) break;
                 RowsParams c = *p;
                 c.width = width;
-                c.ranges = (p->N + width - 1) / width;
+                c.ranges = count_of(p->N, width);
                 c.pieces = P;
                 c.mw = mw;
                 c.k_stages = (k_atoms + atoms - 1) / atoms;

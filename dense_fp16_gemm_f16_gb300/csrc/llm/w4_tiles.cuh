@@ -211,7 +211,8 @@ w4_tiles_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     const int n0 = static_cast<int>(tile / p.m_tiles) * kTileRows;
     const int at0 = static_cast<int>(static_cast<int64_t>(j) * p.atoms / S);
     const int at1 = static_cast<int>(static_cast<int64_t>(j + 1) * p.atoms / S);
-    const int blocks = (min(at1 * 256, p.K) - at0 * 256 + 63) / 64;   // this CTA's K blocks, KB to a step
+    // this CTA's K blocks, KB to a step (the last atom's end may pass 2^31)
+    const int blocks = at1 < p.atoms ? (at1 - at0) * 4 : (p.K - at0 * 256 - 1) / 64 + 1;
     const int steps = (blocks + KB - 1) / KB;
     ptx::tc_fence_before();
     if (S > 1) ptx::cluster_sync(); else __syncthreads();

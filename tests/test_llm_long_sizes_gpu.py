@@ -108,3 +108,46 @@ def test_router_with_many_tokens():
     rid, rw = lc.route64(X, Wr, k)
     assert torch.equal(ids, rid)
     assert bool(((w.double() - rw).abs() <= 2.0 ** -19 * rw + 1e-37).all())
+
+
+def test_product_with_the_longest_rows():
+    N, K, group = 16, 2 ** 31 - 128, 128
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    A = _rows(gen, 1, K, torch.float16)
+    W = _w4(gen, (), N, K, group, torch.float16)
+    D = torch.full((1, N), float("nan"), dtype=torch.float16, device="cuda")
+    g.gemm_w4_nt(A, W, D)
+    g.gemm_f16_nt_check(device=D.device)
+    w, mag = lc.w64(_w4_ends(W))
+    a = _ends(A).double()
+    ref = a @ w.t()
+    lc.check(D, ref, 1.01 * lc.U[D.dtype] * ref.abs() + lc.E32 * (a.abs() @ mag.t()) + lc.FLOOR, f"K = {K}")
+
+
+@pytest.mark.parametrize("M", [1, 17])
+def test_product_with_the_most_rows_of_weights(M):
+    N, K, group = 2 ** 31 - 8, 32, 32
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    A = torch.randn((M, K), generator=gen, device="cuda").bfloat16()
+    W = _w4(gen, (), N, K, group, torch.bfloat16)
+    D = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    g.gemm_w4_nt(A, W, D)
+    g.gemm_f16_nt_check(device=D.device)
+    # nothing is left out, and slices in fp32: exact to 2^-20 of the sums' magnitudes
+    step, worst = 1 << 22, 0.0
+    assert not any(bool(torch.isnan(D[m]).any()) for m in range(M))
+    for r in (0, 1 << 29, (1 << 30) - step // 2, 3 << 29, N - step):
+        w, _ = lc.w64(g.W4(W.codes[r:r + step], W.scales[:, r:r + step], None, group))
+        w = w.float()
+        d = D[:, r:r + step].float()
+        for m in range(M):
+            prod = w * A[m].float()
+            ref = prod.sum(1)
+            off = (d[m] - ref).abs() - 1.01 * lc.U[D.dtype] * ref.abs()
+            # offset codes enter the sums: see llm_check
+            worst = max(worst, float((off / (prod.abs().sum(1) + 4 * A[m].float().abs().sum())).max()))
+    assert worst <= 2.0 ** -20
+
+
+def test_experts_with_the_longest_rows():
+    _one_expert(2 ** 31 - 128, 8, 128)
