@@ -131,6 +131,30 @@ __device__ __forceinline__ uint32_t extremes(const uint4& v) {
     }
 }
 
+// This thread's pieces of a tile (Walk's halves and ends) whose scale has no finite
+// reciprocal: bf16 scales of at most 2^-128.  They divide.  Apart from the kernel, whose
+// registers are full (as a branch of it, it cost every tile 2 %).
+template <bool ASYM>
+__device__ __noinline__ void quantize_smallest(const __nv_bfloat16* W, uint8_t* codes, int64_t off0, int64_t off1,
+                                               int row_end, int k_left, int shift,
+                                               const __nv_bfloat16 (*scales)[kCodesRows],
+                                               const __nv_bfloat16 (*zeros)[kCodesRows]) {
+    using B = Elem<__nv_bfloat16>;
+    for (int i = 0; i < 4; ++i) {
+        if (8 * (i >> 1) >= row_end || 256 * (i & 1) >= k_left) continue;
+        const int row = (threadIdx.x >> 5) + 8 * (i >> 1), grp = (256 * (i & 1) + (threadIdx.x & 31) * 8) >> shift;
+        const float s = B::to_float(scales[grp][row]), z = ASYM ? B::to_float(zeros[grp][row]) : 8.0f;
+        if (s == 0.0f || !isinf(__frcp_rn(s))) continue;
+        const int64_t at = (i >> 1 ? off1 : off0) + 256 * (i & 1);
+        float w[8];
+        unpack8<__nv_bfloat16>(*reinterpret_cast<const uint4*>(W + at), w);
+        uint32_t word = 0u;
+        for (int j = 0; j < 8; ++j)
+            word |= static_cast<uint32_t>(fminf(fmaxf(rintf(__fdiv_rn(w[j], s)) + z, 0.0f), 15.0f)) << (4 * j);
+        *reinterpret_cast<uint32_t*>(codes + at / 2) = word;
+    }
+}
+
 template <class T, bool ASYM>
 __global__ void __launch_bounds__(kCodesThreads, kPackPerSm)
 w4_quantize_kernel(const T* __restrict__ W, int64_t rows, int64_t N, int64_t K, int64_t k_tiles, int64_t tiles, int shift,
@@ -216,7 +240,13 @@ w4_quantize_kernel(const T* __restrict__ W, int64_t rows, int64_t N, int64_t K, 
                 __stcs(reinterpret_cast<uint32_t*>(tile.word(codes, i)),
                        __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x5410));
         }
-        __syncthreads();   // two buffers: the next tile's writes go to the other one
+        // two buffers: the next tile's writes go to the other one
+        if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+            if (__syncthreads_or(isinf(inv_mine)))
+                quantize_smallest<ASYM>(W, codes, tile.off[0], tile.off[1], tile.row_end, tile.k_left, shift, s_scale[buf], s_zero[buf]);
+        } else {
+            __syncthreads();
+        }
         const int64_t at = side.at(tile, shift);
         if (at >= 0) {
             scales[at] = s_scale[buf][threadIdx.x / kCodesRows][threadIdx.x % kCodesRows];
