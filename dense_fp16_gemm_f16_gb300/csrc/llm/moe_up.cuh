@@ -245,7 +245,7 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                     gate += a[q * kCols * kUpPitch];
                     up += a[q * kCols * kUpPitch + 8];
                 }
-                const float v = gate / (1.0f + __expf(-gate)) * up;
+                const float v = gate / (1.0f + expf(-gate)) * up;
                 const T hi = Elem<T>::from_float(v);
                 const float back = Elem<T>::to_float(hi);
                 const int64_t to = 2 * static_cast<int64_t>(lists.slot[first + c]) * p.I + at * 8 + r;
