@@ -150,6 +150,32 @@ def _stream_handle(stream, device=None) -> int | None:
     return int(stream) or None
 
 
+def _empty(shape, dtype, device, stream):
+    """An output that a call on ``stream`` (None: the current one) writes.
+
+    With another stream than the current one the memory comes from that stream's
+    share, so work still queued on the current stream cannot be using it, and
+    it is not given away before either stream is done with it."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    handle = _stream_handle(stream) or 0
+    current = torch.cuda.current_stream(device)
+    if handle == current.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if handle == 2:
+        # cudaStreamPerThread: torch would keep one share of memory for all threads' streams
+        raise ValueError("a call on the per-thread default stream needs its outputs given")
+    if handle <= 1:   # the legacy default stream by either handle
+        own = torch.cuda.default_stream(device)
+    else:
+        own = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle, device=device)
+    with torch.cuda.stream(own):
+        out = torch.empty(shape, dtype=dtype, device=device)
+    out.record_stream(current)
+    return out
+
+
 def _torch_types(dtype):
     """(accepted operand dtypes, D dtype) for a Dtype."""
     import torch
@@ -305,7 +331,7 @@ def gemm_nt_plan_ex(dtype, M: int, N: int, K: int, variant=Variant.AUTO, num_sms
 def gemm(A, B, variant=Variant.AUTO, stream=None):
     """Convenience: allocate D with torch on A's device and return A·Bᵀ."""
     import torch
-    D = torch.empty((A.shape[0], B.shape[0]), dtype=torch.float16, device=A.device)
+    D = _empty((A.shape[0], B.shape[0]), torch.float16, A.device, stream)
     gemm_f16_nt_variant(A, B, D, variant=variant, stream=stream)
     return D
 

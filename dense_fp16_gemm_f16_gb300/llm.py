@@ -5,6 +5,10 @@ Tensors are contiguous CUDA tensors on one device; activations, scales, zero
 points and outputs are all float16 or all bfloat16.  Calls are asynchronous on
 ``stream`` (default: the tensors' current stream).  Argument checks happen
 here (``TypeError`` / ``ValueError``) and in the library (``GemmError``).
+
+Outputs that are not given are allocated for ``stream``.  A caller that reads them
+on another stream waits for ``stream`` first; they may be dropped at any time if
+that stream was current at the call, else after ``Tensor.record_stream``.
 """
 from __future__ import annotations
 
@@ -169,11 +173,11 @@ def gemm_w4_quantize(W, group: int = 128, codes=None, scales=None, zeros=None, s
         raise ValueError("symmetric weights have no zero points")
     side = (*lead, K // group, N)
     if codes is None:
-        codes = _torch.empty((*lead, N, K // 2), dtype=_torch.uint8, device=W.device)
+        codes = _g._empty((*lead, N, K // 2), _torch.uint8, W.device, stream)
     if scales is None:
-        scales = _torch.empty(side, dtype=W.dtype, device=W.device)
+        scales = _g._empty(side, W.dtype, W.device, stream)
     if zeros is None and not symmetric:
-        zeros = _torch.empty(side, dtype=W.dtype, device=W.device)
+        zeros = _g._empty(side, W.dtype, W.device, stream)
     out = W4(codes, scales, zeros, group)
     w = _weights(out, "output", W.dtype, tuple(lead), N, K, index)
     _run(lib.gemm_w4_quantize, index, stream,
@@ -193,7 +197,7 @@ def gemm_w4_dequantize(W: W4, out=None, stream=None):
     *lead, N, K = W.shape
     w = _weights(W, "W", W.scales.dtype, tuple(lead), N, K, index)
     if out is None:
-        out = _torch.empty(W.shape, dtype=W.scales.dtype, device=W.codes.device)
+        out = _g._empty(W.shape, W.scales.dtype, W.codes.device, stream)
     ptr = _check(out, "out", W.scales.dtype, W.shape, index)
     _run(lib.gemm_w4_dequantize, index, stream,
          (dt, ctypes.byref(w), lead[0] if lead else 1, N, K, ptr))
@@ -252,9 +256,9 @@ def gemm_moe_route(X, Wr, ids=None, weights=None, k: int | None = None, bias=Non
             raise ValueError("give k or ids")
         k = ids.shape[-1]
     if ids is None:
-        ids = _torch.empty((T, k), dtype=_torch.int32, device=X.device)
+        ids = _g._empty((T, k), _torch.int32, X.device, stream)
     if weights is None:
-        weights = _torch.empty((T, k), dtype=_torch.float32, device=X.device)
+        weights = _g._empty((T, k), _torch.float32, X.device, stream)
     _run(lib.gemm_moe_route, index, stream,
          (dt, X.data_ptr(), wr, b, T, H, E, k, int(scoring), 1 if renormalize else 0,
           _check(ids, "ids", _torch.int32, (T, k), index),
