@@ -83,7 +83,9 @@ GEMM_API gemm_status_t gemm_w4_dequantize(gemm_dtype_t dtype, const gemm_weights
  * M == 0 or N == 0 is a no-op; K == 0 gives act(beta * C + bias).
  * Precision; sums are fp32 throughout.
  *   M <= 16: the products of codes and A are exact, scales and zero points
- *     are applied to each group's sum in fp32.
+ *     are applied to each group's sum in fp32: s * (sum (code + o) A - (z + o) sum A),
+ *     o = 0 for fp16 and 128 for bf16.  So an infinity in a row of A makes all of
+ *     that row's outputs NaN, and in bf16 finite A beyond 2^113 may.
  *   17 <= M <= 64: as above, or, for larger N and K, code - zero rounded to dtype
  *     (exact for whole and half zero points) and its product with the scale kept
  *     as two numbers of dtype, exact but for what lies below dtype's smallest
@@ -126,7 +128,9 @@ GEMM_API gemm_status_t gemm_moe_route(gemm_dtype_t dtype, const void* X, const v
  *   projection U); w2: E matrices of H rows of K = I; each 16-bit or 4-bit
  * silu and its product are formed in fp32 and kept to twice the precision of
  * dtype between the two products; beyond dtype's largest value they are
- * infinite.  H and I multiples of 8, and of the group where weights have 4
+ * infinite.  4-bit experts take their columns as gemm_w4_nt does for M <= 16:
+ * an infinity in X, or in what lies between the products, makes the token's
+ * outputs NaN, and in bf16 finite values beyond 2^113 may.  H and I multiples of 8, and of the group where weights have 4
  * bits; E <= 1024, 1 <= k <= 16.  T == 0 is a no-op.
  */
 GEMM_API gemm_status_t gemm_moe_ffn(gemm_dtype_t dtype, const void* X, const int32_t* ids, const float* weights,
