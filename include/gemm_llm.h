@@ -20,9 +20,9 @@
  * for every thread, and a stream that gets a destroyed one's handle gets a
  * buffer of its own.  A caller that makes and destroys many streams or threads
  * therefore keeps a buffer for each.  A call may be captured into a CUDA graph
- * once an uncaptured call of the same sizes has run on that stream; a replay
- * must be ordered with the calls and the other replays that use that stream's
- * scratch.
+ * once an uncaptured call of the same sizes has run on that stream (on this one,
+ * not on a destroyed stream that had its handle); a replay must be ordered with
+ * the calls and the other replays that use that stream's scratch.
  */
 #ifndef GEMM_LLM_H_
 #define GEMM_LLM_H_

@@ -3,6 +3,8 @@
 The kernels of one call pass logits, choices and the first product's result to one
 another through scratch memory of their stream.  Calls of two threads must never
 find each other's values there."""
+import os
+import subprocess
 import sys
 import threading
 
@@ -142,27 +144,40 @@ def test_a_destroyed_stream_leaves_its_scratch_to_its_work():
         assert torch.equal(outs[0][0], want[0][0]) and torch.equal(outs[1][0], want[1][0])
 
 
-def test_capture_before_and_after_the_first_call_on_a_stream():
-    a = Case("layer", 16, 512, 256, 8, 2, 13)
-    want = a.alone()[0]
-    rt = torch.cuda.cudart()
-    handle = torch.zeros(1, dtype=torch.int64)
-    assert int(rt.cudaStreamCreate(handle.data_ptr())) == 0
-    fresh = torch.cuda.ExternalStream(int(handle))
-    out = a.outputs()
-    graph = torch.cuda.CUDAGraph()
-    torch.cuda.synchronize()
-    with pytest.raises(g.GemmError):   # no scratch yet: refused, and the stream stays usable
-        with torch.cuda.graph(graph, stream=fresh):
-            a.call(out, fresh)
-    a.call(out, fresh)
-    torch.cuda.synchronize()
-    assert torch.equal(out[0], want)
-    graph = torch.cuda.CUDAGraph()
-    with torch.cuda.graph(graph, stream=fresh):
+# In a process of its own: no stream has had the new one's handle before.
+_CAPTURE = """
+import torch
+import dense_fp16_gemm_f16_gb300 as g
+from test_llm_threads_gpu import Case
+a = Case("layer", 16, 512, 256, 8, 2, 13)
+want = a.alone()[0]
+fresh = torch.cuda.Stream()
+out = a.outputs()
+torch.cuda.synchronize()
+refused = False
+try:
+    with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=fresh):
         a.call(out, fresh)
-    out[0].zero_()
-    torch.cuda.synchronize()
-    graph.replay()
-    torch.cuda.synchronize()
-    assert torch.equal(out[0], want)
+except g.GemmError:
+    refused = True
+assert refused   # no scratch yet; the capture ended well and the stream stays usable
+a.call(out, fresh)
+torch.cuda.synchronize()
+assert torch.equal(out[0], want)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph, stream=fresh):
+    a.call(out, fresh)
+out[0].zero_()
+torch.cuda.synchronize()
+graph.replay()
+torch.cuda.synchronize()
+assert torch.equal(out[0], want)
+print("as expected")
+"""
+
+
+def test_capture_before_and_after_the_first_call_on_a_stream():
+    here = os.path.dirname(os.path.abspath(__file__))
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([here, os.path.dirname(here), os.environ.get("PYTHONPATH", "")]))
+    out = subprocess.run([sys.executable, "-c", _CAPTURE], capture_output=True, text=True, timeout=300, env=env)
+    assert out.returncode == 0 and "as expected" in out.stdout, out.stdout + out.stderr
