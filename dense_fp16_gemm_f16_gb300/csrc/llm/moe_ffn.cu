@@ -35,6 +35,7 @@ gemm_status_t launch_up(const FfnParams& f, void* h, const DeviceView& dev, cuda
     p.timeout_ns = kStreamTimeoutNs;
     const int lists = list_offsets(f.T * f.k, f.E).end;
     const int cols = std::min(8 * NT, f.T);
+    constexpr int kBudget = kSmemBudget<W4, NT, true>;
     int smem = 0;
     for (int mw = kUpGranules / kTilesPerWarp<W4, NT, true>; mw <= kUpGranules; mw *= 2) {
         // as few warps per stage as the registers allow, more where the sums
@@ -49,24 +50,26 @@ gemm_status_t launch_up(const FfnParams& f, void* h, const DeviceView& dev, cuda
         // in 64 bits: eight columns of 2^27 elements pass 2^31 bytes
         const int64_t x_pitch = (2ll * f.H + 127) / 128 * 128 + 64;
         const int64_t all_columns = W4 ? (up_to(cols, 8) * x_pitch + 127) / 128 * 128 : 0;
-        p.x_resident = W4 && all_columns <= kSmemBudget<W4, NT, true> / 2 && fixed + all_columns + kw * 12 * 1024 <= kSmemBudget<W4, NT, true>;
+        p.x_resident = W4 && all_columns <= kBudget / 2 && fixed + all_columns + kw * 12 * 1024 <= kBudget;
         p.x_pitch = p.x_resident ? static_cast<int32_t>(x_pitch) : 0;
         const int resident = p.x_resident ? static_cast<int>(all_columns) : 0;
         p.ring = ring_layout(W4, 1, kUpRows, 2 * kUpGranules * 8, sg.atom_groups, p.x_resident ? 0 : cols,
-                             kSmemBudget<W4, NT, true> - fixed - resident, kw);
+                             kBudget - fixed - resident, kw);
         p.x_off = p.ring.end;
         p.list_off = p.x_off + resident;
         p.sums_off = p.list_off + lists;
         smem = p.sums_off + sums + 1024;
-        if (smem <= kSmemBudget<W4, NT, true> && p.ring.slots >= 8) break;
+        if (smem <= kBudget && p.ring.slots >= 8) break;
     }
     if (smem > kMaxDynamicSmem) return GEMM_ERR_CUDA;
     p.k_stages = count_of(f.H, kAtomElems<W4>);
     CUtensorMap w, sc, zr;
-    if (!encode_weights(f.w13, rows, static_cast<int64_t>(f.E) * sg.groups_k, 2 * f.I, f.H, 8, kUpGranules * 8, sg.atom_groups, &w, &sc, &zr) ||
+    if (!encode_weights(f.w13, rows, static_cast<int64_t>(f.E) * sg.groups_k, 2 * f.I, f.H, 8, kUpGranules * 8,
+                        sg.atom_groups, &w, &sc, &zr) ||
         !encode_weights_box(f.w13, rows, f.H, 8 * kUpGranules, &p.tm_piece))
         return GEMM_ERR_INVALID_VALUE;
-    return launch_stream(moe_up_kernel<T, CPG, NT>, dev.dev, kCtasPerSm<W4, NT, true> * dev.sms, 1, smem, true, s, w, sc, zr, p);
+    return launch_stream(moe_up_kernel<T, CPG, NT>, dev.dev, kCtasPerSm<W4, NT, true> * dev.sms, 1, smem, true, s, w, sc,
+                         zr, p);
 }
 
 template <class T, int CPG, int NT>
@@ -77,7 +80,9 @@ gemm_status_t launch_down(const FfnParams& f, const void* h, const DeviceView& d
     const int lists = list_offsets(f.T * f.k, f.E).end;
     p.N = f.H;
     p.K = f.I;
-    const int smem = plan_rows<W4, NT, true>(reinterpret_cast<const void*>(weight_rows_kernel<T, CPG, NT, true>), &p, f.T, std::min(8 * NT, 2 * f.T), std::min(8 * NT, 2 * typical_slots(f)), std::min(f.E, f.T * f.k), sg.atom_groups, lists, dev);
+    const int cols = std::min(8 * NT, 2 * f.T), typical_cols = std::min(8 * NT, 2 * typical_slots(f));
+    const int smem = plan_rows<W4, NT, true>(reinterpret_cast<const void*>(weight_rows_kernel<T, CPG, NT, true>), &p, f.T,
+                                             cols, typical_cols, std::min(f.E, f.T * f.k), sg.atom_groups, lists, dev);
     if (smem <= 0) return GEMM_ERR_CUDA;
     p.groups_k = sg.groups_k;
     p.atom_groups = sg.atom_groups;
@@ -94,13 +99,15 @@ gemm_status_t launch_down(const FfnParams& f, const void* h, const DeviceView& d
     p.status = dev.status;
     p.timeout_ns = kStreamTimeoutNs;
     CUtensorMap w, sc, zr;
-    if (!encode_weights(f.w2, rows, static_cast<int64_t>(f.E) * sg.groups_k, f.H, f.I, p.width, p.width, p.ring.atoms * sg.atom_groups, &w, &sc, &zr))
+    if (!encode_weights(f.w2, rows, static_cast<int64_t>(f.E) * sg.groups_k, f.H, f.I, p.width, p.width,
+                        p.ring.atoms * sg.atom_groups, &w, &sc, &zr))
         return GEMM_ERR_INVALID_VALUE;
     // Clusters of 8 that start while the CTAs of the first product end here and there
     // are placed so that some are left for a second round: 64 tokens, 2 of 64
     // experts of 2048 x 1408 in 4 bits 184 us, 134 if they wait for its end.  The
     // smaller clusters gain 1 to 3 us by starting early.
-    return launch_stream(weight_rows_kernel<T, CPG, NT, true>, dev.dev, p.ranges * p.pieces, p.pieces, smem, p.pieces < 8, s, w, sc, zr, p);
+    return launch_stream(weight_rows_kernel<T, CPG, NT, true>, dev.dev, p.ranges * p.pieces, p.pieces, smem, p.pieces < 8,
+                         s, w, sc, zr, p);
 }
 
 // How many columns a kernel is built for (8 NT).  An expert with more slots than
@@ -108,7 +115,8 @@ gemm_status_t launch_down(const FfnParams& f, const void* h, const DeviceView& d
 // more tiles per warp or for two CTAs per SM, and shared memory for weights in
 // flight.  Matrices of up to kResident bytes are still in L2 when they are read again,
 // so for them the narrow kernels win well past the slots that an expert
-// usually gets.  Measured, E experts of H x I, T tokens with k choices (us):
+// usually gets.  Measured, E experts of H x I, T tokens with k choices, us of the whole
+// layer for each width of the product named:
 //   first product, 16 bits: 64 of 2048 x 1024, T = 64, k = 6: 8 columns 184, 16
 //     columns 202; k = 8: 226, 222.  8 of 4096 x 8200, k = 2, T = 16: 265, 275;
 //     T = 32: 390, 338; T = 64: 16 columns 550, 32 columns 564.
@@ -123,7 +131,9 @@ gemm_status_t launch_down(const FfnParams& f, const void* h, const DeviceView& d
 //     columns 165, 32 columns 171; T = 64: 246, 240, 206.
 constexpr int64_t kResident = 24ll << 20;
 
-bool resident(const Weights& w, int64_t rows, int64_t K) { return (w.scales != nullptr ? rows * K / 2 : rows * K * 2) <= kResident; }
+bool resident(const Weights& w, int64_t rows, int64_t K) {
+    return (w.scales != nullptr ? rows * K / 2 : rows * K * 2) <= kResident;
+}
 
 int up_columns(const FfnParams& f) {
     const int usual = typical_slots(f);

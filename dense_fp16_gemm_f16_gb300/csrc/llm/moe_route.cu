@@ -22,7 +22,6 @@
 
 #include "llm/llm.h"
 #include "llm/stream.cuh"
-#include "llm/w4.cuh"
 
 namespace gemm_gb300 {
 namespace {

@@ -118,14 +118,17 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
             if (count == kUpGranules) {
                 if (lane < 2) ptx::tma_load_2d_hint(dst, &p.tm_piece, full_bar(s), kb * (W4 ? 128 : 64), y, pol_w);
             } else if (lane < 2 * count) {
-                ptx::tma_load_2d_hint(dst + (lane >> 1) * 1024u, &tmW, full_bar(s), kb * (W4 ? 128 : 64), y + (lane >> 1) * 8, pol_w);
+                ptx::tma_load_2d_hint(dst + (lane >> 1) * 1024u, &tmW, full_bar(s), kb * (W4 ? 128 : 64),
+                                      y + (lane >> 1) * 8, pol_w);
             }
             if constexpr (W4) {
                 // [scales | zero points] x [gate | up] x [groups][32 rows]
                 const int q = lane - 8;
-                if (q >= 0 && q < (p.has_zeros ? 4 : 2))
-                    ptx::tma_load_2d(base + static_cast<uint32_t>(p.ring.side_off + s * p.ring.side_bytes + (q >> 1) * (p.ring.side_bytes / 2)) + (q & 1) * side_half,
-                                     (q >> 1) ? &tmZ : &tmS, full_bar(s), at * 8 + ((q & 1) ? p.I : 0), e * p.groups_k + kb * p.atom_groups);
+                if (q >= 0 && q < (p.has_zeros ? 4 : 2)) {
+                    const int side = p.ring.side_off + s * p.ring.side_bytes + (q >> 1) * (p.ring.side_bytes / 2);
+                    ptx::tma_load_2d(base + static_cast<uint32_t>(side) + (q & 1) * side_half, (q >> 1) ? &tmZ : &tmS,
+                                     full_bar(s), at * 8 + ((q & 1) ? p.I : 0), e * p.groups_k + kb * p.atom_groups);
+                }
             }
         }
         if (p.x_resident) return;
@@ -133,9 +136,11 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
         constexpr int kShift = W4 ? 5 : 3;   // 32 or 8 pieces of 16 bytes per column
         for (int i = mg * 32 + lane; i < (n << kShift); i += 32 * p.mw) {   // the group's warps share them
             const int c = i >> kShift, o = (i - (c << kShift)) * 8;
-            if (o < kv)
+            if (o < kv) {
+                const int64_t token = lists.slot[first + c] / p.k;
                 ptx::cp_async16(x + static_cast<uint32_t>(c * pitch + o * 2),
-                                static_cast<const T*>(p.X) + static_cast<int64_t>(lists.slot[first + c] / p.k) * p.H + static_cast<int64_t>(kb) * KE + o);
+                                static_cast<const T*>(p.X) + token * p.H + static_cast<int64_t>(kb) * KE + o);
+            }
         }
         ptx::cp_async_arrive(full_bar(s));
     };

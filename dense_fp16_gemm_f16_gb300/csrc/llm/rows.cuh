@@ -109,18 +109,19 @@ weight_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         const int kv = min(stage_elems, p.K - kb * stage_elems);
         const int na = (kv + KE - 1) / KE;
         const int matrix = MOE ? lists.seg_e[seg] : 0;
-        if (lane == 0)
-            ptx::mbar_arrive_expect_tx(full_bar(s), static_cast<uint32_t>(na * p.width * 128) +
-                                                        (W4 ? static_cast<uint32_t>(p.width * p.ring.atoms * p.atom_groups * 2) * (p.has_zeros ? 2u : 1u) : 0u));
+        const uint32_t w_tx = static_cast<uint32_t>(na * p.width * 128);
+        const uint32_t side_tx = W4 ? static_cast<uint32_t>(p.width * p.ring.atoms * p.atom_groups * 2) : 0u;
+        if (lane == 0) ptx::mbar_arrive_expect_tx(full_bar(s), w_tx + side_tx * (p.has_zeros ? 2u : 1u));
         __syncwarp();
         if (lane < na)
-            ptx::tma_load_2d_hint(base + static_cast<uint32_t>(s * p.ring.w_bytes + lane * p.ring.atom_bytes), &tmW, full_bar(s),
-                                  (kb * p.ring.atoms + lane) * (W4 ? 128 : 64), matrix * p.N + row0, pol_w);
+            ptx::tma_load_2d_hint(base + static_cast<uint32_t>(s * p.ring.w_bytes + lane * p.ring.atom_bytes), &tmW,
+                                  full_bar(s), (kb * p.ring.atoms + lane) * (W4 ? 128 : 64), matrix * p.N + row0, pol_w);
         if constexpr (W4) {
             const uint32_t side = base + static_cast<uint32_t>(p.ring.side_off + s * p.ring.side_bytes);
             const int y = matrix * p.groups_k + kb * p.ring.atoms * p.atom_groups;
             if (lane == 8) ptx::tma_load_2d(side, &tmS, full_bar(s), row0, y);
-            if (lane == 9 && p.has_zeros) ptx::tma_load_2d(side + static_cast<uint32_t>(p.ring.side_bytes / 2), &tmZ, full_bar(s), row0, y);
+            if (lane == 9 && p.has_zeros)
+                ptx::tma_load_2d(side + static_cast<uint32_t>(p.ring.side_bytes / 2), &tmZ, full_bar(s), row0, y);
         }
     };
     // ... and the columns
@@ -247,8 +248,10 @@ weight_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                 const uint32_t x = there + static_cast<uint32_t>(p.ring.x_off + s * p.ring.x_bytes + a * KE * 2);
                 const int k = min(KE, kv - a * KE);
                 if constexpr (W4) {
-                    const uint32_t sc = there + static_cast<uint32_t>(p.ring.side_off + s * p.ring.side_bytes + (a * p.atom_groups * p.width + tile0 * 16) * 2);
-                    const SideView side{sc, sc + static_cast<uint32_t>(p.ring.side_bytes / 2), 16u, static_cast<uint32_t>(p.width * 2)};
+                    const int first_scale = a * p.atom_groups * p.width + tile0 * 16;
+                    const uint32_t sc = there + static_cast<uint32_t>(p.ring.side_off + s * p.ring.side_bytes + first_scale * 2);
+                    const SideView side{sc, sc + static_cast<uint32_t>(p.ring.side_bytes / 2), 16u,
+                                        static_cast<uint32_t>(p.width * 2)};
                     sw.template atom4<CPG, 2048, 32>(w, 1024u, x, pitch, side, p.has_zeros != 0, k, tiles, nt, lane);
                 } else {
                     sw.template atom16<2048>(w, 1024u, x, pitch, k, tiles, nt, lane);
@@ -328,17 +331,12 @@ weight_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
 }
 
 // ------------------------------------------------------------------- host side
-struct RowsShape {
-    int width, ranges, pieces, mw, smem;
-    RingLayout ring;
-    int list_off, table_off, recv_off, table_pitch;
-};
-
 inline int up_to(int a, int b) { return (a + b - 1) / b * b; }
 
 // A ring for kw groups with `rows` rows and `cols` columns a stage, with as many
 // slots as `budget` bytes allow (at least one a group; the caller checks `end`).
-inline RingLayout ring_layout(bool w4, int atoms, int rows, int side_rows, int atom_groups, int cols, int budget, int kw) {
+inline RingLayout ring_layout(bool w4, int atoms, int rows, int side_rows, int atom_groups, int cols, int budget,
+                              int kw) {
     RingLayout r;
     r.atoms = atoms;
     r.atom_bytes = up_to(rows, 16) * 128;

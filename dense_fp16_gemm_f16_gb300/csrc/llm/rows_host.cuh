@@ -32,7 +32,9 @@ inline int count_of(int n, int part) { return n / part + (n % part != 0); }
 
 // Weights that cannot stay in L2 (129 MB) from one call to the next anyway
 // are read with evict-first, so they do not push out what can.
-inline int32_t stream_weights(bool w4, int64_t rows, int64_t K) { return (w4 ? rows * K / 2 : rows * K * 2) > (48ll << 20); }
+inline int32_t stream_weights(bool w4, int64_t rows, int64_t K) {
+    return (w4 ? rows * K / 2 : rows * K * 2) > (48ll << 20);
+}
 
 // Tensor maps of a stack: rows x K codes or 16-bit numbers in boxes of
 // box_rows x 128 bytes; scales and zero points [side_rows][N] in boxes of
@@ -45,12 +47,13 @@ inline bool encode_weights(const Weights& w, int64_t rows, int64_t side_rows, in
         return true;
     }
     if (!encode_map(tw, w.data, 1, K / 2, rows, 128, static_cast<uint32_t>(box_rows), true)) return false;
-    if (!encode_map(ts, w.scales, 2, N, side_rows, static_cast<uint32_t>(side_box), static_cast<uint32_t>(side_groups), false)) return false;
+    const uint32_t box_n = static_cast<uint32_t>(side_box), box_groups = static_cast<uint32_t>(side_groups);
+    if (!encode_map(ts, w.scales, 2, N, side_rows, box_n, box_groups, false)) return false;
     if (w.zeros == nullptr) {
         *tz = *ts;
         return true;
     }
-    return encode_map(tz, w.zeros, 2, N, side_rows, static_cast<uint32_t>(side_box), static_cast<uint32_t>(side_groups), false);
+    return encode_map(tz, w.zeros, 2, N, side_rows, box_n, box_groups, false);
 }
 
 // The same rows in boxes of another height.
@@ -251,13 +254,16 @@ int plan_rows_anew(const void* kernel, RowsParams* p, int tokens, int cols, int 
                 // kw groups side by side; warps that share a stage wait for one
                 // another.
                 const int per_warp = (tiles + mw - 1) / mw;
-                const double work = W4 ? 8.0 * (10.0 * nt + per_warp * (22.0 + 6.0 * nt)) : 4.0 * (6.0 * nt + per_warp * (5.0 + 3.0 * nt));
+                const double work = W4 ? 8.0 * (10.0 * nt + per_warp * (22.0 + 6.0 * nt))
+                                       : 4.0 * (6.0 * nt + per_warp * (5.0 + 3.0 * nt));
                 const double arith = kCtasPerSm<W4, NT, MOE> * (work + 200.0 / atoms) * mw * (0.9 + 0.1 * mw) / 2.0;
                 const double flight = std::min(1.0, c.ring.slots * atoms * width * 128 / (65536.0 / kCtasPerSm<W4, NT, MOE>));
-                const double copies = kCtasPerSm<W4, NT, MOE> * (width * 128 / 23.5 + typical_cols * (W4 ? 512 : 128) / 50.0) / flight;
+                const double copies =
+                    kCtasPerSm<W4, NT, MOE> * (width * 128 / 23.5 + typical_cols * (W4 ? 512 : 128) / 50.0) / flight;
                 const double latency = (1500.0 + 1500.0 * (mw - 1)) / (kw * atoms) + 2.0 * work / kw;
                 const double n_atoms = std::ceil(std::ceil(static_cast<double>(segments) * c.k_stages / P) / kw) * kw * atoms;
-                const double t = rounds * n_atoms * std::max(std::max(arith, copies), latency) + (P > 1 ? 800.0 : 0.0) + tables / 100.0;
+                const double t = rounds * n_atoms * std::max(std::max(arith, copies), latency) + (P > 1 ? 800.0 : 0.0) +
+                                 tables / 100.0;
                 if (best == 0 || t < best_t || (fits && !best_fits)) {
                     best_t = t;
                     best_fits = fits;

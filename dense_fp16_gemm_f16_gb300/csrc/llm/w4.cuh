@@ -1,4 +1,4 @@
-// w4.cuh -- reading 16-bit and 4-bit weights one at a time.
+// w4.cuh -- eight 16-bit weights as fp32 numbers and back.
 #pragma once
 
 #include <cuda_bf16.h>

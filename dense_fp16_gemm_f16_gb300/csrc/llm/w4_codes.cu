@@ -243,7 +243,8 @@ w4_quantize_kernel(const T* __restrict__ W, int64_t rows, int64_t N, int64_t K, 
         // two buffers: the next tile's writes go to the other one
         if constexpr (std::is_same<T, __nv_bfloat16>::value) {
             if (__syncthreads_or(isinf(inv_mine)))
-                quantize_smallest<ASYM>(W, codes, tile.off[0], tile.off[1], tile.row_end, tile.k_left, shift, s_scale[buf], s_zero[buf]);
+                quantize_smallest<ASYM>(W, codes, tile.off[0], tile.off[1], tile.row_end, tile.k_left, shift, s_scale[buf],
+                                        s_zero[buf]);
         } else {
             __syncthreads();
         }
@@ -319,9 +320,11 @@ void quantize(const void* W, int64_t rows, int64_t N, int64_t K, int group, void
     const T* w = static_cast<const T*>(W);
     uint8_t* c = static_cast<uint8_t*>(codes);
     if (zeros != nullptr)
-        w4_quantize_kernel<T, true><<<grid, kCodesThreads, 0, s>>>(w, rows, N, K, k_tiles_of(K), tiles, shift_of(group), c, static_cast<T*>(scales), static_cast<T*>(zeros));
+        w4_quantize_kernel<T, true><<<grid, kCodesThreads, 0, s>>>(w, rows, N, K, k_tiles_of(K), tiles, shift_of(group), c,
+                                                                   static_cast<T*>(scales), static_cast<T*>(zeros));
     else
-        w4_quantize_kernel<T, false><<<grid, kCodesThreads, 0, s>>>(w, rows, N, K, k_tiles_of(K), tiles, shift_of(group), c, static_cast<T*>(scales), nullptr);
+        w4_quantize_kernel<T, false><<<grid, kCodesThreads, 0, s>>>(w, rows, N, K, k_tiles_of(K), tiles, shift_of(group), c,
+                                                                    static_cast<T*>(scales), nullptr);
 }
 
 template <class T>

@@ -15,7 +15,8 @@ gemm_status_t launch(const void* A, const Weights& w, void* D, int64_t row0, int
     const SideGroups sg(w, K);
     p.N = static_cast<int32_t>(N);
     p.K = static_cast<int32_t>(K);
-    const int smem = plan_rows<true, NT, false>(reinterpret_cast<const void*>(weight_rows_kernel<T, CPG, NT, false>), &p, M, M, M, 1, sg.atom_groups, 0, dev);
+    const int smem = plan_rows<true, NT, false>(reinterpret_cast<const void*>(weight_rows_kernel<T, CPG, NT, false>), &p,
+                                                M, M, M, 1, sg.atom_groups, 0, dev);
     if (smem <= 0) return GEMM_ERR_CUDA;
     p.groups_k = sg.groups_k;
     p.atom_groups = sg.atom_groups;
@@ -29,8 +30,10 @@ gemm_status_t launch(const void* A, const Weights& w, void* D, int64_t row0, int
     p.status = dev.status;
     p.timeout_ns = kStreamTimeoutNs;
     CUtensorMap tw, ts, tz;
-    if (!encode_weights(w, N, sg.groups_k, N, K, p.width, p.width, p.ring.atoms * sg.atom_groups, &tw, &ts, &tz)) return GEMM_ERR_INVALID_VALUE;
-    return launch_stream(weight_rows_kernel<T, CPG, NT, false>, dev.dev, p.ranges * p.pieces, p.pieces, smem, true, s, tw, ts, tz, p);
+    if (!encode_weights(w, N, sg.groups_k, N, K, p.width, p.width, p.ring.atoms * sg.atom_groups, &tw, &ts, &tz))
+        return GEMM_ERR_INVALID_VALUE;
+    return launch_stream(weight_rows_kernel<T, CPG, NT, false>, dev.dev, p.ranges * p.pieces, p.pieces, smem, true, s, tw,
+                         ts, tz, p);
 }
 
 template <class T, int CPG>

@@ -29,10 +29,12 @@ TileShape tile_shape(int64_t M, int64_t N, int64_t K, const DeviceView& dev) {
     const int64_t atoms = (K + 255) / 256, tiles = static_cast<int64_t>(t.m_tiles) * t.n_tiles;
     const double block = std::max(kMmaClocksPerRow * t.rows_a, PAIRS ? kPairClocks : kDecodeClocks);
     for (int s = 1; s <= 8 && s <= atoms; s *= 2) {
-        const int at_once = active_clusters(reinterpret_cast<const void*>(w4_tiles_kernel<T, PAIRS, 1>), dev, kTileThreads, kMaxDynamicSmem, s);
+        const int at_once = active_clusters(reinterpret_cast<const void*>(w4_tiles_kernel<T, PAIRS, 1>), dev, kTileThreads,
+                                            kMaxDynamicSmem, s);
         if (at_once < 1) continue;
         const double rounds = static_cast<double>((tiles + at_once - 1) / at_once);
-        const double c = rounds * (4.0 * static_cast<double>((atoms + s - 1) / s) * block + kTileFixedClocks) + (s > 1 ? kTileExchangeClocks : 0.0);
+        const double c = rounds * (4.0 * static_cast<double>((atoms + s - 1) / s) * block + kTileFixedClocks) +
+                         (s > 1 ? kTileExchangeClocks : 0.0);
         if (t.split == 0 || c < t.clocks) {
             t.split = s;
             t.clocks = c;
@@ -81,7 +83,8 @@ gemm_status_t launch(const void* A, const Weights& w, void* D, int64_t M, int64_
         return GEMM_ERR_INVALID_VALUE;
     const int64_t ctas = static_cast<int64_t>(t.m_tiles) * t.n_tiles * t.split;
     if (ctas > INT32_MAX) return GEMM_ERR_INVALID_VALUE;
-    return launch_clusters(w4_tiles_kernel<T, PAIRS, KB>, dev.dev, static_cast<int>(ctas), kTileThreads, t.split, smem, true, s, tw, ts, tz, ta, p);
+    return launch_clusters(w4_tiles_kernel<T, PAIRS, KB>, dev.dev, static_cast<int>(ctas), kTileThreads, t.split, smem,
+                           true, s, tw, ts, tz, ta, p);
 }
 
 template <class T>
@@ -90,7 +93,8 @@ gemm_status_t run(const void* A, const Weights& w, void* D, int64_t M, int64_t N
     const TileShape t = M <= 64 ? tile_shape<T, true>(M, N, K, dev) : tile_shape<T, false>(M, N, K, dev);
     if (t.split == 0) return GEMM_ERR_CUDA;
     if (M <= 64) return launch<T, true, 1>(A, w, D, M, N, K, epi, t, dev, s);
-    return t.rows_a <= 128 ? launch<T, false, 2>(A, w, D, M, N, K, epi, t, dev, s) : launch<T, false, 1>(A, w, D, M, N, K, epi, t, dev, s);
+    return t.rows_a <= 128 ? launch<T, false, 2>(A, w, D, M, N, K, epi, t, dev, s)
+                           : launch<T, false, 1>(A, w, D, M, N, K, epi, t, dev, s);
 }
 
 }  // namespace
