@@ -161,16 +161,14 @@ moe_logits_kernel(const LogitsParams p, const ChoiceParams c) {
     float acc[NT][4] = {};
     // steps of 32 k, dealt in turn to the cluster's warps
     constexpr int kUnroll = NT <= 2 ? 4 : 2;
-    const int stride = P * kRouteWarps;
-    const int steps = p.H / 32 + (p.H % 32 != 0);   // counted in steps: an element past the end may pass 2^31
+    const uint32_t stride = P * kRouteWarps, H = p.H;   // unsigned: an element past the end may pass 2^31
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    for (int s = j * kRouteWarps + warp; s < steps; s += kUnroll * stride) {
+    for (uint32_t s = j * kRouteWarps + warp; s * 32u < H; s += kUnroll * stride) {
         uint4 a[kUnroll][2], b[kUnroll][NT];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int step = s + u * stride;
-            const int64_t k = static_cast<int64_t>(step) * 32;
-            const bool in = step < steps && k + t * 8 < p.H;   // H is a multiple of 8
+            const uint32_t k = (s + u * stride) * 32u;
+            const bool in = k + t * 8u < H;   // H is a multiple of 8
             a[u][0] = in ? *reinterpret_cast<const uint4*>(w0 + k) : zero;
             a[u][1] = in ? *reinterpret_cast<const uint4*>(w1 + k) : zero;
 #pragma unroll
