@@ -1,5 +1,5 @@
-// llm.h -- launch entry points of the 4-bit-weight and mixture-of-experts
-// kernels.  Arguments are checked by llm_api.cu before these are called.
+// llm.h -- launch entry points of the 4-bit-weight, mixture-of-experts,
+// normalisation and adapter kernels.  Arguments are checked by llm_api.cu before these are called.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -57,6 +57,17 @@ gemm_status_t run_w4_tiles(bool bf16, const void* A, const Weights& w, void* D, 
 
 gemm_status_t run_w4_gemm(bool bf16, const void* A, const Weights& w, void* D, int64_t M, int64_t N, int64_t K,
                           const EpiParams& epi, const DeviceView& dev, gemm_stream_t stream);
+
+struct NormArgs {
+    const void *X, *residual, *weight;
+    void *Y, *Y8;
+    float* scales;        // nullptr: `scale` for every row
+    void* total;
+    int64_t T, H;
+    float eps, scale;
+    bool e5m2;
+};
+gemm_status_t run_rmsnorm(bool bf16, const NormArgs& a, const DeviceView& dev, cudaStream_t s);
 
 // bytes of scratch that run_route needs at `data`; counters: one zero, left at zero
 size_t route_scratch_bytes(int64_t T, int64_t E);

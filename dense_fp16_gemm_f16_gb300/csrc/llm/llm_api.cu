@@ -2,6 +2,7 @@
 // per-stream scratch and the calls into the kernels' launchers.  Nothing here
 // computes on the CPU.
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <map>
 #include <mutex>
@@ -305,6 +306,46 @@ gemm_status_t layer(int dtype, const void* X, const void* Wr, const float* bias,
     return run_ffn(bf16, p, ws.data + logits + 2 * side, dev, stream);
 }
 
+gemm_status_t rmsnorm(int dtype, const void* X, const void* residual, const void* weight, float eps, int64_t T, int64_t H,
+                      const gemm_norm_out_t* out, gemm_stream_t stream) {
+    if (!type16(dtype) || !dim_ok(T) || !dim_ok(H) || out == nullptr) return GEMM_ERR_INVALID_VALUE;
+    if (!(eps >= 0.0f) || eps > FLT_MAX) return GEMM_ERR_INVALID_VALUE;
+    if (out->Y == nullptr && out->Y8 == nullptr && T > 0 && H > 0) return GEMM_ERR_INVALID_VALUE;
+    const bool eight = out->Y8 != nullptr;
+    if (eight && out->dtype8 != GEMM_DTYPE_E4M3 && out->dtype8 != GEMM_DTYPE_E5M2) return GEMM_ERR_INVALID_VALUE;
+    // one scale for all rows, or a place for one per row, and neither without an 8-bit output
+    const bool fixed = out->scale != 0.0f;
+    if (fixed && (!(out->scale > 0.0f) || out->scale > FLT_MAX)) return GEMM_ERR_INVALID_VALUE;
+    if (eight ? fixed == (out->scales != nullptr) : fixed || out->scales != nullptr) return GEMM_ERR_INVALID_VALUE;
+    if (T == 0 || H == 0) return GEMM_OK;
+    if (X == nullptr) return GEMM_ERR_INVALID_VALUE;
+    if (H % 8 != 0) return GEMM_ERR_MISALIGNED;
+    if (!aligned16(X) || !aligned16(residual) || !aligned16(weight) || !aligned16(out->Y) || !aligned16(out->Y8) ||
+        !aligned16(out->scales) || !aligned16(out->total))
+        return GEMM_ERR_MISALIGNED;
+    if (mul_sat(T, H) < 0) return GEMM_ERR_INVALID_VALUE;
+    // Y and total may be X or the residual themselves (a row is read before it is
+    // written); no output may overlap anything else
+    const struct { const void* p; int64_t bytes; } outs[4] = {{out->Y, T * H * 2}, {out->total, T * H * 2},
+                                                              {out->Y8, T * H}, {out->scales, T * 4}};
+    for (int i = 0; i < 4; ++i) {
+        if (outs[i].p == nullptr) continue;
+        for (const void* in : {X, residual})
+            if (in != nullptr && ranges_overlap(outs[i].p, outs[i].bytes, in, T * H * 2) && (i > 1 || outs[i].p != in))
+                return GEMM_ERR_INVALID_VALUE;
+        if (weight != nullptr && ranges_overlap(outs[i].p, outs[i].bytes, weight, H * 2)) return GEMM_ERR_INVALID_VALUE;
+        for (int j = 0; j < i; ++j)
+            if (outs[j].p != nullptr && ranges_overlap(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes))
+                return GEMM_ERR_INVALID_VALUE;
+    }
+    DeviceView dev;
+    const gemm_status_t st = device_view(&dev);
+    if (st != GEMM_OK) return st;
+    const NormArgs a{X, residual, weight, out->Y, out->Y8, out->scales, out->total, T, H, eps, out->scale,
+                     out->dtype8 == GEMM_DTYPE_E5M2};
+    return run_rmsnorm(dtype == GEMM_DTYPE_BF16, a, dev, reinterpret_cast<cudaStream_t>(stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -322,6 +363,11 @@ GEMM_API gemm_status_t gemm_w4_dequantize(gemm_dtype_t dtype, const gemm_weights
 GEMM_API gemm_status_t gemm_w4_nt(gemm_dtype_t dtype, const void* A, const gemm_weights_t* B, void* D, int64_t M,
                                   int64_t N, int64_t K, const gemm_epilogue_t* epilogue, gemm_stream_t stream) {
     return guarded([&] { return w4_nt(dtype, A, B, D, M, N, K, epilogue, stream); });
+}
+
+GEMM_API gemm_status_t gemm_rmsnorm(gemm_dtype_t dtype, const void* X, const void* residual, const void* weight, float eps,
+                                    int64_t T, int64_t H, const gemm_norm_out_t* out, gemm_stream_t stream) {
+    return guarded([&] { return rmsnorm(dtype, X, residual, weight, eps, T, H, out, stream); });
 }
 
 GEMM_API gemm_status_t gemm_moe_route(gemm_dtype_t dtype, const void* X, const void* Wr, const float* bias, int64_t T,

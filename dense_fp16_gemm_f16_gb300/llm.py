@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import enum
+import typing
 
 import dense_fp16_gemm_f16_gb300 as _g
 
@@ -48,12 +49,27 @@ class W4:
         return (*s[:-1], s[-1] * 2)
 
 
+class NormOut(ctypes.Structure):
+    """Mirror of gemm_norm_out_t."""
+    _fields_ = [("Y", ctypes.c_void_p), ("Y8", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("total", ctypes.c_void_p),
+                ("dtype8", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class Normed(typing.NamedTuple):
+    """What gemm_rmsnorm wrote; None for what was not asked for."""
+    Y: object
+    Y8: object
+    scales: object
+    total: object
+
+
 def declare(lib) -> None:
     p, i64, i32, w = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.POINTER(Weights)
     for name, args in {
         "gemm_w4_quantize": [i32, p, i64, i64, i64, i32, p, p, p, p],
         "gemm_w4_dequantize": [i32, w, i64, i64, i64, p, p],
         "gemm_w4_nt": [i32, p, w, p, i64, i64, i64, ctypes.POINTER(_g.Epilogue), p],
+        "gemm_rmsnorm": [i32, p, p, p, ctypes.c_float, i64, i64, ctypes.POINTER(NormOut), p],
         "gemm_moe_route": [i32, p, p, p, i64, i64, i64, i32, i32, i32, p, p, p],
         "gemm_moe_ffn": [i32, p, p, p, w, w, p, i64, i64, i64, i64, i32, p],
         "gemm_moe_layer": [i32, p, p, p, w, w, p, i64, i64, i64, i64, i32, i32, i32, p],
@@ -66,6 +82,7 @@ def declare(lib) -> None:
 _torch = None
 _lib = None
 _dtypes: dict = {}
+_dtypes8: dict = {}
 _raw_stream = None
 _current_device = None
 
@@ -76,6 +93,7 @@ def _setup():
     lib = _g.load()
     import torch
     _dtypes.update({torch.float16: int(_g.Dtype.F16), torch.bfloat16: int(_g.Dtype.BF16)})
+    _dtypes8.update({torch.float8_e4m3fn: int(_g.Dtype.E4M3), torch.float8_e5m2: int(_g.Dtype.E5M2)})
     # the current stream's handle without a Stream object around it, which
     # costs 2 us of the 8 that a small call takes
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
@@ -226,6 +244,58 @@ def gemm_w4_nt(A, B: W4, D, alpha=1.0, beta=0.0, C=None, bias=None, activation=_
             None if bias is None else _check(bias, "bias", dtype, (N,), index), int(activation), 0,
             None if scale_n is None else _check(scale_n, "scale_n", _torch.float32, (N,), index)))
     _run(lib.gemm_w4_nt, index, stream, (dt, A.data_ptr(), ctypes.byref(w), d, M, N, K, epi))
+
+
+def gemm_rmsnorm(X, weight=None, residual=None, eps: float = 1e-6, Y=None, Y8=None, scales=None, total=None,
+                 scale: float | None = None, stream=None) -> Normed:
+    """y = h / sqrt(mean(h², per row) + eps) · weight of h = X + residual, in 16 bits, 8 bits or both.
+
+    X, residual, Y and total are [T, H], weight [H], all of one 16-bit type.  ``Y8`` is a
+    float8_e4m3fn or float8_e5m2 tensor [T, H], or the ``Dtype`` of one to allocate; with
+    it, ``scales`` float32 [T] (allocated unless given) gets max|y| of each row over the type's largest
+    number, unless ``scale`` gives one for all rows.  ``Y`` is allocated where neither Y nor Y8 is given.
+    ``total`` gets h; it and Y may be X or residual themselves.  The 8-bit rows are what
+    ``gemm_nt_ex(..., scale_m=scales)`` takes."""
+    lib = _lib or _setup()
+    index = _cuda(X, "X")
+    dt = _type16(X, "X")
+    if X.dim() != 2:
+        raise ValueError(f"X must be [T, H], got {tuple(X.shape)}")
+    shape = X.shape
+    T, H = shape
+    dtype = X.dtype
+    r = None if residual is None else _check(residual, "residual", dtype, shape, index)
+    w = None if weight is None else _check(weight, "weight", dtype, (H,), index)
+    if Y8 is None:
+        if scales is not None or scale is not None:
+            raise ValueError("scales belong to an 8-bit output")
+        if Y is None:
+            Y = _g._empty(shape, dtype, X.device, stream)
+        dt8, y8, sc = 0, None, None
+    else:
+        if not _g._is_tensor(Y8):
+            kinds = {v: k for k, v in _dtypes8.items()}
+            if not isinstance(Y8, (int, _g.Dtype)) or int(Y8) not in kinds:
+                raise TypeError("Y8 must be a float8 tensor, Dtype.E4M3 or Dtype.E5M2")
+            Y8 = _g._empty(shape, kinds[int(Y8)], X.device, stream)
+        dt8 = _dtypes8.get(Y8.dtype)
+        if dt8 is None:
+            raise TypeError(f"Y8 must be float8_e4m3fn or float8_e5m2, got {Y8.dtype}")
+        y8 = _check(Y8, "Y8", Y8.dtype, shape, index)
+        if scale is not None:
+            if scales is not None:
+                raise ValueError("give scale or scales, not both")
+            if not 0.0 < scale < float("inf"):
+                raise ValueError(f"scale must be positive, got {scale}")
+            sc = None
+        else:
+            if scales is None:
+                scales = _g._empty((T,), _torch.float32, X.device, stream)
+            sc = _check(scales, "scales", _torch.float32, (T,), index)
+    out = NormOut(None if Y is None else _check(Y, "Y", dtype, shape, index), y8, sc,
+                  None if total is None else _check(total, "total", dtype, shape, index), dt8, scale or 0.0)
+    _run(lib.gemm_rmsnorm, index, stream, (dt, X.data_ptr(), r, w, eps, T, H, ctypes.byref(out)))
+    return Normed(Y, Y8, scales, total)
 
 
 def _tokens(X, Wr, bias):

@@ -1,6 +1,7 @@
 /*
- * gemm_llm.h -- C ABI of the operators that read weights in 4 bits and of the
- * mixture-of-experts layer, part of the library of gemm_f16.h.
+ * gemm_llm.h -- C ABI of the operators that read weights in 4 bits, of the
+ * mixture-of-experts layer, of the norm between products and of low-rank adapters
+ * beside a product, part of the library of gemm_f16.h.
  *
  * The conventions of gemm_f16.h hold for every entry point here: device
  * pointers owned by the caller, dense row-major arrays, 16-byte aligned bases,
@@ -96,6 +97,43 @@ GEMM_API gemm_status_t gemm_w4_dequantize(gemm_dtype_t dtype, const gemm_weights
  */
 GEMM_API gemm_status_t gemm_w4_nt(gemm_dtype_t dtype, const void* A, const gemm_weights_t* B, void* D, int64_t M,
                                   int64_t N, int64_t K, const gemm_epilogue_t* epilogue, gemm_stream_t stream);
+
+/*
+ * What gemm_rmsnorm writes: Y, Y8 or both, and the sum.
+ *   Y       [T][H] in the call's dtype, or NULL
+ *   Y8      [T][H] in 8 bits, or NULL
+ *   scales  [T] fp32, the scale of each row of Y8; NULL where `scale` is given
+ *   total   [T][H] in the call's dtype: X + residual; NULL where it is not wanted
+ *   dtype8  GEMM_DTYPE_E4M3 or GEMM_DTYPE_E5M2, the type of Y8
+ *   scale   0 for a scale per row, else one positive scale for every row of Y8
+ */
+typedef struct {
+    void* Y;
+    void* Y8;
+    float* scales;
+    void* total;
+    int32_t dtype8;
+    float scale;
+} gemm_norm_out_t;
+
+/*
+ * gemm_rmsnorm -- root-mean-square norm of the rows of X + residual, in fp32:
+ *     h = X + residual                                  (residual NULL: h = X)
+ *     y = h / sqrt(mean over the row of h^2 + eps) * weight      (NULL: ones)
+ *     Y = y rounded to dtype,  total = h rounded to dtype
+ *     scales[t] = max|y[t]| / F,  F = 448 (E4M3) or 57344 (E5M2)
+ *     Y8 = y / scale rounded to 8 bits, at most F in magnitude
+ * y is taken from h before its rounding and Y8 from y before its own.  A row whose
+ * y is all zero has scale 0 and codes 0.  A row that holds an infinity or NaN, or
+ * whose squares or products with the weight pass fp32's largest number, has
+ * NaN or zeros in Y as the formula gives them and unspecified scale and codes.
+ * X, residual, Y, total [T][H] and weight [H] in dtype; H a multiple of 8; eps >= 0.
+ * Y and total may each be X or residual itself; outputs overlap nothing else.
+ * T or H of zero is a no-op.  The 8-bit rows and their scales are what
+ * gemm_nt_scaled takes as A and scale_m.
+ */
+GEMM_API gemm_status_t gemm_rmsnorm(gemm_dtype_t dtype, const void* X, const void* residual, const void* weight, float eps,
+                                    int64_t T, int64_t H, const gemm_norm_out_t* out, gemm_stream_t stream);
 
 typedef enum {
     GEMM_MOE_SOFTMAX = 0,   /* p = softmax of the token's E logits */
