@@ -120,6 +120,8 @@ def load():
         lib.gemm_bf16_nt.restype = ctypes.c_int
         lib.gemm_nt_ex.argtypes = [ctypes.c_int, p, p, p, i64, i64, i64, ctypes.POINTER(Epilogue), ctypes.c_int, p]
         lib.gemm_nt_ex.restype = ctypes.c_int
+        lib.gemm_nt_scaled.argtypes = [ctypes.c_int, p, p, p, p, i64, i64, i64, ctypes.POINTER(Epilogue), p]
+        lib.gemm_nt_scaled.restype = ctypes.c_int
         lib.gemm_nt_plan_ex.argtypes = [ctypes.c_int, i64, i64, i64, ctypes.c_int, ctypes.c_int32,
                                         ctypes.POINTER(Plan)]
         lib.gemm_nt_plan_ex.restype = ctypes.c_int
@@ -270,13 +272,18 @@ def _tensor_dtype(A):
 
 
 def gemm_nt_ex(A, B, D, M=None, N=None, K=None, dtype=None, alpha=1.0, beta=0.0, C=None, bias=None,
-               activation=Activation.NONE, variant=Variant.AUTO, stream=None, scale_n=None) -> None:
-    """D = act(alpha·scale_n[n]·A·Bᵀ + beta·C + bias[n]).
+               activation=Activation.NONE, variant=Variant.AUTO, stream=None, scale_n=None, scale_m=None) -> None:
+    """D = act(alpha·scale_m[m]·scale_n[n]·A·Bᵀ + beta·C + bias[n]).
 
     Operands fp16, bf16, or 8-bit (E4M3 / E5M2, as torch float8 or uint8
     tensors; D, C and bias are then bf16); the dtype is taken from the tensors
     unless given (uint8 tensors need it).  ``scale_n`` is an optional float32
-    [N] tensor (or device pointer) of per-column scales."""
+    [N] tensor (or device pointer) of per-column scales, ``scale_m`` an optional float32
+    [M] one of per-row scales (8-bit operands and ``Variant.AUTO`` only: ``gemm_nt_scaled``)."""
+    if scale_m is not None and Variant(variant) != Variant.AUTO:
+        raise ValueError("scale_m needs Variant.AUTO")
+    if scale_m is not None and _is_tensor(A):
+        return _llm.nt_scaled(A, B, D, (M, N, K), dtype, alpha, beta, C, bias, activation, stream, scale_n, scale_m)
     if dtype is None:
         dtype = _tensor_dtype(A) if _is_tensor(A) else Dtype.F16
     a, b, d, m, n, k, dev = _operands(A, B, D, M, N, K, Dtype(dtype))
@@ -294,6 +301,11 @@ def gemm_nt_ex(A, B, D, M=None, N=None, K=None, dtype=None, alpha=1.0, beta=0.0,
         import torch
         sc = ptr(scale_n, "scale_n", torch.float32)
     epi = Epilogue(float(alpha), float(beta), ptr(C), ptr(bias), int(activation), 0, sc)
+    if scale_m is not None:
+        import torch
+        _call("gemm_nt_scaled", (int(dtype), a or None, ptr(scale_m, "scale_m", torch.float32), b or None, d or None,
+                                 m, n, k, ctypes.byref(epi), _stream_handle(stream, dev)), dev)
+        return
     _call("gemm_nt_ex", (int(dtype), a or None, b or None, d or None, m, n, k, ctypes.byref(epi), int(variant),
                          _stream_handle(stream, dev)), dev)
 

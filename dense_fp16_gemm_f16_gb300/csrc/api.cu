@@ -549,13 +549,15 @@ gemm_status_t get_device(DeviceState** out, int* dev_out) {
             return GEMM_ERR_CUDA;
         }
         const TiledOps* tiled[3] = {&tiled_ops_2cta256(0), &tiled_ops_1cta128(0), &tiled_ops_1cta256(0)};
-        for (int dt : {0, 1, 2}) {   // fp16, bf16, 8-bit (one kernel for both formats)
+        // fp16, bf16, 8-bit (one kernel for both formats), 8-bit with row scales
+        for (int dt : {0, 1, 2, kOpsRowScaled}) {
             const TiledOps* all[4] = {&tiled_ops_2cta256(dt), &tiled_ops_1cta128(dt), &tiled_ops_1cta256(dt),
                                       &tiled_ops_2cta512(dt)};
             for (const TiledOps* t : all)
                 if (t->prepare() != cudaSuccess) { cudaGetLastError(); return GEMM_ERR_CUDA; }
             for (int mn : {16, 32, 64})
-                if (skinny_ops(mn, dt).prepare() != cudaSuccess || streamk_ops(mn, dt).prepare() != cudaSuccess) {
+                if (skinny_ops(mn, dt).prepare() != cudaSuccess ||
+                    (dt != kOpsRowScaled && streamk_ops(mn, dt).prepare() != cudaSuccess)) {
                     cudaGetLastError();
                     return GEMM_ERR_CUDA;
                 }
@@ -704,15 +706,23 @@ __global__ void epilogue_only_kernel(T* D, int64_t M, int64_t N, EpiParams e) {
 
 gemm_status_t run(const void* A, const void* B, void* D, int64_t M, int64_t N, int64_t K,
                   gemm_variant_t variant, gemm_stream_t stream, int dtype = 0,
-                  const gemm_epilogue_t* epilogue = nullptr) {
+                  const gemm_epilogue_t* epilogue = nullptr, const float* scale_m = nullptr) {
     // ---- host-only argument checks (nothing touches a device before these pass)
     if (!dtype_valid(dtype)) return GEMM_ERR_INVALID_VALUE;
     const int in_bytes = dtype_in_bytes(dtype);
     gemm_status_t st = check_sizes(M, N, K, in_bytes);
     if (st != GEMM_OK) return st;
-    const EpiParams epi = epi_params(epilogue);
+    EpiParams epi = epi_params(epilogue);
     st = check_epilogue(epilogue, D, M, N);
     if (st != GEMM_OK) return st;
+    if (scale_m != nullptr) {
+        if (!aligned16(scale_m)) return GEMM_ERR_MISALIGNED;
+        if (ranges_overlap(scale_m, M * 4, D, M * N * 2)) return GEMM_ERR_INVALID_VALUE;
+        if (K > 0) {   // the empty sum is zero whatever the scales
+            epi.scale_m = scale_m;
+            epi.on = 1;
+        }
+    }
     if (variant < GEMM_VARIANT_AUTO || variant > GEMM_VARIANT_TILE_1CTA_SPLITK) return GEMM_ERR_INVALID_VALUE;
     if ((variant == GEMM_VARIANT_SKINNY_SPLITK || variant == GEMM_VARIANT_SKINNY_STREAMK) && M > 64)
         return GEMM_ERR_INVALID_VALUE;
@@ -731,6 +741,7 @@ gemm_status_t run(const void* A, const void* B, void* D, int64_t M, int64_t N, i
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int out_dtype = dtype_out(dtype);
     const int bk = stage_k(in_bytes);
+    const int kernels = epi.scale_m != nullptr ? kOpsRowScaled : dtype;
 
     if (K == 0) return run_empty_sum(D, M, N, epi, out_dtype, dev->sms, s);
 
@@ -739,7 +750,7 @@ gemm_status_t run(const void* A, const void* B, void* D, int64_t M, int64_t N, i
     if (st != GEMM_OK) return st;
 
     if (pl.variant == GEMM_VARIANT_SKINNY_SPLITK) {
-        const SkinnyOps& ops = skinny_ops(pl.tile_m, dtype);
+        const SkinnyOps& ops = skinny_ops(pl.tile_m, kernels);
         CUtensorMap tw, tx;
         if (!encode_2d(&tw, B, K, N, bk, static_cast<uint32_t>(pl.tile_n), dtype, kStreamL2Promotion) ||
             !encode_2d(&tx, A, K, M, bk, static_cast<uint32_t>(ops.mn), dtype, kStreamL2Promotion))
@@ -810,7 +821,7 @@ gemm_status_t run(const void* A, const void* B, void* D, int64_t M, int64_t N, i
         return GEMM_OK;
     }
 
-    const TiledOps& ops = tiled_ops_of(static_cast<gemm_variant_t>(pl.variant), dtype);
+    const TiledOps& ops = tiled_ops_of(static_cast<gemm_variant_t>(pl.variant), kernels);
     CUtensorMap ta, tb, tbp, td;
     const uint32_t b_rows = static_cast<uint32_t>(ops.b_box_rows);
     if (!encode_2d(&ta, A, K, M, bk, 128, dtype) || !encode_2d(&tb, B, K, N, bk, b_rows, dtype) ||
@@ -1045,6 +1056,7 @@ EpiParams epi_params(const gemm_epilogue_t* e) {
     p.scale_n = nullptr;
     p.act = 0;
     p.on = 0;
+    p.scale_m = nullptr;
     if (e == nullptr) return p;
     p.alpha = e->alpha;
     p.beta = e->beta;
@@ -1079,6 +1091,14 @@ GEMM_API gemm_status_t gemm_nt_ex(gemm_dtype_t dtype, const void* A, const void*
                                   int64_t K, const gemm_epilogue_t* epilogue, gemm_variant_t variant,
                                   gemm_stream_t stream) {
     return run(A, B, D, M, N, K, variant, stream, static_cast<int>(dtype), epilogue);
+}
+
+GEMM_API gemm_status_t gemm_nt_scaled(gemm_dtype_t dtype, const void* A, const float* scale_m, const void* B, void* D,
+                                      int64_t M, int64_t N, int64_t K, const gemm_epilogue_t* epilogue,
+                                      gemm_stream_t stream) {
+    if (dtype != GEMM_DTYPE_E4M3 && dtype != GEMM_DTYPE_E5M2) return GEMM_ERR_INVALID_VALUE;
+    if (scale_m == nullptr && M > 0 && N > 0) return GEMM_ERR_INVALID_VALUE;
+    return run(A, B, D, M, N, K, GEMM_VARIANT_AUTO, stream, static_cast<int>(dtype), epilogue, scale_m);
 }
 
 GEMM_API gemm_status_t gemm_f16_nt_check(gemm_stream_t stream) {

@@ -13,7 +13,11 @@
 // the "epilogue fusion" the Croqtile tutorial credits cuBLAS with in its
 // comparison section.  s[n] is an optional fp32 scale per output column: the
 // per-channel weight scale of the blog post's 8-bit quantisation (section
-// 4.2), with the per-tensor activation scale folded into alpha.
+// 4.2), with the per-tensor activation scale folded into alpha.  The kernels of
+// 8-bit operands are also built with a scale per row of A (ROWS), which
+// multiplies the accumulator before the rest.  That is one more factor in an
+// epilogue that is not the bound: it is a build of its own so that the code of the others
+// stays what it was.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -31,6 +35,7 @@ struct EpiParams {
     const float* scale_n;  // [N] fp32, or nullptr
     int32_t act;        // 0 none, 1 relu
     int32_t on;         // 0: plain D = A B^T (the other fields are ignored)
+    const float* scale_m;  // [M] fp32: read only by the kernels built with row scales
 };
 
 template <class T>

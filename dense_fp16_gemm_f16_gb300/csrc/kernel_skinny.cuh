@@ -55,8 +55,19 @@ __device__ __forceinline__ void skinny_acc_sum(uint32_t taddr, uint32_t (&v)[MN]
     }
 }
 
-// T is the element type of D (and C, bias); F8 selects 8-bit operands.
-template <class Cfg, class T, bool F8>
+// This warp's columns of the accumulator times the scale of each row m, of which
+// lane l holds r[i] for m = 32 i + l.  Scaled before pieces of K are exchanged: a
+// row's scale is then at hand without a load behind the exchange.
+template <int MN>
+__device__ __forceinline__ void skinny_scale_rows(uint32_t (&v)[MN], const float (&r)[(MN + 31) / 32]) {
+#pragma unroll
+    for (int m = 0; m < MN; ++m)
+        v[m] = __float_as_uint(__uint_as_float(v[m]) * __shfl_sync(0xffffffffu, r[m / 32], m % 32));
+}
+
+// T is the element type of D (and C, bias); F8 selects 8-bit operands; ROWS = with
+// a scale per row of A.
+template <class Cfg, class T, bool F8, bool ROWS = false>
 __global__ void __launch_bounds__(kThreads, 1)
 gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                    const SkinnyParams p) {
@@ -224,6 +235,12 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         const int n_local = q * 32 + lane;   // TMEM lane = column within the range
         const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
         T* D = static_cast<T*>(p.D);
+        float row_scale[(MN + 31) / 32];
+        if constexpr (ROWS) {
+#pragma unroll
+            for (int i = 0; i < (MN + 31) / 32; ++i)
+                row_scale[i] = 32 * i + lane < p.M ? p.epi.scale_m[32 * i + lane] : 0.0f;
+        }
         if (!clustered) {
             // one whole K loop per range: straight from TMEM to D
             uint32_t it = 0;
@@ -239,6 +256,7 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                 ptx::tc_fence_after();
                 uint32_t v[MN];
                 skinny_acc_sum<MN, Cfg::ACCS>(t_lane + buf * Cfg::ACC_COLS, v);
+                if constexpr (ROWS) skinny_scale_rows<MN>(v, row_scale);
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(tempty_bar(buf));
@@ -271,6 +289,7 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
             if (ready) {
                 ptx::tc_fence_after();
                 skinny_acc_sum<MN, Cfg::ACCS>(t_lane, v);
+                if constexpr (ROWS) skinny_scale_rows<MN>(v, row_scale);
             } else {
 #pragma unroll
                 for (int m = 0; m < MN; ++m) v[m] = 0u;

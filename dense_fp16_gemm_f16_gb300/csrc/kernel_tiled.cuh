@@ -107,9 +107,10 @@ __device__ __forceinline__ void split_k_send(uint32_t recv_base, uint32_t t_row,
 
 // Sum of the S partials of this CTA's slice for row `row` (D row grow), in
 // ascending piece order, with the fused transform, written to D.
-template <class Cfg, class T>
+// ROWS: the sum is multiplied by the row's scale first.
+template <class Cfg, class T, bool ROWS>
 __device__ __forceinline__ void split_k_reduce(const uint8_t* recv, const TiledParams& p, int piece, int row,
-                                               int64_t grow, int64_t n0, int S) {
+                                               int64_t grow, int64_t n0, int S, float row_scale) {
     constexpr int kGroups = Cfg::BN / 8;
     const int slice_quads = 2 * ((kGroups + S - 1) / S);
     const int g0 = split_group_begin(piece, kGroups, S);
@@ -132,6 +133,10 @@ __device__ __forceinline__ void split_k_reduce(const uint8_t* recv, const TiledP
             acc[0] += lo.x; acc[1] += lo.y; acc[2] += lo.z; acc[3] += lo.w;
             acc[4] += hi.x; acc[5] += hi.y; acc[6] += hi.z; acc[7] += hi.w;
         }
+        if constexpr (ROWS) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] *= row_scale;
+        }
         if (p.epi.on) epi_apply8_c<T>(p.epi, acc, cv, gcol);
         uint32_t h[4];
 #pragma unroll
@@ -143,8 +148,8 @@ __device__ __forceinline__ void split_k_reduce(const uint8_t* recv, const TiledP
 // T is the element type of D (and C, bias); F8 selects 8-bit operands
 // (kind::f8f6f4, 128 K elements per stage) instead of 16-bit ones of type T;
 // KA = K blocks per ring stage (a compile-time constant, so the one-block
-// loops compile to straight-line issue code).
-template <class Cfg, class T, bool F8, int KA = 1>
+// loops compile to straight-line issue code); ROWS = with a scale per row of A.
+template <class Cfg, class T, bool F8, int KA = 1, bool ROWS = false>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
 gemm_tiled_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ CUtensorMap tmBpiece, const __grid_constant__ CUtensorMap tmD,
@@ -388,6 +393,9 @@ gemm_tiled_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
         int64_t tm = 0, n0 = 0;
         int nw = 0, kb0 = 0, kb1 = 0;
         if (u < p.num_units) work_unit(u, p, Cfg::BN, piece, tm, n0, nw, kb0, kb1);
+        const int64_t grow = tm * Cfg::BM + rank * 128 + row;   // the row of D
+        float row_scale = 1.0f;
+        if constexpr (ROWS) row_scale = grow < p.M ? p.epi.scale_m[grow] : 0.0f;
         const bool ready = u < p.num_units &&
                            wait_phase_warp(tfull_bar(0), 0, p.status, kSiteEpilogueTmemFull, p.timeout_ns);
         if (ready) ptx::tc_fence_after();
@@ -397,7 +405,7 @@ gemm_tiled_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                           p.ksplit);
         // B: every partial of this CTA's slice is in its receive buffer
         ptx::cluster_sync();
-        if (ready) split_k_reduce<Cfg, T>(smem, p, piece, row, tm * Cfg::BM + rank * 128 + row, n0, p.ksplit);
+        if (ready) split_k_reduce<Cfg, T, ROWS>(smem, p, piece, row, grow, n0, p.ksplit, row_scale);
     } else {
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3;    // TMEM lanes 32q .. 32q+31 are readable by this warp
@@ -427,9 +435,11 @@ gemm_tiled_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                 for (int c = 0; c < kChunks; ++c)
                     if (c < chunks) ev[c].load(p.epi, n0 + c * Cfg::EPI_COLS, lane, p.N);
             }
+            const int64_t row0 = tm * Cfg::BM + h * Cfg::MMA_M + rank * 128 + q * 32;  // D row of lane 0
+            float row_scale = 1.0f;
+            if constexpr (ROWS) row_scale = row0 + lane < p.M ? p.epi.scale_m[row0 + lane] : 0.0f;
             if (!wait_phase_warp(tfull_bar(buf), use, p.status, kSiteEpilogueTmemFull, p.timeout_ns)) break;
             ptx::tc_fence_after();
-            const int64_t row0 = tm * Cfg::BM + h * Cfg::MMA_M + rank * 128 + q * 32;  // D row of lane 0
             const bool rows_in = row0 < p.M;
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + (buf * CONS + h) * Cfg::BN;
 #pragma unroll 1
@@ -456,6 +466,10 @@ gemm_tiled_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                         if constexpr (CG == 2) ptx::mbar_arrive_cluster(tempty_leader0 + 8u * buf);
                         else ptx::mbar_arrive(tempty_bar(buf));
                     }
+                }
+                if constexpr (ROWS) {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * row_scale);
                 }
                 // the TMA store issued two chunks ago from this buffer has read it
                 if (lane == 0) ptx::bulk_wait_group_read<1>();

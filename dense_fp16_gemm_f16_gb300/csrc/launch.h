@@ -45,7 +45,9 @@ struct StreamKOps {
 };
 
 // dtype: 0 = fp16 operands and output, 1 = bf16, 2 / 3 = E4M3 / E5M2 operands
-// with a bf16 output
+// with a bf16 output, kOpsRowScaled = the latter with a scale per row of A (no
+// stream-K kernel: AUTO does not pick it)
+constexpr int kOpsRowScaled = 4;
 const TiledOps& tiled_ops_2cta256(int dtype);
 const TiledOps& tiled_ops_2cta512(int dtype);   // two consumers per CTA
 const TiledOps& tiled_ops_1cta128(int dtype);

@@ -6,18 +6,18 @@
 
 namespace gemm_gb300 {
 
-template <class Cfg, class T, bool F8>
+template <class Cfg, class T, bool F8, bool ROWS = false>
 struct TiledLauncher {
     // 1-CTA configurations also come with two K blocks per ring stage (for
     // launches made only of narrow column pieces)
     static constexpr int kMaxAtoms = Cfg::CG == 1 ? 2 : 1;
 
     static cudaError_t prepare() {
-        cudaError_t e = cudaFuncSetAttribute(gemm_tiled_kernel<Cfg, T, F8, 1>,
+        cudaError_t e = cudaFuncSetAttribute(gemm_tiled_kernel<Cfg, T, F8, 1, ROWS>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
         if constexpr (kMaxAtoms > 1) {
             if (e == cudaSuccess)
-                e = cudaFuncSetAttribute(gemm_tiled_kernel<Cfg, T, F8, 2>,
+                e = cudaFuncSetAttribute(gemm_tiled_kernel<Cfg, T, F8, 2, ROWS>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
         }
         return e;
@@ -36,9 +36,9 @@ struct TiledLauncher {
             attr[0].val.clusterDim.z = 1;
             cfg.attrs = attr;
             cfg.numAttrs = 1;
-            return cudaOccupancyMaxActiveClusters(out, gemm_tiled_kernel<Cfg, T, F8>, &cfg);
+            return cudaOccupancyMaxActiveClusters(out, gemm_tiled_kernel<Cfg, T, F8, 1, ROWS>, &cfg);
         } else {
-            return cudaOccupancyMaxActiveBlocksPerMultiprocessor(out, gemm_tiled_kernel<Cfg, T, F8>, Cfg::THREADS,
+            return cudaOccupancyMaxActiveBlocksPerMultiprocessor(out, gemm_tiled_kernel<Cfg, T, F8, 1, ROWS>, Cfg::THREADS,
                                                                  Cfg::SMEM_BYTES);
         }
     }
@@ -55,7 +55,7 @@ struct TiledLauncher {
         attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        return cudaOccupancyMaxActiveClusters(out, gemm_tiled_kernel<Cfg, T, F8>, &cfg);
+        return cudaOccupancyMaxActiveClusters(out, gemm_tiled_kernel<Cfg, T, F8, 1, ROWS>, &cfg);
     }
 
     static cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& b_piece,
@@ -84,10 +84,10 @@ struct TiledLauncher {
         cfg.attrs = attr;
         if constexpr (kMaxAtoms > 1) {
             if (p.stage_atoms == 2)
-                return cudaLaunchKernelEx(&cfg, gemm_tiled_kernel<Cfg, T, F8, 2>, a, b, b_piece, d, p);
+                return cudaLaunchKernelEx(&cfg, gemm_tiled_kernel<Cfg, T, F8, 2, ROWS>, a, b, b_piece, d, p);
         }
         if (p.stage_atoms != 1) return cudaErrorInvalidValue;
-        return cudaLaunchKernelEx(&cfg, gemm_tiled_kernel<Cfg, T, F8, 1>, a, b, b_piece, d, p);
+        return cudaLaunchKernelEx(&cfg, gemm_tiled_kernel<Cfg, T, F8, 1, ROWS>, a, b, b_piece, d, p);
     }
 
     static const TiledOps& ops() {
@@ -100,9 +100,10 @@ struct TiledLauncher {
 
 // The table for a gemm_dtype_t: fp16 operands and D (0), bf16 (1), or 8-bit
 // operands (2 = E4M3, 3 = E5M2; one kernel, the format is a launch
-// parameter) with a bf16 D.
+// parameter) with a bf16 D, or those with a scale per row of A (kOpsRowScaled).
 template <class Cfg>
 const TiledOps& tiled_ops_for(int dtype) {
+    if (dtype == kOpsRowScaled) return TiledLauncher<Cfg, __nv_bfloat16, true, true>::ops();
     if (dtype >= 2) return TiledLauncher<Cfg, __nv_bfloat16, true>::ops();
     if (dtype == 1) return TiledLauncher<Cfg, __nv_bfloat16, false>::ops();
     return TiledLauncher<Cfg, __half, false>::ops();

@@ -6,10 +6,10 @@
 namespace gemm_gb300 {
 namespace {
 
-template <class Cfg, class T, bool F8>
+template <class Cfg, class T, bool F8, bool ROWS = false>
 struct SkinnyLauncher {
     static cudaError_t prepare() {
-        return cudaFuncSetAttribute(gemm_skinny_kernel<Cfg, T, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(gemm_skinny_kernel<Cfg, T, F8, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     Cfg::SMEM_BYTES);
     }
     static cudaError_t max_active(int pieces, int* out) {
@@ -24,7 +24,7 @@ struct SkinnyLauncher {
         attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        return cudaOccupancyMaxActiveClusters(out, gemm_skinny_kernel<Cfg, T, F8>, &cfg);
+        return cudaOccupancyMaxActiveClusters(out, gemm_skinny_kernel<Cfg, T, F8, ROWS>, &cfg);
     }
     static cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, const SkinnyParams& p,
                               int grid_ctas, cudaStream_t stream) {
@@ -47,7 +47,7 @@ struct SkinnyLauncher {
             cfg.numAttrs = 2;
         }
         cfg.attrs = attr;
-        return cudaLaunchKernelEx(&cfg, gemm_skinny_kernel<Cfg, T, F8>, w, x, p);
+        return cudaLaunchKernelEx(&cfg, gemm_skinny_kernel<Cfg, T, F8, ROWS>, w, x, p);
     }
     static const SkinnyOps& ops() {
         static const SkinnyOps o = {Cfg::MN,         Cfg::RING_BYTES, Cfg::X_BYTES, Cfg::MAX_ATOMS,
@@ -59,6 +59,7 @@ struct SkinnyLauncher {
 
 template <class Cfg>
 const SkinnyOps& skinny_ops_for(int dtype) {
+    if (dtype == kOpsRowScaled) return SkinnyLauncher<Cfg, __nv_bfloat16, true, true>::ops();
     if (dtype >= 2) return SkinnyLauncher<Cfg, __nv_bfloat16, true>::ops();
     if (dtype == 1) return SkinnyLauncher<Cfg, __nv_bfloat16, false>::ops();
     return SkinnyLauncher<Cfg, __half, false>::ops();

@@ -222,6 +222,41 @@ def gemm_w4_dequantize(W: W4, out=None, stream=None):
     return out
 
 
+def _epilogue(dtype, M, N, index, alpha, beta, C, bias, activation, scale_n):
+    """The fused output transform of a product as the library takes it; None where there is none."""
+    if alpha == 1.0 and beta == 0.0 and bias is None and scale_n is None and not activation:
+        return None
+    return ctypes.byref(_g.Epilogue(
+        float(alpha), float(beta), None if C is None else _check(C, "C", dtype, (M, N), index),
+        None if bias is None else _check(bias, "bias", dtype, (N,), index), int(activation), 0,
+        None if scale_n is None else _check(scale_n, "scale_n", _torch.float32, (N,), index)))
+
+
+def nt_scaled(A, B, D, sizes, dtype, alpha, beta, C, bias, activation, stream, scale_n, scale_m) -> None:
+    """gemm_nt_ex of tensors with a scale per row of A."""
+    lib = _lib or _setup()
+    index = _cuda(A, "A")
+    kind = A.dtype
+    dt = _dtypes8.get(kind)
+    if dt is None:
+        dt = -1 if dtype is None else int(dtype)
+        if kind is not _torch.uint8 or dt not in _dtypes8.values():
+            raise TypeError("scale_m belongs to 8-bit operands: float8 tensors, or uint8 ones with their Dtype")
+    elif dtype is not None and int(dtype) != dt:
+        raise TypeError(f"A is {kind}, not {_g.Dtype(dtype).name}")
+    if A.dim() != 2 or not _g._is_tensor(B) or B.dim() != 2:
+        raise ValueError("A and B must be matrices")
+    M, K = A.shape
+    N = B.shape[0]
+    for name, given, actual in zip("MNK", sizes, (M, N, K)):
+        if given is not None and given != actual:
+            raise ValueError(f"{name}={given} does not match the tensors ({actual})")
+    b, out = _check(B, "B", kind, (N, K), index), _torch.bfloat16
+    sm, d = _check(scale_m, "scale_m", _torch.float32, (M,), index), _check(D, "D", out, (M, N), index)
+    epi = _epilogue(out, M, N, index, alpha, beta, C, bias, activation, scale_n)
+    _run(lib.gemm_nt_scaled, index, stream, (dt, A.data_ptr(), sm, b, d, M, N, K, epi))
+
+
 def gemm_w4_nt(A, B: W4, D, alpha=1.0, beta=0.0, C=None, bias=None, activation=_g.Activation.NONE, stream=None,
                scale_n=None) -> None:
     """D = act(alpha·scale_n[n]·A·Bᵀ + beta·C + bias[n]) with the weights B [N, K] in 4 bits."""
@@ -237,12 +272,7 @@ def gemm_w4_nt(A, B: W4, D, alpha=1.0, beta=0.0, C=None, bias=None, activation=_
     dtype = A.dtype
     w = _weights(B, "B", dtype, (), N, K, index)
     d = _check(D, "D", dtype, (M, N), index)
-    epi = None
-    if alpha != 1.0 or beta != 0.0 or bias is not None or scale_n is not None or activation:
-        epi = ctypes.byref(_g.Epilogue(
-            float(alpha), float(beta), None if C is None else _check(C, "C", dtype, (M, N), index),
-            None if bias is None else _check(bias, "bias", dtype, (N,), index), int(activation), 0,
-            None if scale_n is None else _check(scale_n, "scale_n", _torch.float32, (N,), index)))
+    epi = _epilogue(dtype, M, N, index, alpha, beta, C, bias, activation, scale_n)
     _run(lib.gemm_w4_nt, index, stream, (dt, A.data_ptr(), ctypes.byref(w), d, M, N, K, epi))
 
 

@@ -213,6 +213,18 @@ GEMM_API gemm_status_t gemm_nt_ex(gemm_dtype_t dtype, const void* A, const void*
                                   gemm_variant_t variant, gemm_stream_t stream);
 
 /*
+ * gemm_nt_scaled -- gemm_nt_ex for 8-bit operands (GEMM_DTYPE_E4M3, GEMM_DTYPE_E5M2)
+ * quantised with a scale per row of A, as gemm_rmsnorm (gemm_llm.h) leaves them:
+ *     D = act(alpha * scale_m[m] * scale_n[n] * (A B^T) + beta * C + bias[n])
+ *   scale_m  [M] fp32, device memory, 16-byte aligned, must not overlap D
+ * Everything else as for gemm_nt_ex with GEMM_VARIANT_AUTO.  Errors: also
+ * GEMM_ERR_INVALID_VALUE for a 16-bit dtype or a NULL scale_m with work to do.
+ */
+GEMM_API gemm_status_t gemm_nt_scaled(gemm_dtype_t dtype, const void* A, const float* scale_m, const void* B, void* D,
+                                      int64_t M, int64_t N, int64_t K, const gemm_epilogue_t* epilogue,
+                                      gemm_stream_t stream);
+
+/*
  * gemm_f16_nt_check -- synchronise `stream`, then report and clear the
  * device-side status word of the current device.  Returns GEMM_OK,
  * GEMM_ERR_TIMEOUT if any kernel since the last check gave up waiting on a
