@@ -349,5 +349,5 @@ def gemm(A, B, variant=Variant.AUTO, stream=None):
 
 
 from . import llm as _llm  # noqa: E402  (needs the names above)
-from .llm import (W4, MoeScoring, Normed, gemm_moe_ffn, gemm_moe_layer, gemm_moe_route,  # noqa: E402,F401
-                  gemm_rmsnorm, gemm_w4_dequantize, gemm_w4_nt, gemm_w4_quantize)
+from .llm import (Lora, MoeScoring, Normed, W4, gemm_lora_delta, gemm_lora_nt, gemm_moe_ffn,  # noqa: E402,F401
+                  gemm_moe_layer, gemm_moe_route, gemm_rmsnorm, gemm_w4_dequantize, gemm_w4_nt, gemm_w4_quantize)

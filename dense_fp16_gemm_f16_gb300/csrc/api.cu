@@ -706,7 +706,7 @@ __global__ void epilogue_only_kernel(T* D, int64_t M, int64_t N, EpiParams e) {
 
 gemm_status_t run(const void* A, const void* B, void* D, int64_t M, int64_t N, int64_t K,
                   gemm_variant_t variant, gemm_stream_t stream, int dtype = 0,
-                  const gemm_epilogue_t* epilogue = nullptr, const float* scale_m = nullptr) {
+                  const gemm_epilogue_t* epilogue = nullptr, const float* scale_m = nullptr, bool late = false) {
     // ---- host-only argument checks (nothing touches a device before these pass)
     if (!dtype_valid(dtype)) return GEMM_ERR_INVALID_VALUE;
     const int in_bytes = dtype_in_bytes(dtype);
@@ -773,6 +773,7 @@ gemm_status_t run(const void* A, const void* B, void* D, int64_t M, int64_t N, i
         p.stream_b = b_bytes >= kStreamBBytes ? 1 : 0;
         p.ab_format = dtype_ab_format(dtype);
         p.prefetch_blocks = skinny_prefetch_blocks(pl, b_bytes);
+        p.late = late ? 1 : 0;
         if (ops.launch(tw, tx, p, pl.grid_ctas, s) != cudaSuccess) {
             cudaGetLastError();
             return GEMM_ERR_LAUNCH;
@@ -847,6 +848,7 @@ gemm_status_t run(const void* A, const void* B, void* D, int64_t M, int64_t N, i
     p.stage_atoms = tiled_stage_atoms(pl, ops.max_stage_atoms);
     p.D = D;
     p.epi = epi;
+    p.late = late ? 1 : 0;
     p.status = dev->status;
     p.timeout_ns = timeout_for(pl.k_blocks);
     if (ops.launch(ta, tb, tbp, td, p, pl.grid_ctas, s) != cudaSuccess) {
@@ -992,6 +994,11 @@ gemm_status_t stream_key(int dev, gemm_stream_t stream, StreamKey* out) {
     }
     *out = StreamKey{dev, id};
     return GEMM_OK;
+}
+
+gemm_status_t run_dense(int dtype, const void* A, const void* B, void* D, int64_t M, int64_t N, int64_t K,
+                        const gemm_epilogue_t* epilogue, bool late, gemm_stream_t stream) {
+    return run(A, B, D, M, N, K, GEMM_VARIANT_AUTO, stream, dtype, epilogue, nullptr, late);
 }
 
 bool encode_map(CUtensorMap* map, const void* base, int elem_bytes, int64_t inner, int64_t outer, uint32_t box_inner,

@@ -128,6 +128,7 @@ struct TiledParams {
     void* D;                  // the output (fp16 or bf16 [M][N]); written directly by the
                               // split-K slice sums, through tmD otherwise
     EpiParams epi;            // fused output transform (epi.on == 0: plain D = A B^T)
+    int32_t late;             // only the epilogue waits for the kernel before (A and B are complete)
     uint32_t* status;         // device status word (0 = ok)
     uint64_t timeout_ns;      // per-wait budget
 };
@@ -335,6 +336,7 @@ struct SkinnyParams {
     int32_t stream_b;         // B is too large to stay in L2: load it evict-first
     uint32_t ab_format;       // operand format field of the MMA instruction descriptor
     int32_t prefetch_blocks;  // B blocks a CTA prefetches into L2 before its dependency wait
+    int32_t late;             // only the epilogue waits for the kernel before (A and B are complete)
 };
 
 // Stream-K kernel (GEMM_VARIANT_SKINNY_STREAMK, and the no-allocation entry

@@ -144,7 +144,7 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     // of an SM's shared memory, so a CTA of this grid never shares an SM, or
     // its TMEM, with one of the last.)
     ptx::griddep_launch_dependents();
-    ptx::griddep_wait();
+    if (!p.late) ptx::griddep_wait();
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -231,6 +231,7 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         if (clustered) ptx::cluster_sync();   // meets the epilogue's exchange barrier
     } else {
         // ------------------------------------------------------------ epilogue
+        if (p.late) ptx::griddep_wait();   // C is read, and D written, only by these warps
         const int q = warp & 3;
         const int n_local = q * 32 + lane;   // TMEM lane = column within the range
         const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(q * 32) << 16);

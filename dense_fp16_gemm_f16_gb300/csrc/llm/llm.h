@@ -69,6 +69,21 @@ struct NormArgs {
 };
 gemm_status_t run_rmsnorm(bool bf16, const NormArgs& a, const DeviceView& dev, cudaStream_t s);
 
+// U = beta C + the adapters' part of the rows: c_a (X A_aT) B_aT, a = ids[m]
+struct LoraArgs {
+    const void *X, *A, *B;
+    const float* factors;  // nullptr: ones
+    const int32_t* ids;
+    const void* C;         // nullptr: none
+    float beta;
+    void* U;               // may be C
+    int64_t M, N, K, R, count;
+};
+constexpr int kLoraMaxRank = 256;
+// bytes of scratch that run_lora needs at `data`
+size_t lora_scratch_bytes(const LoraArgs& a, const DeviceView& dev);
+gemm_status_t run_lora(bool bf16, const LoraArgs& a, uint8_t* data, const DeviceView& dev, cudaStream_t s);
+
 // bytes of scratch that run_route needs at `data`; counters: one zero, left at zero
 size_t route_scratch_bytes(int64_t T, int64_t E);
 gemm_status_t run_route(bool bf16, const RouteParams& p, uint8_t* data, uint32_t* counters, const DeviceView& dev,

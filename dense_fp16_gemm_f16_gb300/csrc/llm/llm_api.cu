@@ -346,6 +346,90 @@ gemm_status_t rmsnorm(int dtype, const void* X, const void* residual, const void
     return run_rmsnorm(dtype == GEMM_DTYPE_BF16, a, dev, reinterpret_cast<cudaStream_t>(stream));
 }
 
+// The checks of adapters beside X [M][K] and an output U [M][N]; fills all of `a` but C, beta and U.
+gemm_status_t check_lora(int dtype, const void* X, const gemm_lora_t* l, const int32_t* ids, const void* U, int64_t M,
+                         int64_t N, int64_t K, LoraArgs* a) {
+    if (!type16(dtype) || !dim_ok(M) || !dim_ok(N) || !dim_ok(K) || l == nullptr) return GEMM_ERR_INVALID_VALUE;
+    if (l->count < 0 || l->R < 1 || l->R > kLoraMaxRank) return GEMM_ERR_INVALID_VALUE;
+    const int64_t count = l->count, R = l->R, a_size = mul_sat(mul_sat(count, R), K), b_size = mul_sat(mul_sat(count, R), N);
+    if (a_size < 0 || b_size < 0) return GEMM_ERR_INVALID_VALUE;
+    if (M > 0 && N > 0) {
+        if (U == nullptr || (K > 0 && X == nullptr)) return GEMM_ERR_INVALID_VALUE;
+        if (count > 0 && K > 0 && (l->A == nullptr || l->B == nullptr || ids == nullptr)) return GEMM_ERR_INVALID_VALUE;
+    }
+    if (K % 8 != 0 || N % 8 != 0 || R % 8 != 0) return GEMM_ERR_MISALIGNED;
+    if (!aligned16(X) || !aligned16(U) || !aligned16(ids) || !aligned16(l->A) || !aligned16(l->B) || !aligned16(l->factors))
+        return GEMM_ERR_MISALIGNED;
+    const int64_t out = mul_sat(M, N) < 0 ? -1 : M * N * 2;
+    if (out < 0 || mul_sat(M, K) < 0) return GEMM_ERR_INVALID_VALUE;
+    if (ranges_overlap(U, out, X, M * K * 2) || (l->A != nullptr && ranges_overlap(U, out, l->A, a_size * 2)) ||
+        (l->B != nullptr && ranges_overlap(U, out, l->B, b_size * 2)) ||
+        (l->factors != nullptr && ranges_overlap(U, out, l->factors, count * 4)) ||
+        (ids != nullptr && ranges_overlap(U, out, ids, M * 4)))
+        return GEMM_ERR_INVALID_VALUE;
+    *a = LoraArgs{X, l->A, l->B, l->factors, ids, nullptr, 0.0f, nullptr, M, N, K, R, count};
+    return GEMM_OK;
+}
+
+gemm_status_t lora_delta(int dtype, const void* X, const gemm_lora_t* l, const int32_t* ids, float beta, const void* C, void* U,
+                         int64_t M, int64_t N, int64_t K, gemm_stream_t stream) {
+    LoraArgs a;
+    gemm_status_t st = check_lora(dtype, X, l, ids, U, M, N, K, &a);
+    if (st != GEMM_OK) return st;
+    const gemm_epilogue_t epilogue{1.0f, beta, C, nullptr, GEMM_ACT_NONE, 0, nullptr};
+    st = check_epilogue(&epilogue, U, M, N);
+    if (st != GEMM_OK) return st;
+    if (M == 0 || N == 0) return GEMM_OK;
+    a.C = beta != 0.0f ? C : nullptr;
+    a.beta = beta;
+    a.U = U;
+    DeviceView dev;
+    st = device_view(&dev);
+    if (st != GEMM_OK) return st;
+    Scratch ws;
+    st = get_scratch(dev.dev, stream, lora_scratch_bytes(a, dev), &ws);
+    if (st != GEMM_OK) return st;
+    return run_lora(dtype == GEMM_DTYPE_BF16, a, ws.data, dev, reinterpret_cast<cudaStream_t>(stream));
+}
+
+gemm_status_t lora_nt(int dtype, const void* X, const gemm_weights_t* weights, const gemm_lora_t* l, const int32_t* ids,
+                      void* D, int64_t M, int64_t N, int64_t K, const gemm_epilogue_t* epilogue, gemm_stream_t stream) {
+    LoraArgs a;
+    gemm_status_t st = check_lora(dtype, X, l, ids, D, M, N, K, &a);
+    if (st != GEMM_OK) return st;
+    Weights w;
+    st = check_weights(weights, N, N, K, false, &w);
+    if (st != GEMM_OK) return st;
+    st = check_epilogue(epilogue, D, M, N);
+    if (st != GEMM_OK) return st;
+    if (M == 0 || N == 0) return GEMM_OK;
+    if (K > 0 && overlaps_weights(D, M * N * 2, w, N, K)) return GEMM_ERR_INVALID_VALUE;
+    DeviceView dev;
+    st = device_view(&dev);
+    if (st != GEMM_OK) return st;
+    // beta C and the adapters' part go to D, and the projection's epilogue adds them
+    gemm_epilogue_t epi{1.0f, 0.0f, nullptr, nullptr, GEMM_ACT_NONE, 0, nullptr};
+    if (epilogue != nullptr) epi = *epilogue;
+    if (K == 0 || a.count == 0) {
+        const EpiParams plain = epi_params(epilogue);
+        if (K == 0) return run_empty_sum(D, M, N, plain, dtype, dev.sms, reinterpret_cast<cudaStream_t>(stream));
+        return w.scales != nullptr ? run_w4_gemm(dtype == GEMM_DTYPE_BF16, X, w, D, M, N, K, plain, dev, stream)
+                                   : run_dense(dtype, X, w.data, D, M, N, K, epilogue, false, stream);
+    }
+    a.C = epi.beta != 0.0f ? epi.C : nullptr;
+    a.beta = epi.beta;
+    a.U = D;
+    epi.beta = 1.0f;
+    epi.C = D;
+    Scratch ws;
+    st = get_scratch(dev.dev, stream, lora_scratch_bytes(a, dev), &ws);
+    if (st != GEMM_OK) return st;
+    st = run_lora(dtype == GEMM_DTYPE_BF16, a, ws.data, dev, reinterpret_cast<cudaStream_t>(stream));
+    if (st != GEMM_OK) return st;
+    return w.scales != nullptr ? run_w4_gemm(dtype == GEMM_DTYPE_BF16, X, w, D, M, N, K, epi_params(&epi), dev, stream)
+                               : run_dense(dtype, X, w.data, D, M, N, K, &epi, true, stream);
+}
+
 }  // namespace
 
 extern "C" {
@@ -374,6 +458,18 @@ GEMM_API gemm_status_t gemm_moe_route(gemm_dtype_t dtype, const void* X, const v
                                       int64_t H, int64_t E, int32_t k, gemm_moe_scoring_t scoring,
                                       int32_t renormalize, int32_t* ids, float* weights, gemm_stream_t stream) {
     return guarded([&] { return route(dtype, X, Wr, bias, T, H, E, k, scoring, renormalize, ids, weights, stream); });
+}
+
+GEMM_API gemm_status_t gemm_lora_delta(gemm_dtype_t dtype, const void* X, const gemm_lora_t* lora, const int32_t* ids,
+                                       float beta, const void* C, void* U, int64_t M, int64_t N, int64_t K,
+                                       gemm_stream_t stream) {
+    return guarded([&] { return lora_delta(dtype, X, lora, ids, beta, C, U, M, N, K, stream); });
+}
+
+GEMM_API gemm_status_t gemm_lora_nt(gemm_dtype_t dtype, const void* X, const gemm_weights_t* W, const gemm_lora_t* lora,
+                                    const int32_t* ids, void* D, int64_t M, int64_t N, int64_t K,
+                                    const gemm_epilogue_t* epilogue, gemm_stream_t stream) {
+    return guarded([&] { return lora_nt(dtype, X, W, lora, ids, D, M, N, K, epilogue, stream); });
 }
 
 GEMM_API gemm_status_t gemm_moe_ffn(gemm_dtype_t dtype, const void* X, const int32_t* ids, const float* weights,

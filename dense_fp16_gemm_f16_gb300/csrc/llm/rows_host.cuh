@@ -119,14 +119,14 @@ inline int active_clusters(const void* kernel, const DeviceView& dev, int thread
 
 // Programmatic stream serialisation (where `early`), and clusters of `cluster` CTAs.
 template <class Kernel, class... Args>
-gemm_status_t launch_clusters(Kernel kernel, int dev, int grid, int threads, int cluster, int smem, bool early,
+gemm_status_t launch_clusters(Kernel kernel, int dev, dim3 grid, int threads, int cluster, int smem, bool early,
                               cudaStream_t s, const Args&... args) {
     if (allow_smem(reinterpret_cast<const void*>(kernel), dev) != cudaSuccess) {
         cudaGetLastError();
         return GEMM_ERR_CUDA;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = s;

@@ -49,6 +49,22 @@ class W4:
         return (*s[:-1], s[-1] * 2)
 
 
+class Lora:
+    """Low-rank adapters beside a projection [N, K]: A [count, R, K], B [count, N, R] and
+    factors float32 [count] (None: ones).  The adapter a adds factors[a] · x A[a]ᵀ B[a]ᵀ.
+    R is a multiple of 8 up to 256; an adapter of a lower rank is stored with zeros."""
+    __slots__ = ("A", "B", "factors")
+
+    def __init__(self, A, B, factors=None):
+        self.A, self.B, self.factors = A, B, factors
+
+
+class LoraStack(ctypes.Structure):
+    """Mirror of gemm_lora_t."""
+    _fields_ = [("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("factors", ctypes.c_void_p),
+                ("count", ctypes.c_int32), ("R", ctypes.c_int32)]
+
+
 class NormOut(ctypes.Structure):
     """Mirror of gemm_norm_out_t."""
     _fields_ = [("Y", ctypes.c_void_p), ("Y8", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("total", ctypes.c_void_p),
@@ -70,6 +86,8 @@ def declare(lib) -> None:
         "gemm_w4_dequantize": [i32, w, i64, i64, i64, p, p],
         "gemm_w4_nt": [i32, p, w, p, i64, i64, i64, ctypes.POINTER(_g.Epilogue), p],
         "gemm_rmsnorm": [i32, p, p, p, ctypes.c_float, i64, i64, ctypes.POINTER(NormOut), p],
+        "gemm_lora_delta": [i32, p, ctypes.POINTER(LoraStack), p, ctypes.c_float, p, p, i64, i64, i64, p],
+        "gemm_lora_nt": [i32, p, w, ctypes.POINTER(LoraStack), p, p, i64, i64, i64, ctypes.POINTER(_g.Epilogue), p],
         "gemm_moe_route": [i32, p, p, p, i64, i64, i64, i32, i32, i32, p, p, p],
         "gemm_moe_ffn": [i32, p, p, p, w, w, p, i64, i64, i64, i64, i32, p],
         "gemm_moe_layer": [i32, p, p, p, w, w, p, i64, i64, i64, i64, i32, i32, i32, p],
@@ -326,6 +344,53 @@ def gemm_rmsnorm(X, weight=None, residual=None, eps: float = 1e-6, Y=None, Y8=No
                   None if total is None else _check(total, "total", dtype, shape, index), dt8, scale or 0.0)
     _run(lib.gemm_rmsnorm, index, stream, (dt, X.data_ptr(), r, w, eps, T, H, ctypes.byref(out)))
     return Normed(Y, Y8, scales, total)
+
+
+def _adapters(X, lora, ids):
+    """(index, dtype code, M, N, K, the adapters and ids as the library takes them)."""
+    index = _cuda(X, "X")
+    dt = _type16(X, "X")
+    if not isinstance(lora, Lora):
+        raise TypeError("lora must be a Lora")
+    A, B, f = lora.A, lora.B, lora.factors
+    if X.dim() != 2:
+        raise ValueError(f"X must be [M, K], got {tuple(X.shape)}")
+    if not _g._is_tensor(A) or not _g._is_tensor(B) or A.dim() != 3 or B.dim() != 3:
+        raise ValueError("lora.A must be [count, R, K] and lora.B [count, N, R]")
+    M, K = X.shape
+    count, R, _ = A.shape
+    N = B.shape[1]
+    l = LoraStack(_check(A, "lora.A", X.dtype, (count, R, K), index), _check(B, "lora.B", X.dtype, (count, N, R), index),
+                  None if f is None else _check(f, "lora.factors", _torch.float32, (count,), index), count, R)
+    return index, dt, M, N, K, ctypes.byref(l), _check(ids, "ids", _torch.int32, (M,), index)
+
+
+def gemm_lora_delta(X, lora: Lora, ids, U=None, beta=0.0, C=None, stream=None):
+    """U[m] = beta·C[m] + factors[a]·(X[m] A[a]ᵀ) B[a]ᵀ with a = ids[m] (int32 [M]; outside [0, count): none).
+
+    U (allocated unless given; may be C) is the ``C`` of any product with ``beta=1``."""
+    lib = _lib or _setup()
+    index, dt, M, N, K, l, i = _adapters(X, lora, ids)
+    if U is None:
+        U = _g._empty((M, N), X.dtype, X.device, stream)
+    c = None if C is None else _check(C, "C", X.dtype, (M, N), index)
+    _run(lib.gemm_lora_delta, index, stream,
+         (dt, X.data_ptr(), l, i, beta, c, _check(U, "U", X.dtype, (M, N), index), M, N, K))
+    return U
+
+
+def gemm_lora_nt(X, W, lora: Lora, ids, D, alpha=1.0, beta=0.0, C=None, bias=None, activation=_g.Activation.NONE,
+                 stream=None, scale_n=None) -> None:
+    """D[m] = act(alpha·scale_n·X[m] Wᵀ + factors[a]·(X[m] A[a]ᵀ) B[a]ᵀ + beta·C[m] + bias) with a = ids[m].
+
+    W [N, K] is a tensor of X's type or a ``W4``; ``ids`` as in gemm_lora_delta.  D may be C."""
+    lib = _lib or _setup()
+    index, dt, M, N, K, l, i = _adapters(X, lora, ids)
+    dtype = X.dtype
+    w = _weights(W, "W", dtype, (), N, K, index)
+    d = _check(D, "D", dtype, (M, N), index)
+    epi = _epilogue(dtype, M, N, index, alpha, beta, C, bias, activation, scale_n)
+    _run(lib.gemm_lora_nt, index, stream, (dt, X.data_ptr(), ctypes.byref(w), l, i, d, M, N, K, epi))
 
 
 def _tokens(X, Wr, bias):

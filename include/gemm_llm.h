@@ -10,7 +10,7 @@
  * Activations, scales and outputs are fp16 (GEMM_DTYPE_F16) or bf16
  * (GEMM_DTYPE_BF16); sums are held in fp32 and each output is rounded once.
  *
- * Scratch memory.  The mixture-of-experts calls keep intermediate values in a
+ * Scratch memory.  The mixture-of-experts and adapter calls keep intermediate values in a
  * scratch buffer of the (device, stream) pair.  The first call that needs it
  * allocates it with cudaMalloc; a larger problem gets a new buffer of at least
  * twice the size.  Buffers are kept until the process exits, so a captured
@@ -134,6 +134,51 @@ typedef struct {
  */
 GEMM_API gemm_status_t gemm_rmsnorm(gemm_dtype_t dtype, const void* X, const void* residual, const void* weight, float eps,
                                     int64_t T, int64_t H, const gemm_norm_out_t* out, gemm_stream_t stream);
+
+/*
+ * A stack of `count` low-rank adapters of rank R beside an [N][K] projection.
+ *   A [count][R][K] and B [count][N][R] in the call's dtype
+ *   factors [count] fp32, or NULL for ones
+ * R a multiple of 8 up to 256.  An adapter of a lower rank is stored with zeros.
+ */
+typedef struct {
+    const void* A;
+    const void* B;
+    const float* factors;
+    int32_t count;
+    int32_t R;
+} gemm_lora_t;
+
+/*
+ * gemm_lora_delta -- what the adapters of many requests add to a projection of
+ * their rows, each row with an adapter of its own:
+ *     U[m] = beta * C[m] + factors[a] * (X[m] A_a^T) B_a^T,   a = ids[m]
+ *   X [M][K], C and U [M][N] in dtype; C may be U itself and is not read with beta 0
+ *   ids [M] int32, device memory; an id outside [0, count) leaves beta * C[m]
+ * Rows may come in any order; rows of one adapter share its reads, within 256 rows
+ * (128 where M is larger).  X A^T is held in fp32 and enters the second product with
+ * twice the precision of dtype, so U is rounded once.
+ * U is what any product of the library takes as C with beta = 1: gemm_nt_scaled for
+ * 8-bit operands, or gemm_lora_nt in one call.  K and N multiples of 8.  M or N of zero
+ * is a no-op.  Uses the stream's scratch memory.
+ */
+GEMM_API gemm_status_t gemm_lora_delta(gemm_dtype_t dtype, const void* X, const gemm_lora_t* lora, const int32_t* ids,
+                                       float beta, const void* C, void* U, int64_t M, int64_t N, int64_t K,
+                                       gemm_stream_t stream);
+
+/*
+ * gemm_lora_nt -- a projection shared by many requests, with their adapters:
+ *     D[m] = act(alpha * scale_n[n] * X[m] W^T + factors[a] * (X[m] A_a^T) B_a^T + beta * C[m] + bias)
+ * W [N][K] 16-bit or 4-bit weights; the rest as for gemm_lora_delta and the
+ * epilogue of gemm_nt_ex (NULL: none).  D may be C itself.  beta * C and the adapters'
+ * part are summed in fp32 and rounded to dtype once before the projection's sum in fp32
+ * joins them and D is rounded: an error of at most half a unit in the last place of
+ * each.  Rows without an adapter whose beta * C is a number of dtype (beta 0 or 1) get the
+ * plain product's D.  count == 0: the plain product.
+ */
+GEMM_API gemm_status_t gemm_lora_nt(gemm_dtype_t dtype, const void* X, const gemm_weights_t* W, const gemm_lora_t* lora,
+                                    const int32_t* ids, void* D, int64_t M, int64_t N, int64_t K,
+                                    const gemm_epilogue_t* epilogue, gemm_stream_t stream);
 
 typedef enum {
     GEMM_MOE_SOFTMAX = 0,   /* p = softmax of the token's E logits */

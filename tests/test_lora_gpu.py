@@ -1,0 +1,318 @@
+"""Low-rank adapters of many requests beside a projection, against 64 bits.
+
+Bounds per element, fixed from the arithmetic before any run; u is half a unit in the
+last place (2^-11 for fp16, 2^-8 for bf16), taken 1 % wider:
+  V = X Aᵀ in fp32: a chain of at most K / 128 MMAs in a warp, 8 warps and at most 32
+      pieces are added, each addition off by at most 2^-23 of the magnitudes that enter
+  V cut into hi + lo: off by 2^-17 of it (bf16; fp16 less), or 2^-24 of the row's largest
+      where fp16 runs out of small numbers
+  times B: R / 8 MMAs (hi and lo), the factor, beta C: 2^-23 each
+  one rounding of U: u |U|;  D: u |D| and 2^-22 of the projection's magnitudes besides
+"""
+import pytest
+import torch
+
+import dense_fp16_gemm_f16_gb300 as g
+from llm_check import E32, FLOOR, U as UNIT, random_w4, w64
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+TYPES = [torch.float16, torch.bfloat16]
+
+
+def draw(M, N, K, R, count, dtype, seed, runs=False, none=0.15):
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+
+    def normal(*shape):
+        return (torch.randn(*shape, generator=gen, device=DEV) * shape[-1] ** -0.5).to(dtype)
+
+    X = torch.randn(M, K, generator=gen, device=DEV).to(dtype)
+    lora = g.Lora(normal(count, R, K), normal(count, N, R), torch.rand(count, generator=gen, device=DEV) + 0.25)
+    ids = torch.randint(0, max(count, 1), (M,), generator=gen, device=DEV, dtype=torch.int32)
+    if runs:
+        ids = ids.sort().values
+    ids[torch.rand(M, generator=gen, device=DEV) < none] = -1
+    return X, lora, ids, gen
+
+
+def delta64(X, lora, ids, beta=0.0, C=None):
+    """(beta C + the adapters' part, the error that may come before its rounding)."""
+    M, K = X.shape
+    count, R, _ = lora.A.shape
+    ref = torch.zeros(M, lora.B.shape[1], dtype=torch.float64, device=X.device)
+    err = torch.zeros_like(ref)
+    for a in range(count):
+        rows = (ids == a).nonzero(as_tuple=True)[0]
+        if not len(rows):
+            continue
+        x, A, B = X[rows].double(), lora.A[a].double(), lora.B[a].double()
+        f = 1.0 if lora.factors is None else lora.factors[a].double()
+        V, mag = x @ A.T, x.abs() @ A.abs().T
+        ref[rows] = f * (V @ B.T)
+        eV = (K / 128 + 44) * 2.0 ** -23 * mag + 2.0 ** -17 * V.abs() + 2.0 ** -24 * V.abs().amax(1, keepdim=True)
+        err[rows] = abs(f) * ((eV + (R / 8 + 4) * 2.0 ** -23 * V.abs()) @ B.abs().T)
+    if C is not None:
+        ref += beta * C.double()
+        err += 2.0 ** -22 * abs(beta) * C.double().abs()
+    return ref, err
+
+
+def check(got, ref, tol):
+    bad = ~((got.double() - ref).abs() <= tol)
+    assert not bool(bad.any()), (f"{int(bad.sum())} of {bad.numel()} out of bounds, worst "
+                                 f"{float(((got.double() - ref).abs() / tol)[bad].max())}, first at {bad.nonzero()[0].tolist()}")
+
+
+SIZES = [  # M, N, K, R, count
+    (1, 8, 8, 8, 1), (1, 1024, 2048, 8, 4), (3, 40, 72, 16, 2), (16, 8192, 1024, 16, 32), (17, 264, 520, 24, 3),
+    (33, 1000, 4104, 40, 40), (64, 2048, 1032, 64, 5), (61, 512, 8192, 128, 48), (9, 320, 256, 256, 4), (130, 600, 264, 136, 7),
+    (200, 72, 2048, 32, 1), (255, 136, 512, 8, 300), (256, 1032, 520, 16, 64), (257, 512, 512, 16, 3), (400, 328, 1000, 72, 500),
+    (1000, 2048, 1024, 64, 8), (2048, 520, 2056, 16, 1), (8200, 64, 256, 24, 40), (9500, 136, 4096, 16, 2)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,N,K,R,count", SIZES)
+def test_delta(M, N, K, R, count, dtype):
+    for runs in (False, True):
+        X, lora, ids, gen = draw(M, N, K, R, count, dtype, M + N + R, runs)
+        ref, err = delta64(X, lora, ids)
+        U = torch.full((M, N), float("nan"), dtype=dtype, device=DEV)
+        assert g.gemm_lora_delta(X, lora, ids, U) is U
+        check(U, ref, 1.01 * UNIT[dtype] * ref.abs() + err + FLOOR)
+        C = torch.randn(M, N, generator=gen, device=DEV).to(dtype)
+        ref, err = delta64(X, lora, ids, -0.7, C)
+        assert g.gemm_lora_delta(X, lora, ids, U, beta=-0.7, C=C) is U
+        check(U, ref, 1.01 * UNIT[dtype] * ref.abs() + err + FLOOR)
+        E = C.clone()
+        g.gemm_lora_delta(X, lora, ids, E, beta=-0.7, C=E)
+        assert torch.equal(E, U)
+    g.gemm_f16_nt_check(device=DEV)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,N,K,R,count", [(1, 1024, 2048, 8, 4), (16, 8192, 1024, 16, 32), (17, 264, 520, 24, 3), (64, 2048, 1032, 64, 5),
+                                           (65, 72, 136, 16, 2), (250, 5000, 1032, 32, 64), (256, 256, 8192, 16, 9),
+                                           (512, 2048, 4096, 128, 8), (3000, 4104, 1024, 16, 4), (8300, 520, 512, 8, 3)])
+def test_projection_with_adapters(M, N, K, R, count, dtype):
+    X, lora, ids, gen = draw(M, N, K, R, count, dtype, M + K, runs=M > 256)
+    W = (torch.randn(N, K, generator=gen, device=DEV) * K ** -0.5).to(dtype)
+    C, bias = (torch.randn(s, generator=gen, device=DEV).to(dtype) for s in ((M, N), (N,)))
+    sn = torch.rand(N, generator=gen, device=DEV) + 0.5
+    for args in (dict(), dict(alpha=0.6, beta=1.0, C=C, bias=bias, scale_n=sn, activation=g.Activation.RELU)):
+        D = torch.full((M, N), float("nan"), dtype=dtype, device=DEV)
+        g.gemm_lora_nt(X, W, lora, ids, D, **args)
+        part, err = delta64(X, lora, ids, args.get("beta", 0.0), args.get("C"))
+        f = (args.get("alpha", 1.0) * (sn.double() if args else 1.0))
+        x, w = X.double(), W.double()
+        ref, mag = (x @ w.T) * f + part, (x.abs() @ w.abs().T) * f
+        if args:
+            ref = ref + bias.double()
+        tol = UNIT[dtype] * 1.01 * (ref.abs() + part.abs()) + err + E32 * (mag + part.abs() + 4) + 2 * FLOOR
+        check(D, ref.clamp(min=0) if args else ref, tol)
+        # the same as the two calls that it stands for
+        T, E = (torch.empty_like(D) for _ in range(2))
+        g.gemm_lora_delta(X, lora, ids, T, beta=args.get("beta", 0.0), C=args.get("C"))
+        g.gemm_nt_ex(X, W, E, **(args | dict(beta=1.0, C=T)))
+        assert torch.equal(D, E)
+        if "C" in args:
+            E = C.clone()
+            g.gemm_lora_nt(X, W, lora, ids, E, **(args | dict(C=E)))
+            assert torch.equal(D, E)
+    # rows without an adapter, and all rows with none: the plain product
+    D, P = (torch.empty(M, N, dtype=dtype, device=DEV) for _ in range(2))
+    g.gemm_lora_nt(X, W, lora, ids, D)
+    g.gemm_nt_ex(X, W, P)
+    assert torch.equal(D[ids < 0], P[ids < 0])
+    g.gemm_lora_nt(X, W, lora, torch.full_like(ids, count), D)
+    assert torch.equal(D, P)
+    g.gemm_f16_nt_check(device=DEV)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,group,asym", [(1, 128, False), (13, 32, True), (40, 64, False), (64, 128, True), (300, 64, True)])
+def test_beside_4_bit_weights(M, group, asym, dtype):
+    N, K = 1032, 1024
+    X, lora, ids, gen = draw(M, N, K, 16, 6, dtype, M)
+    W = random_w4(torch.Generator().manual_seed(M), (), N, K, group, asym, dtype, DEV)
+    C, bias = (torch.randn(s, generator=gen, device=DEV).to(dtype) for s in ((M, N), (N,)))
+    D, E = (torch.empty(M, N, dtype=dtype, device=DEV) for _ in range(2))
+    g.gemm_lora_nt(X, W, lora, ids, D, beta=0.5, C=C, bias=bias)
+    g.gemm_w4_nt(X, W, E, beta=1.0, C=g.gemm_lora_delta(X, lora, ids, beta=0.5, C=C), bias=bias)
+    assert torch.equal(D, E)
+    if M <= 16:
+        w, wm = w64(W)
+        part, err = delta64(X, lora, ids, 0.5, C)
+        ref = X.double() @ w.T + part + bias.double()
+        tol = UNIT[dtype] * 1.01 * (ref.abs() + part.abs()) + err + E32 * (X.double().abs() @ wm.T + part.abs() + 8) + 2 * FLOOR
+        check(D, ref, tol)
+
+
+@pytest.mark.parametrize("kind", [torch.float8_e4m3fn, torch.float8_e5m2])
+@pytest.mark.parametrize("M", [1, 30, 64, 300])
+def test_norm_adapters_and_8_bit_product(M, kind):
+    """A step of a decoder: norm of the summed stream, its 16-bit rows to the adapters, its 8-bit rows to the
+    projection, all in one graph that is replayed on other activations."""
+    N, K, dtype = 1024, 2048, torch.bfloat16
+    X, lora, ids, gen = draw(M, N, K, 16, 5, dtype, M)
+    r, w = torch.randn(M, K, generator=gen, device=DEV).to(dtype), (torch.rand(K, generator=gen, device=DEV) + 0.5).to(dtype)
+    top = 448.0 if kind == torch.float8_e4m3fn else 57344.0
+    W = (torch.randn(N, K, generator=gen, device=DEV) * top / 5).clamp(-top, top).to(kind)
+    sn = (torch.rand(N, generator=gen, device=DEV) + 0.5) * K ** -0.5 * 5 / top
+    Y, Y8, total = torch.empty_like(X), torch.empty(M, K, dtype=kind, device=DEV), torch.empty_like(X)
+    scales, T, D = torch.empty(M, device=DEV), torch.empty(M, N, dtype=dtype, device=DEV), torch.empty(M, N, dtype=dtype, device=DEV)
+
+    def step():
+        g.gemm_rmsnorm(X, w, r, Y=Y, Y8=Y8, scales=scales, total=total)
+        g.gemm_lora_delta(Y, lora, ids, T)
+        g.gemm_nt_ex(Y8, W, D, scale_m=scales, scale_n=sn, beta=1.0, C=T)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            step()
+        for i in range(4):
+            X.copy_(torch.randn(X.shape, generator=gen, device=DEV))
+            ids.copy_(torch.randint(-1, 5, ids.shape, generator=gen, device=DEV))
+            graph.replay()
+    torch.cuda.synchronize()
+    part, err = delta64(Y, lora, ids)
+    check(T, part, 1.01 * UNIT[dtype] * part.abs() + err + FLOOR)
+    a, b = Y8.float().double() * scales.double()[:, None], W.float().double() * sn.double()[:, None]
+    ref = a @ b.T + T.double()
+    check(D, ref, 1.01 * UNIT[dtype] * ref.abs() + (K / 32 + 6) * 2.0 ** -23 * (a.abs() @ b.abs().T + T.double().abs()))
+    assert torch.equal(total, (X.float() + r.float()).to(dtype))
+    g.gemm_f16_nt_check(device=DEV)
+
+
+def test_special_values_stay_in_their_rows_and_adapters():
+    M, N, K, R = 40, 264, 512, 16
+    X, lora, ids, _ = draw(M, N, K, R, 4, torch.float16, 3, none=0.0)
+    ids = torch.arange(M, device=DEV, dtype=torch.int32) % 4
+    want = g.gemm_lora_delta(X, lora, ids)
+    X[5, 3], X[6, 4] = float("nan"), float("inf")
+    lora.A[1, 0, 0] = float("nan")      # adapter 1 is not to be used
+    lora.B[1] = float("inf")
+    ids[ids == 1] = 7
+    ids[0], ids[2] = -2 ** 31, 2 ** 31 - 1
+    got = g.gemm_lora_delta(X, lora, ids)
+    none = (ids < 0) | (ids >= 4)
+    assert int(none.sum()) >= 12 and not bool(got[none].any())
+    keep = ~none
+    keep[5], keep[6] = False, False
+    assert torch.equal(got[keep], want[keep])
+    if not bool(none[5]):
+        assert bool(got[5].isnan().all())
+    assert not bool(got[6].isfinite().any())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_large_and_small_inner_values(dtype):
+    """X Aᵀ may lie far outside fp16's range: only U is a number of the type."""
+    M, N, K, R = 20, 128, 1024, 16
+    X, lora, ids, _ = draw(M, N, K, R, 3, dtype, 8)
+    big, small = 2.0 ** 12, 2.0 ** -12
+    up = g.Lora(lora.A * big, lora.B * small, lora.factors)
+    X2 = X * big
+    ref, err = delta64(X2, up, ids)
+    check(g.gemm_lora_delta(X2, up, ids) , ref, 1.01 * UNIT[dtype] * ref.abs() + err + FLOOR)
+    down = g.Lora((lora.A * small).to(dtype), lora.B, torch.full((3,), 2.0 ** 14, device=DEV))
+    ref, err = delta64(X, down, ids)
+    check(g.gemm_lora_delta(X, down, ids), ref, 1.01 * UNIT[dtype] * ref.abs() + err + FLOOR)
+
+
+def test_a_row_does_not_depend_on_its_place():
+    """Rows in another order give the same rows: sums do not depend on what shares a tile."""
+    M, N, K = 200, 520, 1024
+    X, lora, ids, gen = draw(M, N, K, 32, 9, torch.bfloat16, 4)
+    want = g.gemm_lora_delta(X, lora, ids)
+    p = torch.randperm(M, generator=gen, device=DEV)
+    assert torch.equal(g.gemm_lora_delta(X[p], lora, ids[p]), want[p])
+    assert torch.equal(g.gemm_lora_delta(X, lora, ids), want)
+
+
+def test_no_factors_no_adapters_and_empty():
+    X, lora, ids, gen = draw(6, 64, 128, 8, 3, torch.float16, 5)
+    one = g.Lora(lora.A, lora.B)
+    ref, err = delta64(X, one, ids)
+    check(g.gemm_lora_delta(X, one, ids), ref, 1.01 * UNIT[torch.float16] * ref.abs() + err + FLOOR)
+    W, C = (torch.randn(s, generator=gen, device=DEV).half() for s in ((64, 128), (6, 64)))
+    empty = g.Lora(lora.A[:0], lora.B[:0])
+    D, P = torch.empty(6, 64, dtype=torch.float16, device=DEV), torch.empty(6, 64, dtype=torch.float16, device=DEV)
+    g.gemm_lora_nt(X, W, empty, ids, D, beta=0.3, C=C)
+    g.gemm_nt_ex(X, W, P, beta=0.3, C=C)
+    assert torch.equal(D, P)
+    assert not bool(g.gemm_lora_delta(X, empty, ids).any())
+    assert torch.equal(g.gemm_lora_delta(X, empty, ids, beta=1.0, C=C), C)
+    assert g.gemm_lora_delta(X[:0], lora, ids[:0]).shape == (0, 64)
+    k0 = g.Lora(lora.A[:, :, :0].contiguous(), lora.B)
+    assert torch.equal(g.gemm_lora_delta(X[:, :0].contiguous(), k0, ids, beta=2.0, C=C), C * 2)
+    g.gemm_lora_nt(X[:, :0].contiguous(), W[:, :0].contiguous(), k0, ids, D, beta=2.0, C=C)
+    assert torch.equal(D, C * 2)
+
+
+def test_nothing_is_written_beyond_the_rows():
+    M, N = 5, 40
+    X, lora, ids, _ = draw(M, N, 128, 8, 3, torch.bfloat16, 6)
+    wide = torch.full((M + 4, N), 3.0, dtype=torch.bfloat16, device=DEV)
+    g.gemm_lora_delta(X, lora, ids, wide[:M])
+    assert bool((wide[M:] == 3.0).all()) and bool((wide[:M] != 3.0).any())
+
+
+def test_streams_and_captured_calls():
+    """Two streams at one time, and replays with other ids and activations."""
+    N, K = 520, 1024
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    work = []
+    for i, s in enumerate(streams):
+        X, lora, ids, gen = draw(70 + 200 * i, N, K, 16, 5, torch.bfloat16, i)
+        W = (torch.randn(N, K, generator=gen, device=DEV) * K ** -0.5).bfloat16()
+        D = torch.empty(len(X), N, dtype=torch.bfloat16, device=DEV)
+        g.gemm_lora_nt(X, W, lora, ids, D, stream=s)
+        work.append((X, W, lora, ids, D, gen))
+    torch.cuda.synchronize()
+    want = [w[4].clone() for w in work]
+    for _ in range(20):
+        for (X, W, lora, ids, D, _), s in zip(work, streams):
+            g.gemm_lora_nt(X, W, lora, ids, D, stream=s)
+    torch.cuda.synchronize()
+    for w, ref in zip(work, want):
+        assert torch.equal(w[4], ref)
+    X, W, lora, ids, D, gen = work[0]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=streams[0]):
+        g.gemm_lora_nt(X, W, lora, ids, D)
+    for _ in range(3):
+        X.copy_(torch.randn(X.shape, generator=gen, device=DEV))
+        ids.copy_(torch.randint(-1, 5, ids.shape, generator=gen, device=DEV))
+        graph.replay()
+    torch.cuda.synchronize()
+    E = torch.empty_like(D)
+    g.gemm_lora_nt(X, W, lora, ids, E)
+    assert torch.equal(D, E)
+    g.gemm_f16_nt_check(device=DEV)
+
+
+def test_refusals():
+    X, lora, ids, _ = draw(4, 64, 128, 8, 3, torch.float16, 1)
+    W, D = torch.zeros(64, 128, dtype=torch.float16, device=DEV), torch.zeros(4, 64, dtype=torch.float16, device=DEV)
+    A, B, f = lora.A, lora.B, lora.factors
+    for error, change in [
+            (TypeError, dict(X=X.float())), (ValueError, dict(X=X[:, :64])), (TypeError, dict(lora=(A, B))),
+            (ValueError, dict(lora=g.Lora(A[:2], B, f))), (ValueError, dict(lora=g.Lora(A, B[:, :, :4].contiguous(), f))),
+            (TypeError, dict(lora=g.Lora(A.bfloat16(), B, f))), (TypeError, dict(lora=g.Lora(A, B, f.double()))),
+            (ValueError, dict(lora=g.Lora(A, B, f[:2]))), (TypeError, dict(ids=ids.long())), (ValueError, dict(ids=ids[:3])),
+            (ValueError, dict(ids=ids.cpu())), (ValueError, dict(W=W[:32])), (TypeError, dict(D=D.bfloat16())),
+            (ValueError, dict(D=D[:2])), (g.GemmError, dict(beta=1.0)),
+            (g.GemmError, dict(lora=g.Lora(A[:, :4].contiguous(), B[:, :, :4].contiguous(), f)))]:
+        args = dict(X=X, W=W, lora=lora, ids=ids, D=D) | change
+        with pytest.raises(error):
+            g.gemm_lora_nt(**args)
+        if "W" in change:
+            continue
+        args.pop("W")
+        args["U"] = args.pop("D")
+        with pytest.raises(error):
+            g.gemm_lora_delta(**args)

@@ -6,7 +6,7 @@ import pytest
 
 import dense_fp16_gemm_f16_gb300 as g
 from dense_fp16_gemm_f16_gb300 import build as gbuild
-from dense_fp16_gemm_f16_gb300.llm import NormOut
+from dense_fp16_gemm_f16_gb300.llm import LoraStack, NormOut, Weights
 
 P = 0x7F0000000000          # 16-byte aligned addresses that are never dereferenced here
 GAP = 1 << 36
@@ -51,3 +51,35 @@ def test_scaled_product_refusals(lib):
     assert call(epi=ctypes.byref(epi)) == S.ERR_INVALID_VALUE   # beta without C
     assert call(M=0, a=0, d=0, sm=0) == S.OK
     assert call(N=0, b=0, d=0, sm=0) == S.OK
+
+
+def _lora(a=B, b=C, f=D, count=4, R=16):
+    return ctypes.byref(LoraStack(a, b, f, count, R))
+
+
+def test_adapter_refusals(lib):
+    def delta(dtype=0, X=A, l=None, ids=E, beta=0.0, c=None, U=F, M=4, N=64, K=64):
+        return lib.gemm_lora_delta(dtype, X, l or _lora(), ids, beta, c, U, M, N, K, None)
+
+    def nt(dtype=0, X=A, l=None, ids=E, U=F, M=4, N=64, K=64, w=None, epi=None):
+        return lib.gemm_lora_nt(dtype, X, w or ctypes.byref(Weights(G, None, None, 0, 0)), l or _lora(), ids, U, M, N, K, epi, None)
+
+    assert lib.gemm_lora_delta(0, A, None, E, 0.0, None, F, 4, 64, 64, None) == S.ERR_INVALID_VALUE
+    assert lib.gemm_lora_nt(0, A, None, _lora(), E, F, 4, 64, 64, None, None) == S.ERR_INVALID_VALUE
+    for f in (delta, nt):
+        for bad in (dict(dtype=2), dict(M=-1), dict(N=-8), dict(K=-8), dict(M=2 ** 31), dict(X=0), dict(U=0), dict(ids=0),
+                    dict(l=_lora(a=0)), dict(l=_lora(b=0)), dict(l=_lora(count=-1)), dict(l=_lora(R=0)), dict(l=_lora(R=264)),
+                    dict(U=A), dict(U=B + 64), dict(U=C), dict(U=D), dict(U=E),
+                    dict(l=_lora(count=2 ** 31 - 1, R=256), K=2 ** 30, N=8)):
+            assert f(**bad) == S.ERR_INVALID_VALUE, bad
+        for bad in (dict(K=60), dict(N=12), dict(l=_lora(R=12)), dict(X=A + 8), dict(U=F + 8), dict(ids=E + 4),
+                    dict(l=_lora(a=B + 8)), dict(l=_lora(b=C + 2)), dict(l=_lora(f=D + 4))):
+            assert f(**bad) == S.ERR_MISALIGNED, bad
+        assert f(M=0, X=0, U=0, ids=0) == S.OK
+        assert f(N=0, U=0) == S.OK
+    assert delta(beta=1.0) == S.ERR_INVALID_VALUE            # beta without C
+    assert delta(beta=1.0, c=F + 64) == S.ERR_INVALID_VALUE  # partly over U
+    assert nt(U=G) == S.ERR_INVALID_VALUE
+    assert nt(w=ctypes.byref(Weights(G, D, None, 48, 0))) == S.ERR_INVALID_VALUE
+    epi = g.Epilogue(1.0, 1.0, None, None, 0, 0, None)
+    assert nt(epi=ctypes.byref(epi)) == S.ERR_INVALID_VALUE
