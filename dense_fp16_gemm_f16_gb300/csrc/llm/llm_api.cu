@@ -386,10 +386,7 @@ gemm_status_t lora_delta(int dtype, const void* X, const gemm_lora_t* l, const i
     DeviceView dev;
     st = device_view(&dev);
     if (st != GEMM_OK) return st;
-    Scratch ws;
-    st = get_scratch(dev.dev, stream, lora_scratch_bytes(a, dev), &ws);
-    if (st != GEMM_OK) return st;
-    return run_lora(dtype == GEMM_DTYPE_BF16, a, ws.data, dev, reinterpret_cast<cudaStream_t>(stream));
+    return run_lora(dtype == GEMM_DTYPE_BF16, a, dev, reinterpret_cast<cudaStream_t>(stream));
 }
 
 gemm_status_t lora_nt(int dtype, const void* X, const gemm_weights_t* weights, const gemm_lora_t* l, const int32_t* ids,
@@ -421,10 +418,7 @@ gemm_status_t lora_nt(int dtype, const void* X, const gemm_weights_t* weights, c
     a.U = D;
     epi.beta = 1.0f;
     epi.C = D;
-    Scratch ws;
-    st = get_scratch(dev.dev, stream, lora_scratch_bytes(a, dev), &ws);
-    if (st != GEMM_OK) return st;
-    st = run_lora(dtype == GEMM_DTYPE_BF16, a, ws.data, dev, reinterpret_cast<cudaStream_t>(stream));
+    st = run_lora(dtype == GEMM_DTYPE_BF16, a, dev, reinterpret_cast<cudaStream_t>(stream));
     if (st != GEMM_OK) return st;
     return w.scales != nullptr ? run_w4_gemm(dtype == GEMM_DTYPE_BF16, X, w, D, M, N, K, epi_params(&epi), dev, stream)
                                : run_dense(dtype, X, w.data, D, M, N, K, &epi, true, stream);
