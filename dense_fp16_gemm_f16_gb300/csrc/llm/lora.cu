@@ -160,7 +160,7 @@ __device__ void group_rows(const LoraParams& p, int row0, int rows, Groups& s) {
 // -------------------------------------------------------------------------- down
 // 16-byte loads of a thread that are under way at one time, and how many steps make them.
 template <int MT, int NT>
-constexpr int kDownUnroll = 16 / (2 * MT + NT) > 4 ? 4 : (16 / (2 * MT + NT) < 1 ? 1 : 16 / (2 * MT + NT));
+constexpr int kDownUnroll = 12 / (2 * MT + NT);
 // Floats between the sums of two rows in the warps' exchange: the two columns of
 // a fragment fall into different banks.
 __host__ __device__ constexpr int down_pitch(int MT) { return 16 * MT + 4; }
@@ -255,10 +255,16 @@ __device__ __forceinline__ void down(const LoraParams& p, const T* A, const int3
 }
 
 // ---------------------------------------------------------------------------- up
-// Bytes of a row of V in shared memory: groups of four fp32 sums become four hi and
-// four lo numbers in the same 16 bytes; 64 more than a multiple of 128 keeps the rows' reads
-// in different banks.
-__host__ __device__ constexpr int up_pitch(int R) { return R * 4 + ((64 - R * 4) & 127); }
+// Ranks of a chunk: the MMA steps whose part of B a thread reads with one load, 8
+// bytes a row for up to 16 ranks, else 16.  V is kept with zeros up to a whole chunk.
+__host__ __device__ constexpr int up_chunk(int R) { return R <= 16 ? 16 : 32; }
+__host__ __device__ constexpr int up_ranks(int R) { return (R + up_chunk(R) - 1) / up_chunk(R) * up_chunk(R); }
+// Bytes of a row of V in shared memory: groups of four fp32 sums become four hi and four
+// lo numbers in the same 16 bytes.  A thread reads one group (or two) of its chunk's; the
+// rows' distance keeps eight threads' reads in different banks.
+__host__ __device__ constexpr int up_pitch(int R) {
+    return up_ranks(R) * 4 + (((R <= 16 ? 64 : 16) - up_ranks(R) * 4) & 127);
+}
 // rows of V in shared memory at one time
 __host__ __device__ constexpr int up_rows(int R) { return R <= 64 ? 128 : (R <= 128 ? 64 : 32); }
 
@@ -280,6 +286,9 @@ __device__ __forceinline__ void take_rows(const LoraParams& p, int m, float fact
                                           uint32_t* row_max) {
     constexpr bool kScaled = std::is_same<T, __half>::value;   // bf16 has fp32's exponents
     const int quads = p.R / 4, items = m * quads, pitch = up_pitch(p.R);
+    const int pad = up_ranks(p.R) / 4 - quads;   // at most 6
+    for (int i = threadIdx.x; i < m * pad; i += kLoraThreads)
+        *reinterpret_cast<uint4*>(v + i / pad * pitch + 16 * (quads + i % pad)) = make_uint4(0u, 0u, 0u, 0u);
     if (kScaled && threadIdx.x < 128) row_max[threadIdx.x] = 0u;
     if (kScaled) __syncthreads();
     for (int i = threadIdx.x; i < items; i += kLoraThreads) {
@@ -327,105 +336,131 @@ __device__ __forceinline__ void take_rows(const LoraParams& p, int m, float fact
     }
 }
 
-// Fragments of B for 32 columns and S steps of 16 ranks.  Column c of MMA tile j is
-// column 8 (c / 2) + 2 j + c % 2 of the 32, so that a thread's two of every tile are
-// eight in a row of the output.
+// Fragments of B for 32 columns and one chunk of ranks (S steps of 16).  Column c of
+// MMA tile j is column 8 (c / 2) + 2 j + c % 2 of the 32, so that a thread's two of every tile are
+// eight in a row of the output; rank 4 S t + 4 k + e of the chunk is thread t's e-th of step k.
 template <class T, int S>
 struct BFragments {
-    uint2 b[S][4];
+    uint32_t b[4][2 * S];
     __device__ __forceinline__ void load(const T* rows, int R, int k0, int nb, int columns, int gr, int t) {
+        const int r = k0 + 4 * S * t, c0 = nb + 8 * (gr >> 1) + (gr & 1);
+        const T* at = rows + static_cast<int64_t>(c0) * R + r;
 #pragma unroll
-        for (int k = 0; k < S; ++k)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int c = nb + 8 * (gr >> 1) + 2 * j + (gr & 1), r = k0 + 16 * k + 4 * t;
-                b[k][j] = r < R && c < columns ? *reinterpret_cast<const uint2*>(rows + static_cast<int64_t>(c) * R + r)
-                                               : make_uint2(0u, 0u);
+        for (int j = 0; j < 4; ++j) {
+            const bool in = r < R && c0 + 2 * j < columns;
+            if constexpr (S == 1) {
+                const uint2 v = in ? *reinterpret_cast<const uint2*>(at + 2 * j * R) : make_uint2(0u, 0u);
+                b[j][0] = v.x;
+                b[j][1] = v.y;
+            } else {
+                const uint4 v = in ? *reinterpret_cast<const uint4*>(at + 2 * j * R) : make_uint4(0u, 0u, 0u, 0u);
+                b[j][0] = v.x;
+                b[j][1] = v.y;
+                b[j][2] = v.z;
+                b[j][3] = v.w;
             }
+        }
     }
 };
 
-// acc += V's 16 rows at v (this thread's place in them) times the fragments.
-template <class T, int S>
-__device__ __forceinline__ void up_mma(float (&acc)[4][4], const uint8_t* v, int pitch, int R, int k0, int t,
-                                       const BFragments<T, S>& f) {
+// acc (FIRST: =, else +=) V's 16 rows times the fragments of a chunk; v: this thread's
+// place in the rows and the chunk.
+template <class T, int S, bool FIRST>
+__device__ __forceinline__ void up_mma(float (&acc)[4][4], const uint8_t* v, int pitch, const BFragments<T, S>& f) {
 #pragma unroll
     for (int k = 0; k < S; ++k) {
-        uint4 f0 = make_uint4(0u, 0u, 0u, 0u), f1 = f0;
-        if (k0 + 16 * k + 4 * t < R) {
-            f0 = *reinterpret_cast<const uint4*>(v + 4 * k0 + 64 * k);
-            f1 = *reinterpret_cast<const uint4*>(v + 8 * pitch + 4 * k0 + 64 * k);
-        }
+        const uint4 f0 = *reinterpret_cast<const uint4*>(v + 16 * k);
+        const uint4 f1 = *reinterpret_cast<const uint4*>(v + 8 * pitch + 16 * k);
         const uint32_t hi[4] = {f0.x, f1.x, f0.y, f1.y}, lo[4] = {f0.z, f1.z, f0.w, f1.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            ptx::mma16816<T>(acc[j], hi, f.b[k][j].x, f.b[k][j].y);
-            ptx::mma16816<T>(acc[j], lo, f.b[k][j].x, f.b[k][j].y);
+            if (FIRST && k == 0) ptx::mma16816_first<T>(acc[j], hi, f.b[j][2 * k], f.b[j][2 * k + 1]);
+            else ptx::mma16816<T>(acc[j], hi, f.b[j][2 * k], f.b[j][2 * k + 1]);
+            ptx::mma16816<T>(acc[j], lo, f.b[j][2 * k], f.b[j][2 * k + 1]);
         }
     }
 }
 
+// Writes a thread's eight columns of one row: y (times `back` for fp16) + beta C.
+template <class T>
+__device__ __forceinline__ void up_store(const LoraParams& p, const float (&acc)[4][4], int h, int64_t at, float back) {
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        y[2 * j] = acc[j][2 * h];
+        y[2 * j + 1] = acc[j][2 * h + 1];
+    }
+    if constexpr (std::is_same<T, __half>::value) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] *= back;
+    }
+    if (p.C != nullptr) {
+        const uint4 cv = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.C) + at);
+        const uint32_t w[4] = {cv.x, cv.y, cv.z, cv.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            y[2 * j] += p.beta * Elem<T>::lo(w[j]);
+            y[2 * j + 1] += p.beta * Elem<T>::hi(w[j]);
+        }
+    }
+    *reinterpret_cast<uint4*>(static_cast<T*>(p.U) + at) =
+        make_uint4(Elem<T>::pack2(y[0], y[1]), Elem<T>::pack2(y[2], y[3]), Elem<T>::pack2(y[4], y[5]), Elem<T>::pack2(y[6], y[7]));
+}
+
 // U of m rows of one group and `columns` columns from n0 on; b_rows: their part of B.
+// The next fragments are on their way while a chunk is multiplied; with one chunk
+// (!LONG) they serve all rows.
 template <class T, int S, bool LONG>
-__device__ __forceinline__ void up(const LoraParams& p, const T* b_rows, bool has, const int32_t* order, int m, int row0,
-                                   int64_t n0, int columns, const uint8_t* v_rows, const uint32_t* row_max) {
+__device__ __forceinline__ void up(const LoraParams& p, const T* b_rows, const int32_t* order, int m, int row0, int64_t n0,
+                                   int columns, const uint8_t* v_rows, const uint32_t* row_max) {
+    constexpr int kStride = kLoraWarps * kLoraColumns;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, t = lane & 3, pitch = up_pitch(p.R);
     BFragments<T, S> next;
-    if (has && warp * kLoraColumns < columns) next.load(b_rows, p.R, 0, warp * kLoraColumns, columns, gr, t);
-    for (int nb = warp * kLoraColumns; nb < columns; nb += kLoraWarps * kLoraColumns) {
+    if (warp * kLoraColumns < columns) next.load(b_rows, p.R, 0, warp * kLoraColumns, columns, gr, t);
+    for (int nb = warp * kLoraColumns; nb < columns; nb += kStride) {
+        BFragments<T, S> b = next;
+        if (!LONG && nb + kStride < columns) next.load(b_rows, p.R, 0, nb + kStride, columns, gr, t);
         const int64_t n = n0 + nb + 8 * t;   // this thread's 8 columns of the output
         const bool n_in = nb + 8 * t < columns;
-        BFragments<T, S> b = next;
-        if (has && nb + kLoraWarps * kLoraColumns < columns)
-            next.load(b_rows, p.R, 0, nb + kLoraWarps * kLoraColumns, columns, gr, t);
         for (int rb = 0; rb < m; rb += 16) {
+            // rows beyond m read what lies there: only outputs that are not written come of it
+            const uint8_t* v = v_rows + (rb + gr) * pitch + 16 * S * t;
             float acc[4][4];
+            if constexpr (!LONG) {
+                up_mma<T, S, true>(acc, v, pitch, b);
+            } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
-            if (has) {
-                // rows beyond m read what lies there: only outputs that are not written come of it
-                const uint8_t* v = v_rows + (rb + gr) * pitch + 16 * t;
-                up_mma<T, S>(acc, v, pitch, p.R, 0, t, b);
-                if constexpr (LONG) {
-                    for (int k0 = 16 * S; k0 < p.R; k0 += 16 * S) {
-                        BFragments<T, S> more;
-                        more.load(b_rows, p.R, k0, nb, columns, gr, t);
-                        up_mma<T, S>(acc, v, pitch, p.R, k0, t, more);
-                    }
+                    for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
+                for (int k0 = 0; k0 < p.R; k0 += 16 * S) {
+                    b = next;
+                    if (k0 + 16 * S < p.R) next.load(b_rows, p.R, k0 + 16 * S, nb, columns, gr, t);
+                    else if (rb + 16 < m) next.load(b_rows, p.R, 0, nb, columns, gr, t);
+                    else if (nb + kStride < columns) next.load(b_rows, p.R, 0, nb + kStride, columns, gr, t);
+                    up_mma<T, S, false>(acc, v + 4 * k0, pitch, b);
                 }
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int r = rb + gr + 8 * h;
                 if (r >= m || !n_in) continue;
-                const int64_t at = static_cast<int64_t>(row0 + order[r]) * p.N + n;
-                float y[8];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    y[2 * j] = acc[j][2 * h];
-                    y[2 * j + 1] = acc[j][2 * h + 1];
-                }
-                if constexpr (std::is_same<T, __half>::value) {
-                    const float back = has ? __uint_as_float(row_exponent(row_max[r]) << 23) : 1.0f;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) y[j] *= back;
-                }
-                if (p.C != nullptr) {
-                    const uint4 cv = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.C) + at);
-                    const uint32_t w[4] = {cv.x, cv.y, cv.z, cv.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        y[2 * j] += p.beta * Elem<T>::lo(w[j]);
-                        y[2 * j + 1] += p.beta * Elem<T>::hi(w[j]);
-                    }
-                }
-                *reinterpret_cast<uint4*>(static_cast<T*>(p.U) + at) =
-                    make_uint4(Elem<T>::pack2(y[0], y[1]), Elem<T>::pack2(y[2], y[3]), Elem<T>::pack2(y[4], y[5]),
-                               Elem<T>::pack2(y[6], y[7]));
+                float back = 1.0f;
+                if constexpr (std::is_same<T, __half>::value) back = __uint_as_float(row_exponent(row_max[r]) << 23);
+                up_store<T>(p, acc, h, static_cast<int64_t>(row0 + order[r]) * p.N + n, back);
             }
         }
+    }
+}
+
+// U = beta C (or zero) of rows without an adapter.
+template <class T>
+__device__ void up_none(const LoraParams& p, const int32_t* order, int m, int row0, int64_t n0, int columns) {
+    const int vecs = columns / 8;
+    for (int i = threadIdx.x; i < m * vecs; i += kLoraThreads) {
+        const int r = i / vecs;
+        const float zero[4][4] = {};
+        up_store<T>(p, zero, 0, static_cast<int64_t>(row0 + order[r]) * p.N + n0 + 8 * (i - r * vecs), 1.0f);
     }
 }
 
@@ -437,7 +472,7 @@ __host__ __device__ constexpr int lora_exchange_bytes(int MT, int R) {
 
 // Grid: clusters that share a tile, tiles; a cluster takes groups in turn, the last
 // of which is the rows without an adapter.  MT: 16-row tiles of ranks of the first
-// product in hand; S: steps of 16 ranks whose part of B is in hand, LONG: R has more of them.
+// product in hand; S: steps of 16 ranks per chunk, LONG: R has more than one chunk.
 template <class T, int MT, int S, bool LONG>
 __global__ void __launch_bounds__(kLoraThreads, 2) lora_kernel(const LoraParams p) {
     extern __shared__ __align__(16) uint8_t smem[];
@@ -469,15 +504,17 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_kernel(const LoraParams 
             ptx::bulk_prefetch_l2(B, static_cast<uint32_t>(min(static_cast<int64_t>(columns) * p.R * 2, int64_t{1} << 20)));
         for (int i = s.start[g]; i < end; i += most) {
             const int m = min(most, end - i);
-            if (has) {
-                down<T, MT>(p, A, s.order + i, m, row0, s0, s1, reinterpret_cast<float*>(exchange), part);
-                ptx::cluster_sync();   // every CTA's partial sums are there
-                take_rows<T>(p, m, factor, ptx::smem_u32(part), exchange, row_max);
-                ptx::cluster_arrive();   // this CTA has read them
+            if (!has) {
+                up_none<T>(p, s.order + i, m, row0, n0, columns);
+                continue;
             }
-            up<T, S, LONG>(p, B, has, s.order + i, m, row0, n0, columns, exchange, row_max);
-            if (has) ptx::cluster_wait();   // nobody reads this CTA's partial sums any more
-            __syncthreads();                // nor V
+            down<T, MT>(p, A, s.order + i, m, row0, s0, s1, reinterpret_cast<float*>(exchange), part);
+            ptx::cluster_sync();   // every CTA's partial sums are there
+            take_rows<T>(p, m, factor, ptx::smem_u32(part), exchange, row_max);
+            ptx::cluster_arrive();   // this CTA has read them
+            up<T, S, LONG>(p, B, s.order + i, m, row0, n0, columns, exchange, row_max);
+            ptx::cluster_wait();   // nobody reads this CTA's partial sums any more
+            __syncthreads();       // nor V
         }
     }
 }
@@ -495,8 +532,7 @@ template <class T>
 gemm_status_t run(const LoraParams& p, dim3 grid, const DeviceView& dev, cudaStream_t s) {
     if (p.R <= 16) return launch<T, 1, 1, false>(p, grid, dev, s);
     if (p.R <= 32) return launch<T, 2, 2, false>(p, grid, dev, s);
-    if (p.R <= 64) return launch<T, 4, 4, false>(p, grid, dev, s);
-    return launch<T, 4, 2, true>(p, grid, dev, s);
+    return launch<T, 2, 2, true>(p, grid, dev, s);
 }
 
 }  // namespace
@@ -523,9 +559,11 @@ gemm_status_t run_lora(bool bf16, const LoraArgs& a, const DeviceView& dev, cuda
         p.width = static_cast<int32_t>((a.N + per - 1) / per * kLoraColumns);
         // Two CTAs per SM, shared out over the tiles.  A batch of requests is one tile with
         // many groups, a prompt's tiles have one or two each.
-        p.tile_rows = M <= kLoraTile ? kLoraTile : kLoraTile / 2;
+        const int64_t most = 2 * dev.sms / kLoraCluster;
+        const int64_t even = ((M + most - 1) / most + 15) / 16 * 16;
+        p.tile_rows = M <= kLoraTile ? kLoraTile : static_cast<int32_t>(std::min<int64_t>(kLoraTile, std::max<int64_t>(96, even)));
         const int64_t tiles = (M + p.tile_rows - 1) / p.tile_rows;
-        int64_t clusters = std::max<int64_t>(1, 2 * dev.sms / kLoraCluster / tiles);
+        int64_t clusters = std::max<int64_t>(1, most / tiles);
         if (tiles == 1) clusters = std::min({clusters, M, a.count + 1});
         const dim3 grid(static_cast<unsigned>(clusters * kLoraCluster), static_cast<unsigned>(tiles), 1);
         const gemm_status_t st = bf16 ? run<__nv_bfloat16>(p, grid, dev, s) : run<__half>(p, grid, dev, s);
