@@ -550,6 +550,9 @@ gemm_status_t get_device(DeviceState** out, int* dev_out) {
         }
         const TiledOps* tiled[3] = {&tiled_ops_2cta256(0), &tiled_ops_1cta128(0), &tiled_ops_1cta256(0)};
         // fp16, bf16, 8-bit (one kernel for both formats), 8-bit with row scales
+        for (int mn : {16, 32, 64})
+            for (int dt : {0, 1})
+                if (skinny_ops(mn, kOpsLora + dt).prepare() != cudaSuccess) { cudaGetLastError(); return GEMM_ERR_CUDA; }
         for (int dt : {0, 1, 2, kOpsRowScaled}) {
             const TiledOps* all[4] = {&tiled_ops_2cta256(dt), &tiled_ops_1cta128(dt), &tiled_ops_1cta256(dt),
                                       &tiled_ops_2cta512(dt)};
@@ -706,7 +709,7 @@ __global__ void epilogue_only_kernel(T* D, int64_t M, int64_t N, EpiParams e) {
 
 gemm_status_t run(const void* A, const void* B, void* D, int64_t M, int64_t N, int64_t K,
                   gemm_variant_t variant, gemm_stream_t stream, int dtype = 0,
-                  const gemm_epilogue_t* epilogue = nullptr, const float* scale_m = nullptr, bool late = false) {
+                  const gemm_epilogue_t* epilogue = nullptr, const float* scale_m = nullptr, const LoraEpi* lora = nullptr) {
     // ---- host-only argument checks (nothing touches a device before these pass)
     if (!dtype_valid(dtype)) return GEMM_ERR_INVALID_VALUE;
     const int in_bytes = dtype_in_bytes(dtype);
@@ -741,7 +744,7 @@ gemm_status_t run(const void* A, const void* B, void* D, int64_t M, int64_t N, i
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int out_dtype = dtype_out(dtype);
     const int bk = stage_k(in_bytes);
-    const int kernels = epi.scale_m != nullptr ? kOpsRowScaled : dtype;
+    const int kernels = lora != nullptr ? kOpsLora + dtype : (epi.scale_m != nullptr ? kOpsRowScaled : dtype);
 
     if (K == 0) return run_empty_sum(D, M, N, epi, out_dtype, dev->sms, s);
 
@@ -755,7 +758,8 @@ gemm_status_t run(const void* A, const void* B, void* D, int64_t M, int64_t N, i
         if (!encode_2d(&tw, B, K, N, bk, static_cast<uint32_t>(pl.tile_n), dtype, kStreamL2Promotion) ||
             !encode_2d(&tx, A, K, M, bk, static_cast<uint32_t>(ops.mn), dtype, kStreamL2Promotion))
             return GEMM_ERR_INVALID_VALUE;
-        SkinnyParams p;
+        pl.stages = skinny_ring_atoms(ops, pl.tile_n);
+        SkinnyParams p{};
         p.M = static_cast<int32_t>(M);
         p.N = static_cast<int32_t>(N);
         p.K = static_cast<int32_t>(K);
@@ -773,7 +777,7 @@ gemm_status_t run(const void* A, const void* B, void* D, int64_t M, int64_t N, i
         p.stream_b = b_bytes >= kStreamBBytes ? 1 : 0;
         p.ab_format = dtype_ab_format(dtype);
         p.prefetch_blocks = skinny_prefetch_blocks(pl, b_bytes);
-        p.late = late ? 1 : 0;
+        if (lora != nullptr) p.lora = *lora;
         if (ops.launch(tw, tx, p, pl.grid_ctas, s) != cudaSuccess) {
             cudaGetLastError();
             return GEMM_ERR_LAUNCH;
@@ -822,6 +826,7 @@ gemm_status_t run(const void* A, const void* B, void* D, int64_t M, int64_t N, i
         return GEMM_OK;
     }
 
+    if (lora != nullptr) return GEMM_ERR_INVALID_VALUE;   // small M only
     const TiledOps& ops = tiled_ops_of(static_cast<gemm_variant_t>(pl.variant), kernels);
     CUtensorMap ta, tb, tbp, td;
     const uint32_t b_rows = static_cast<uint32_t>(ops.b_box_rows);
@@ -848,7 +853,6 @@ gemm_status_t run(const void* A, const void* B, void* D, int64_t M, int64_t N, i
     p.stage_atoms = tiled_stage_atoms(pl, ops.max_stage_atoms);
     p.D = D;
     p.epi = epi;
-    p.late = late ? 1 : 0;
     p.status = dev->status;
     p.timeout_ns = timeout_for(pl.k_blocks);
     if (ops.launch(ta, tb, tbp, td, p, pl.grid_ctas, s) != cudaSuccess) {
@@ -997,8 +1001,8 @@ gemm_status_t stream_key(int dev, gemm_stream_t stream, StreamKey* out) {
 }
 
 gemm_status_t run_dense(int dtype, const void* A, const void* B, void* D, int64_t M, int64_t N, int64_t K,
-                        const gemm_epilogue_t* epilogue, bool late, gemm_stream_t stream) {
-    return run(A, B, D, M, N, K, GEMM_VARIANT_AUTO, stream, dtype, epilogue, nullptr, late);
+                        const gemm_epilogue_t* epilogue, const LoraEpi* lora, gemm_stream_t stream) {
+    return run(A, B, D, M, N, K, GEMM_VARIANT_AUTO, stream, dtype, epilogue, nullptr, lora);
 }
 
 bool encode_map(CUtensorMap* map, const void* base, int elem_bytes, int64_t inner, int64_t outer, uint32_t box_inner,

@@ -128,7 +128,6 @@ struct TiledParams {
     void* D;                  // the output (fp16 or bf16 [M][N]); written directly by the
                               // split-K slice sums, through tmD otherwise
     EpiParams epi;            // fused output transform (epi.on == 0: plain D = A B^T)
-    int32_t late;             // only the epilogue waits for the kernel before (A and B are complete)
     uint32_t* status;         // device status word (0 = ok)
     uint64_t timeout_ns;      // per-wait budget
 };
@@ -263,7 +262,7 @@ inline int choose_ksplit(int64_t tiles, const int* clusters, int64_t k_blocks, i
 #endif
 constexpr int skinny_accs(int mn) { return GEMM_SKINNY_ACCS != 0 ? GEMM_SKINNY_ACCS : (mn <= 32 ? 4 : 1); }
 
-template <int MN_>
+template <int MN_, bool LORA = false>
 struct SkinnyConfig {
     static constexpr int MN = MN_;
     static constexpr int X_BYTES = MN * kStageRowBytes;    // activation (A) slot: MN rows
@@ -277,6 +276,8 @@ struct SkinnyConfig {
     static constexpr int MAX_ATOMS = 64;    // K blocks in flight (a stage holds one or more)
     // partials received from the cluster: [P][128 columns][MN / P rows] fp32 = MN * 128 fp32
     static constexpr int RECV_BYTES = MN * 128 * 4;
+    // with adapters: what they add to a range ([MN rows][128 columns] fp32), V and the ids
+    static constexpr int LORA_BYTES = LORA ? MN * 128 * 4 + kLoraEpiFloats * 4 + 64 * 4 : 0;
     static constexpr int NUM_BARS = 2 * MAX_STAGES + 5;
     // Each of the two accumulator buffers is ACCS MN-column accumulators
     // (MMA k of a K block adds into accumulator k % ACCS).
@@ -285,11 +286,13 @@ struct SkinnyConfig {
     static constexpr int ACC_COLS = ACCS * MN;
     static constexpr int TMEM_COLS = (2 * ACC_COLS < 32) ? 32 : 2 * ACC_COLS;
     // ring = [stages B slots][stages A slots], split at run time (ring_stages)
-    static constexpr int RING_BYTES = (kMaxDynSmem - 1024 - RECV_BYTES - NUM_BARS * 8 - 16) / 1024 * 1024;
+    static constexpr int RING_BYTES = (kMaxDynSmem - 1024 - RECV_BYTES - LORA_BYTES - NUM_BARS * 8 - 16) / 1024 * 1024;
     static constexpr int OFF_RECV = RING_BYTES;
     static constexpr int OFF_BAR = OFF_RECV + RECV_BYTES;
     static constexpr int OFF_SLOT = OFF_BAR + NUM_BARS * 8;
-    static constexpr int SMEM_BYTES = OFF_SLOT + 16 + 1024;
+    static constexpr int OFF_LORA = OFF_SLOT + 16;
+    static constexpr int SMEM_BYTES = OFF_LORA + LORA_BYTES + 1024;
+    static_assert(!LORA || OFF_LORA % 8 == 0, "V is read as 8-byte words");
     static_assert(X_BYTES % 1024 == 0, "activation tile must stay 1024-aligned");
     static_assert(TMEM_COLS <= 512, "TMEM has 512 columns");
     static_assert(RING_BYTES / (128 * kStageRowBytes + X_BYTES) >= 4, "at least four full-width stages");
@@ -313,10 +316,6 @@ GEMM_HD int skinny_stage_atoms(int atoms) {
     return a < 1 ? 1 : (a > 8 ? 8 : a);
 }
 
-using CfgSkinny16 = SkinnyConfig<16>;
-using CfgSkinny32 = SkinnyConfig<32>;
-using CfgSkinny64 = SkinnyConfig<64>;
-
 // Largest cluster (K pieces per column range) of the column-range kernel.
 constexpr int kSkinnyMaxPieces = 8;
 
@@ -336,7 +335,7 @@ struct SkinnyParams {
     int32_t stream_b;         // B is too large to stay in L2: load it evict-first
     uint32_t ab_format;       // operand format field of the MMA instruction descriptor
     int32_t prefetch_blocks;  // B blocks a CTA prefetches into L2 before its dependency wait
-    int32_t late;             // only the epilogue waits for the kernel before (A and B are complete)
+    LoraEpi lora;             // read only by the kernels built with adapters
 };
 
 // Stream-K kernel (GEMM_VARIANT_SKINNY_STREAMK, and the no-allocation entry

@@ -38,6 +38,19 @@ struct EpiParams {
     const float* scale_m;  // [M] fp32: read only by the kernels built with row scales
 };
 
+// Low-rank adapters in the epilogue of the small-M kernel: row m of D gets
+// B_a V[m], a = ids[m], added after the scales.
+struct LoraEpi {
+    const float* V;       // [M][R], 16-byte aligned; not used where ids[m] is outside [0, count)
+    const void* B;        // [count][N][R] in D's type
+    const int32_t* ids;   // [M]
+    int32_t R, count;     // R % 8 == 0
+};
+// M * R of one launch at most.  The part is summed on the epilogue's warps while the K loop
+// runs, a row and 8 ranks per load of a thread, 8 loads under way: about 1 us for
+// 64 of M * R, which the loop hides up to here.
+constexpr int kLoraEpiFloats = 1024;
+
 template <class T>
 struct Elem;
 

@@ -27,10 +27,10 @@ gemm_status_t device_view(DeviceView* out);
 gemm_status_t check_epilogue(const gemm_epilogue_t* e, const void* D, int64_t M, int64_t N);
 EpiParams epi_params(const gemm_epilogue_t* e);
 
-// gemm_nt_ex with AUTO (api.cu).  late: the stream's last kernel was launched before
-// this one's operands, and all but C, were complete, so only the epilogue waits for it.
+// gemm_nt_ex of 16-bit operands with AUTO, and with the second half of a few rows'
+// adapters in its epilogue (nullptr: none) (api.cu).
 gemm_status_t run_dense(int dtype, const void* A, const void* B, void* D, int64_t M, int64_t N, int64_t K,
-                        const gemm_epilogue_t* epilogue, bool late, gemm_stream_t stream);
+                        const gemm_epilogue_t* epilogue, const LoraEpi* lora, gemm_stream_t stream);
 
 // D = act(beta * C + bias), the K == 0 result (api.cu).
 gemm_status_t run_empty_sum(void* D, int64_t M, int64_t N, const EpiParams& epi, int out_dtype, int sms,

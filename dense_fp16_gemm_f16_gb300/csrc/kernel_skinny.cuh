@@ -65,9 +65,62 @@ __device__ __forceinline__ void skinny_scale_rows(uint32_t (&v)[MN], const float
         v[m] = __float_as_uint(__uint_as_float(v[m]) * __shfl_sync(0xffffffffu, r[m / 32], m % 32));
 }
 
+// V and the ids into shared memory, by the epilogue's threads.
+__device__ __forceinline__ void skinny_lora_load(const LoraEpi& l, int M, int tid, float* V, int32_t* ids) {
+    const int pairs = l.R / 2;
+    for (int i = tid; i < M * pairs; i += 32 * kEpiWarps) {
+        const int m = i / pairs, id = l.ids[m];
+        const bool has = id >= 0 && id < l.count;
+        reinterpret_cast<float2*>(V)[i] = has ? reinterpret_cast<const float2*>(l.V)[i] : make_float2(0.0f, 0.0f);
+        if (i == m * pairs) ids[m] = has ? id : -1;
+    }
+    ptx::named_bar_sync(1, 32 * kEpiWarps);
+}
+
+// out[i * 128] = what the adapters add to column n of rows m0 + i, i < rows: 8 rows at
+// a time, so that 8 loads are under way.  fp32 throughout.
+template <class T>
+__device__ __forceinline__ void skinny_lora_column(const LoraEpi& l, int64_t N, int64_t n, bool in, int m0, int rows,
+                                                   const float* V, const int32_t* ids, float* out) {
+    for (int i0 = 0; i0 < rows; i0 += 8) {
+        float sum[8];
+        const uint4* at[8];
+        const float* v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int m = m0 + (i0 + i < rows ? i0 + i : i0);
+            const int id = ids[m];
+            sum[i] = 0.0f;
+            v[i] = V + m * l.R;
+            at[i] = in && id >= 0 && i0 + i < rows
+                        ? reinterpret_cast<const uint4*>(static_cast<const T*>(l.B) + (id * N + n) * l.R)
+                        : nullptr;
+        }
+#pragma unroll 2
+        for (int r = 0; r < l.R; r += 8) {
+            uint4 b[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) b[i] = at[i] != nullptr ? at[i][r / 8] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t w[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 f = reinterpret_cast<const float2*>(v[i] + r)[e];
+                    sum[i] = fmaf(f.x, Elem<T>::lo(w[e]), sum[i]);
+                    sum[i] = fmaf(f.y, Elem<T>::hi(w[e]), sum[i]);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i0 + i < rows) out[(i0 + i) * 128] = at[i] != nullptr ? sum[i] : 0.0f;
+    }
+}
+
 // T is the element type of D (and C, bias); F8 selects 8-bit operands; ROWS = with
-// a scale per row of A.
-template <class Cfg, class T, bool F8, bool ROWS = false>
+// a scale per row of A; LORA = with adapters.
+template <class Cfg, class T, bool F8, bool ROWS = false, bool LORA = false>
 __global__ void __launch_bounds__(kThreads, 1)
 gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                    const SkinnyParams p) {
@@ -144,7 +197,7 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     // of an SM's shared memory, so a CTA of this grid never shares an SM, or
     // its TMEM, with one of the last.)
     ptx::griddep_launch_dependents();
-    if (!p.late) ptx::griddep_wait();
+    ptx::griddep_wait();
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -231,7 +284,6 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         if (clustered) ptx::cluster_sync();   // meets the epilogue's exchange barrier
     } else {
         // ------------------------------------------------------------ epilogue
-        if (p.late) ptx::griddep_wait();   // C is read, and D written, only by these warps
         const int q = warp & 3;
         const int n_local = q * 32 + lane;   // TMEM lane = column within the range
         const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
@@ -242,6 +294,11 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
             for (int i = 0; i < (MN + 31) / 32; ++i)
                 row_scale[i] = 32 * i + lane < p.M ? p.epi.scale_m[32 * i + lane] : 0.0f;
         }
+        // this thread's column of what the adapters add, and what it is made of
+        float* lora_out = reinterpret_cast<float*>(smem + Cfg::OFF_LORA) + n_local;
+        float* lora_v = reinterpret_cast<float*>(smem + Cfg::OFF_LORA + MN * 128 * 4);
+        int32_t* lora_ids = reinterpret_cast<int32_t*>(lora_v + kLoraEpiFloats);
+        if constexpr (LORA) skinny_lora_load(p.lora, p.M, static_cast<int>(threadIdx.x) - 64, lora_v, lora_ids);
         if (!clustered) {
             // one whole K loop per range: straight from TMEM to D
             uint32_t it = 0;
@@ -252,7 +309,13 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                 const bool col_in = n_local < p.width && n < p.N;
                 // this column's C values, factor and bias, fetched while the K loop runs
                 EpiColumn<T, MN> ec;
-                if (p.epi.on && col_in) ec.load(p.epi, n, p.M, p.N);
+                if ((p.epi.on || LORA) && col_in) ec.load(p.epi, n, p.M, p.N);
+                float scale_n = 1.0f;
+                if constexpr (LORA) {
+                    skinny_lora_column<T>(p.lora, p.N, n, col_in, 0, p.M, lora_v, lora_ids, lora_out);
+                    if (col_in) scale_n = ec.a;
+                    ec.a = 1.0f;   // applied before the adapters' part is added
+                }
                 if (!wait_phase_warp(tfull_bar(buf), use, p.status, kSiteEpilogueTmemFull, p.timeout_ns)) break;
                 ptx::tc_fence_after();
                 uint32_t v[MN];
@@ -261,6 +324,11 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(tempty_bar(buf));
+                if constexpr (LORA) {
+#pragma unroll
+                    for (int m = 0; m < MN; ++m)
+                        if (m < p.M) v[m] = __float_as_uint(__uint_as_float(v[m]) * scale_n + lora_out[m * 128]);
+                }
                 if (col_in) {
                     if (p.epi.on) {
 #pragma unroll
@@ -284,6 +352,14 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
             // this column's factor alpha * s[n] and bias, fetched while the K loop runs
             EpiColumnFactors<T> cf;
             if (p.epi.on && col_in) cf.load(p.epi, n);
+            float scale_n = 1.0f;
+            if constexpr (LORA) {
+                // the rows that this CTA finishes
+                const int MS = MN / P, left = p.M - j * MS;
+                skinny_lora_column<T>(p.lora, p.N, n, col_in, j * MS, left < MS ? left : MS, lora_v, lora_ids, lora_out);
+                scale_n = cf.a;
+                cf.a = 1.0f;   // applied before the adapters' part is added
+            }
             const bool ready = r < p.ranges &&
                                wait_phase_warp(tfull_bar(0), 0, p.status, kSiteEpilogueTmemFull, p.timeout_ns);
             uint32_t v[MN];
@@ -328,6 +404,7 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                 auto finish = [&](int ml, float acc) {
                     const int m = j * MS + ml;
                     if (m < p.M) {
+                        if constexpr (LORA) acc = acc * scale_n + lora_out[ml * 128];
                         const float x = p.epi.on ? cf.apply(p.epi, acc, m, n, p.N) : acc;
                         D[m * static_cast<int64_t>(p.N) + n] = Elem<T>::from_float(x);
                     }

@@ -225,7 +225,7 @@ gemm_tiled_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     // (Every kernel here takes more than half of an SM's shared memory, so a
     // CTA of this grid never shares an SM, or its TMEM, with one of the last.)
     ptx::griddep_launch_dependents();
-    if (!p.late) ptx::griddep_wait();
+    ptx::griddep_wait();
 
     const int64_t cluster_idx = blockIdx.x / csize;
     const int64_t num_clusters = gridDim.x / csize;
@@ -385,7 +385,6 @@ gemm_tiled_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
         }
     } else if (split) {
         // ------------------------------------------------------------ epilogue, split K
-        if (p.late) ptx::griddep_wait();   // C is read, and D written, only by these warps
         // One tile per cluster (the planner launches exactly one cluster per
         // tile).  Every thread reaches both barriers, whatever happened before.
         const int q = warp & 3;
@@ -409,7 +408,6 @@ gemm_tiled_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
         if (ready) split_k_reduce<Cfg, T, ROWS>(smem, p, piece, row, grow, n0, p.ksplit, row_scale);
     } else {
         // ------------------------------------------------------------ epilogue
-        if (p.late) ptx::griddep_wait();   // C is read, and D written, only by these warps
         const int q = warp & 3;    // TMEM lanes 32q .. 32q+31 are readable by this warp
         const int ew = warp - 2;   // owner of staging buffers 2ew, 2ew+1
         const int h = ew / kEpiWarps;   // the consumer (accumulator) this warp drains

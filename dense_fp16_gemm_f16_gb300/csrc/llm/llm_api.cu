@@ -367,7 +367,7 @@ gemm_status_t check_lora(int dtype, const void* X, const gemm_lora_t* l, const i
         (l->factors != nullptr && ranges_overlap(U, out, l->factors, count * 4)) ||
         (ids != nullptr && ranges_overlap(U, out, ids, M * 4)))
         return GEMM_ERR_INVALID_VALUE;
-    *a = LoraArgs{X, l->A, l->B, l->factors, ids, nullptr, 0.0f, nullptr, M, N, K, R, count};
+    *a = LoraArgs{X, l->A, l->B, l->factors, ids, nullptr, 0.0f, nullptr, nullptr, M, N, K, R, count};
     return GEMM_OK;
 }
 
@@ -411,7 +411,18 @@ gemm_status_t lora_nt(int dtype, const void* X, const gemm_weights_t* weights, c
         const EpiParams plain = epi_params(epilogue);
         if (K == 0) return run_empty_sum(D, M, N, plain, dtype, dev.sms, reinterpret_cast<cudaStream_t>(stream));
         return w.scales != nullptr ? run_w4_gemm(dtype == GEMM_DTYPE_BF16, X, w, D, M, N, K, plain, dev, stream)
-                                   : run_dense(dtype, X, w.data, D, M, N, K, epilogue, false, stream);
+                                   : run_dense(dtype, X, w.data, D, M, N, K, epilogue, nullptr, stream);
+    }
+    if (w.scales == nullptr && M <= 64 && M * a.R <= kLoraEpiFloats) {
+        // few rows: X Aᵀ by itself, its product with B on the idle warps of the projection's kernel
+        Scratch ws;
+        st = get_scratch(dev.dev, stream, static_cast<size_t>(M * a.R * 4), &ws);
+        if (st != GEMM_OK) return st;
+        a.V = reinterpret_cast<float*>(ws.data);
+        st = run_lora(dtype == GEMM_DTYPE_BF16, a, dev, reinterpret_cast<cudaStream_t>(stream));
+        if (st != GEMM_OK) return st;
+        const LoraEpi part{a.V, l->B, ids, static_cast<int32_t>(a.R), static_cast<int32_t>(a.count)};
+        return run_dense(dtype, X, w.data, D, M, N, K, epilogue, &part, stream);
     }
     a.C = epi.beta != 0.0f ? epi.C : nullptr;
     a.beta = epi.beta;
@@ -421,7 +432,7 @@ gemm_status_t lora_nt(int dtype, const void* X, const gemm_weights_t* weights, c
     st = run_lora(dtype == GEMM_DTYPE_BF16, a, dev, reinterpret_cast<cudaStream_t>(stream));
     if (st != GEMM_OK) return st;
     return w.scales != nullptr ? run_w4_gemm(dtype == GEMM_DTYPE_BF16, X, w, D, M, N, K, epi_params(&epi), dev, stream)
-                               : run_dense(dtype, X, w.data, D, M, N, K, &epi, true, stream);
+                               : run_dense(dtype, X, w.data, D, M, N, K, &epi, nullptr, stream);
 }
 
 }  // namespace

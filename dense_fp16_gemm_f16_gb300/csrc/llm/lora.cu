@@ -3,7 +3,7 @@
 //
 // One kernel.  Rows are taken in tiles of up to 256; a CTA puts the rows of a tile in
 // order of their adapters itself, so no list has to be made by a kernel before, and every
-// adapter's matrices are read once per tile.  A cluster of eight CTAs takes one
+// adapter's matrices are read once per tile.  A cluster of eight (or four) CTAs takes one
 // adapter's rows: each CTA forms V = X Aᵀ over an eighth of K, the partial sums meet in
 // distributed shared memory in a fixed order, and each CTA multiplies V by an
 // eighth of B's rows.
@@ -34,7 +34,7 @@ constexpr int kLoraWarps = kLoraThreads / 32;
 constexpr int kLoraTile = 256;           // most rows per tile: one per thread
 constexpr int kLoraStepK = 32;           // k per warp and step of `down`: 16 bytes per thread and row
 constexpr int kLoraColumns = 32;         // columns per warp and step of `up`
-constexpr int kLoraCluster = 8;
+constexpr int kLoraMaxCluster = 8;
 
 struct LoraParams {
     const void* X;           // [M][K]
@@ -44,26 +44,32 @@ struct LoraParams {
     const int32_t* ids;      // [M], or nullptr: no row has an adapter
     const void* C;           // [M][N] or nullptr
     void* U;                 // [M][N]
+    float* V;                // [M][R]: factors X Aᵀ is all that is wanted, or nullptr
     int32_t M, N, K, R, count;
     int32_t tile_rows, k_steps, width;   // width: columns per CTA of a cluster
+    int32_t cluster;         // its CTAs
     float beta;
 };
 
-// The rows of one tile in order of their adapters, and the table that finds them.
-constexpr int kLoraSlots = 2 * kLoraTile;
+// The rows of one tile in order of their adapters.
 struct Groups {
     int32_t order[kLoraTile];         // rows of the tile, group by group, each in row order
     int32_t start[kLoraTile + 1];     // group i is order[start[i]] .. order[start[i + 1] - 1]
     int32_t adapter[kLoraTile];       // of each group, in the order of their first rows
-    int32_t key[kLoraSlots];          // the adapter that has this slot, -1 free
-    int32_t first[kLoraSlots];        // its first row, then its group
-    alignas(16) uint8_t rows[kLoraSlots][kLoraWarps];   // its rows in each warp
-    int32_t leaders[kLoraWarps];
-    int32_t none[kLoraWarps];         // rows without an adapter in each warp
     int32_t n;                        // groups with an adapter; rows without one lie behind them
 };
-static_assert(kLoraWarps == 8, "a slot's row counts are read as 8 bytes");
 constexpr int kGroupsBytes = (sizeof(Groups) + 127) / 128 * 128;
+
+// The table that finds them.
+constexpr int kLoraSlots = 2 * kLoraTile;
+struct GroupTable {
+    uint8_t rows[kLoraSlots][kLoraWarps];   // an adapter's rows in each warp
+    int32_t key[kLoraSlots];          // the adapter that has this slot, -1 free
+    int32_t first[kLoraSlots];        // its first row, then its group
+    int32_t leaders[kLoraWarps];
+    int32_t none[kLoraWarps];         // rows without an adapter in each warp
+};
+static_assert(kLoraWarps == 8, "a slot's row counts are cleared as 8 bytes");
 
 // Rows of warps before `warp` in a slot's counts.
 __device__ __forceinline__ int rows_before(const uint8_t (&rows)[kLoraWarps], int warp) {
@@ -76,8 +82,43 @@ __device__ __forceinline__ int rows_before(const uint8_t (&rows)[kLoraWarps], in
 // Called by the whole CTA, one row per thread.  Which slot an adapter gets depends on
 // timing, groups and their order do not.  Ids are read past L1: a kernel launched early may
 // share an SM with one that read older ids there.
-__device__ void group_rows(const LoraParams& p, int row0, int rows, Groups& s) {
+__device__ void group_rows(const LoraParams& p, int row0, int rows, Groups& s, GroupTable& table) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (rows <= 32) {   // one warp: no table
+        if (warp == 0) {
+            int id = -2;
+            if (lane < rows) {
+                id = p.ids != nullptr ? __ldcg(p.ids + row0 + lane) : -1;
+                if (id < 0 || id >= p.count) id = -1;
+            }
+            const uint32_t mine = __match_any_sync(0xffffffffu, id), before = (1u << lane) - 1u;
+            const int lead = __ffs(mine) - 1;
+            const uint32_t leads = __ballot_sync(0xffffffffu, id >= 0 && lead == lane);
+            const uint32_t none = __ballot_sync(0xffffffffu, id == -1);
+            const int number = __popc(leads & ((1u << lead) - 1u));
+            // rows of the groups whose first row comes earlier
+            int start = 0;
+            for (uint32_t l = leads; l != 0; l &= l - 1) {
+                const int at = __ffs(l) - 1, size = __popc(__shfl_sync(0xffffffffu, mine, at));
+                start += at < lead ? size : 0;
+            }
+            if (id >= 0) {
+                s.order[start + __popc(mine & before)] = lane;
+                if (lead == lane) {
+                    s.adapter[number] = id;
+                    s.start[number] = start;
+                }
+            } else if (id == -1) {
+                s.order[rows - __popc(none) + __popc(none & before)] = lane;
+            }
+            if (lane == 0) {
+                s.n = __popc(leads);
+                s.start[s.n] = rows - __popc(none);
+            }
+        }
+        __syncthreads();
+        return;
+    }
     int id = -2;   // no row
     if (tid < rows) {
         id = p.ids != nullptr ? __ldcg(p.ids + row0 + tid) : -1;
@@ -85,9 +126,9 @@ __device__ void group_rows(const LoraParams& p, int row0, int rows, Groups& s) {
     }
 #pragma unroll
     for (int i = tid; i < kLoraSlots; i += kLoraThreads) {
-        s.key[i] = -1;
-        s.first[i] = kLoraTile;
-        *reinterpret_cast<uint2*>(s.rows[i]) = make_uint2(0u, 0u);
+        table.key[i] = -1;
+        table.first[i] = kLoraTile;
+        *reinterpret_cast<uint2*>(table.rows[i]) = make_uint2(0u, 0u);
     }
     s.start[tid] = 0;
     __syncthreads();
@@ -98,34 +139,34 @@ __device__ void group_rows(const LoraParams& p, int row0, int rows, Groups& s) {
     if (id >= 0 && in_warp == 0) {
         slot = static_cast<int>((static_cast<uint32_t>(id) * 2654435761u) >> 23);   // of 512
         while (true) {   // at most 256 adapters in 512 slots
-            const int other = atomicCAS(&s.key[slot], -1, id);
+            const int other = atomicCAS(&table.key[slot], -1, id);
             if (other == -1 || other == id) break;
             slot = (slot + 1) & (kLoraSlots - 1);
         }
-        s.rows[slot][warp] = static_cast<uint8_t>(__popc(mine));
-        atomicMin(&s.first[slot], tid);
+        table.rows[slot][warp] = static_cast<uint8_t>(__popc(mine));
+        atomicMin(&table.first[slot], tid);
     }
     slot = __shfl_sync(0xffffffffu, slot, lead_lane);
     const uint32_t none = __ballot_sync(0xffffffffu, id == -1);
-    if (lane == 0) s.none[warp] = __popc(none);
+    if (lane == 0) table.none[warp] = __popc(none);
     __syncthreads();
-    const bool leads = id >= 0 && s.first[slot] == tid;
+    const bool leads = id >= 0 && table.first[slot] == tid;
     const uint32_t mask = __ballot_sync(0xffffffffu, leads);
-    if (lane == 0) s.leaders[warp] = __popc(mask);
+    if (lane == 0) table.leaders[warp] = __popc(mask);
     __syncthreads();
     int number = __popc(mask & ((1u << lane) - 1u)), n = 0, before = 0;
 #pragma unroll
     for (int w = 0; w < kLoraWarps; ++w) {
         if (w < warp) {
-            number += s.leaders[w];
-            before += s.none[w];
+            number += table.leaders[w];
+            before += table.none[w];
         }
-        n += s.leaders[w];
+        n += table.leaders[w];
     }
     if (leads) {
-        s.first[slot] = number;
+        table.first[slot] = number;
         s.adapter[number] = id;
-        s.start[number] = rows_before(s.rows[slot], kLoraWarps);   // sizes first
+        s.start[number] = rows_before(table.rows[slot], kLoraWarps);   // sizes first
     }
     __syncthreads();
     if (warp == 0) {   // sizes to starts, 8 groups per lane
@@ -152,37 +193,56 @@ __device__ void group_rows(const LoraParams& p, int row0, int rows, Groups& s) {
     }
     __syncthreads();
     // behind the last group, start holds the number of rows that have an adapter
-    if (id >= 0) s.order[s.start[s.first[slot]] + rows_before(s.rows[slot], warp) + in_warp] = tid;
+    if (id >= 0) s.order[s.start[table.first[slot]] + rows_before(table.rows[slot], warp) + in_warp] = tid;
     else if (id == -1) s.order[s.start[n] + before + in_warp] = tid;
     __syncthreads();
 }
 
 // -------------------------------------------------------------------------- down
-// 16-byte loads of a thread that are under way at one time, and how many steps make them.
-template <int MT, int NT>
-constexpr int kDownUnroll = 12 / (2 * MT + NT);
-// Floats between the sums of two rows in the warps' exchange: the two columns of
-// a fragment fall into different banks.
+// Every thread copies the pieces of its own fragments to places of its own in shared
+// memory (cp.async), some steps ahead, and reads them back: many bytes under way without
+// registers for them, and nobody to wait for.
+__host__ __device__ constexpr int down_slots(int MT) { return MT == 1 ? 18 : 16; }   // 16-byte places per thread
+// Floats between the sums of two rows in the warps' exchange, which takes the same
+// space: the two columns of a fragment fall into different banks.
 __host__ __device__ constexpr int down_pitch(int MT) { return 16 * MT + 4; }
-__host__ __device__ constexpr int down_bytes(int MT) { return kLoraWarps * 32 * down_pitch(MT) * 4; }
+__host__ __device__ constexpr int down_bytes(int MT) { return down_slots(MT) * 16 * kLoraThreads; }
+static_assert(kLoraWarps * 32 * down_pitch(1) * 4 <= down_bytes(1) && kLoraWarps * 32 * down_pitch(2) * 4 <= down_bytes(2),
+              "the exchange fits the places");
 
 // part = V of m <= 8 NT WR rows (`rows`) and 16 MT ranks from r0 on over the k steps
 // [s0, s1): WR parts of 8 NT rows, the steps of each dealt out to 8 / WR warps.
 template <class T, int MT, int NT, int WR>
 __device__ __forceinline__ void down_rows(const LoraParams& p, const T* A, int r0, const int32_t* rows, int m, int row0,
-                                          int s0, int s1, float* red, float* part) {
-    constexpr int KW = kLoraWarps / WR, UN = kDownUnroll<MT, NT>, P = down_pitch(MT);
+                                          int s0, int s1, uint8_t* space, float* part) {
+    constexpr int KW = kLoraWarps / WR, NF = 2 * MT + NT, D = down_slots(MT) / NF, P = down_pitch(MT);
+    static_assert(D >= 2, "a step ahead at least");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int first = warp / KW * 8 * NT;   // this warp's rows
-    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t places = ptx::smem_u32(space) + threadIdx.x * 16;   // f of stage d: (d * NF + f) * 4096 behind
     const T* a_ptr = A + static_cast<int64_t>(r0 + g) * p.K + 8 * t;
     const T* x_ptr[NT];
-    bool x_in[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-        x_in[j] = first + 8 * j + g < m;
-        x_ptr[j] = static_cast<const T*>(p.X) + static_cast<int64_t>(row0 + (x_in[j] ? rows[first + 8 * j + g] : 0)) * p.K + 8 * t;
+        const bool in = first + 8 * j + g < m;
+        x_ptr[j] = in ? static_cast<const T*>(p.X) + static_cast<int64_t>(row0 + rows[first + 8 * j + g]) * p.K + 8 * t : nullptr;
     }
+    // copies of one step into stage d; what lies outside becomes zeros
+    auto fetch = [&](int s, int d) {
+        const int64_t k = static_cast<int64_t>(s) * kLoraStepK;
+        const bool in = s < s1 && k + 8 * t < p.K;   // K % 8 == 0: all eight or none
+        const uint32_t to = places + d * (NF * 16 * kLoraThreads);
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i) {
+            const bool take = in && r0 + 8 * i + g < p.R;
+            ptx::cp_async16_or_zero(to + i * (16 * kLoraThreads), take ? a_ptr + static_cast<int64_t>(8 * i) * p.K + k : A, take);
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const bool take = in && x_ptr[j] != nullptr;
+            ptx::cp_async16_or_zero(to + (2 * MT + j) * (16 * kLoraThreads), take ? x_ptr[j] + k : A, take);
+        }
+    };
     float acc[MT][NT][4];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -191,37 +251,41 @@ __device__ __forceinline__ void down_rows(const LoraParams& p, const T* A, int r
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.0f;
     if (first < m) {
-        for (int s = s0 + warp % KW; s < s1; s += KW * UN) {
-            uint4 a[UN][MT][2], x[UN][NT];
+        int s = s0 + warp % KW;
 #pragma unroll
-            for (int u = 0; u < UN; ++u) {
-                const int64_t k = static_cast<int64_t>(s + u * KW) * kLoraStepK;
-                const bool in = s + u * KW < s1 && k + 8 * t < p.K;   // K % 8 == 0: all eight or none
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        a[u][i][h] = in && r0 + 16 * i + 8 * h + g < p.R
-                                         ? *reinterpret_cast<const uint4*>(a_ptr + (16 * i + 8 * h) * static_cast<int64_t>(p.K) + k)
-                                         : none;
-#pragma unroll
-                for (int j = 0; j < NT; ++j) x[u][j] = in && x_in[j] ? *reinterpret_cast<const uint4*>(x_ptr[j] + k) : none;
-            }
-#pragma unroll
-            for (int u = 0; u < UN; ++u)
-#pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    const uint32_t lo[4] = {a[u][i][0].x, a[u][i][1].x, a[u][i][0].y, a[u][i][1].y};
-                    const uint32_t hi[4] = {a[u][i][0].z, a[u][i][1].z, a[u][i][0].w, a[u][i][1].w};
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        ptx::mma16816<T>(acc[i][j], lo, x[u][j].x, x[u][j].y);
-                        ptx::mma16816<T>(acc[i][j], hi, x[u][j].z, x[u][j].w);
-                    }
-                }
+        for (int d = 0; d < D - 1; ++d) {
+            fetch(s + d * KW, d);
+            ptx::cp_async_commit();
         }
+        int d = 0;
+        for (; s < s1; s += KW) {
+            ptx::cp_async_wait_group<D - 2>();   // this step's copies, by this thread, are done
+            uint32_t a[2 * MT][4], x[NT][4];
+            const uint32_t from = places + d * (NF * 16 * kLoraThreads);
+#pragma unroll
+            for (int i = 0; i < 2 * MT; ++i) ptx::ld_shared_v4_u32(from + i * (16 * kLoraThreads), a[i]);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) ptx::ld_shared_v4_u32(from + (2 * MT + j) * (16 * kLoraThreads), x[j]);
+            const int back = d == 0 ? D - 1 : d - 1;   // the stage read in the step before
+            fetch(s + (D - 1) * KW, back);
+            ptx::cp_async_commit();
+            if (++d == D) d = 0;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                const uint32_t lo[4] = {a[2 * i][0], a[2 * i + 1][0], a[2 * i][1], a[2 * i + 1][1]};
+                const uint32_t hi[4] = {a[2 * i][2], a[2 * i + 1][2], a[2 * i][3], a[2 * i + 1][3]};
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    ptx::mma16816<T>(acc[i][j], lo, x[j][0], x[j][1]);
+                    ptx::mma16816<T>(acc[i][j], hi, x[j][2], x[j][3]);
+                }
+            }
+        }
+        ptx::cp_async_wait_group<0>();
     }
+    __syncthreads();   // nobody's copies are under way
     // the sums of a part's warps meet in shared memory and are added in their order
+    float* red = reinterpret_cast<float*>(space);
     float* mine = red + warp * 8 * NT * P;
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -244,13 +308,13 @@ __device__ __forceinline__ void down_rows(const LoraParams& p, const T* A, int r
 
 template <class T, int MT>
 __device__ __forceinline__ void down(const LoraParams& p, const T* A, const int32_t* rows, int m, int row0, int s0, int s1,
-                                     float* red, float* part) {
+                                     uint8_t* space, float* part) {
     for (int r0 = 0; r0 < p.R; r0 += 16 * MT) {
-        if (m <= 8) down_rows<T, MT, 1, 1>(p, A, r0, rows, m, row0, s0, s1, red, part);
-        else if (m <= 16) down_rows<T, MT, 2, 1>(p, A, r0, rows, m, row0, s0, s1, red, part);
-        else if (m <= 32) down_rows<T, MT, 4, 1>(p, A, r0, rows, m, row0, s0, s1, red, part);
-        else if (m <= 64) down_rows<T, MT, 4, 2>(p, A, r0, rows, m, row0, s0, s1, red, part);
-        else down_rows<T, MT, 4, 4>(p, A, r0, rows, m, row0, s0, s1, red, part);
+        if (m <= 8) down_rows<T, MT, 1, 1>(p, A, r0, rows, m, row0, s0, s1, space, part);
+        else if (m <= 16) down_rows<T, MT, 2, 1>(p, A, r0, rows, m, row0, s0, s1, space, part);
+        else if (m <= 32) down_rows<T, MT, 4, 1>(p, A, r0, rows, m, row0, s0, s1, space, part);
+        else if (m <= 64) down_rows<T, MT, 4, 2>(p, A, r0, rows, m, row0, s0, s1, space, part);
+        else down_rows<T, MT, 4, 4>(p, A, r0, rows, m, row0, s0, s1, space, part);
     }
 }
 
@@ -266,7 +330,7 @@ __host__ __device__ constexpr int up_pitch(int R) {
     return up_ranks(R) * 4 + (((R <= 16 ? 64 : 16) - up_ranks(R) * 4) & 127);
 }
 // rows of V in shared memory at one time
-__host__ __device__ constexpr int up_rows(int R) { return R <= 64 ? 128 : (R <= 128 ? 64 : 32); }
+__host__ __device__ constexpr int up_rows(int R) { return R <= 16 ? 128 : (R <= 32 ? 64 : 32); }
 
 // The two numbers of type T that v is the sum of.
 template <class T>
@@ -293,13 +357,14 @@ __device__ __forceinline__ void take_rows(const LoraParams& p, int m, float fact
     if (kScaled) __syncthreads();
     for (int i = threadIdx.x; i < items; i += kLoraThreads) {
         const int r = i / quads, q = i - r * quads;
-        float o[kLoraCluster][4], a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        float o[kLoraMaxCluster][4], a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int c = 0; c < kLoraCluster; ++c) ptx::ld_cluster_v4(ptx::mapa(part + 16 * i, c), o[c]);
+        for (int c = 0; c < kLoraMaxCluster; ++c)
+            if (c < p.cluster) ptx::ld_cluster_v4(ptx::mapa(part + 16 * i, c), o[c]);
 #pragma unroll
-        for (int c = 0; c < kLoraCluster; ++c)
+        for (int c = 0; c < kLoraMaxCluster; ++c)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) a[e] += o[c][e];
+            for (int e = 0; e < 4; ++e) a[e] += c < p.cluster ? o[c][e] : 0.0f;
         uint8_t* at = v + r * pitch + 16 * q;
         float top = 0.0f, h[4], l[4];
 #pragma unroll
@@ -336,30 +401,94 @@ __device__ __forceinline__ void take_rows(const LoraParams& p, int m, float fact
     }
 }
 
+// The same rows, not cut, to V: every CTA of the cluster writes a part.
+__device__ __forceinline__ void give_rows(const LoraParams& p, int m, float factor, uint32_t part, int rank, int row0,
+                                          const int32_t* order) {
+    const int quads = p.R / 4;
+    for (int i = rank * kLoraThreads + threadIdx.x; i < m * quads; i += p.cluster * kLoraThreads) {
+        const int r = i / quads, q = i - r * quads;
+        float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int c = 0; c < kLoraMaxCluster; ++c) {
+            float o[4];
+            if (c >= p.cluster) break;
+            ptx::ld_cluster_v4(ptx::mapa(part + 16 * i, c), o);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a[e] += o[e];
+        }
+        *reinterpret_cast<float4*>(p.V + static_cast<int64_t>(row0 + order[r]) * p.R + 4 * q) =
+            make_float4(a[0] * factor, a[1] * factor, a[2] * factor, a[3] * factor);
+    }
+}
+
 // Fragments of B for 32 columns and one chunk of ranks (S steps of 16).  Column c of
 // MMA tile j is column 8 (c / 2) + 2 j + c % 2 of the 32, so that a thread's two of every tile are
 // eight in a row of the output; rank 4 S t + 4 k + e of the chunk is thread t's e-th of step k.
+// As in the first product, every thread copies its own to places of its own, up_ahead(S) chunks ahead.
 template <class T, int S>
 struct BFragments {
     uint32_t b[4][2 * S];
-    __device__ __forceinline__ void load(const T* rows, int R, int k0, int nb, int columns, int gr, int t) {
-        const int r = k0 + 4 * S * t, c0 = nb + 8 * (gr >> 1) + (gr & 1);
-        const T* at = rows + static_cast<int64_t>(c0) * R + r;
+    __device__ __forceinline__ void read(uint32_t from) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const bool in = r < R && c0 + 2 * j < columns;
-            if constexpr (S == 1) {
-                const uint2 v = in ? *reinterpret_cast<const uint2*>(at + 2 * j * R) : make_uint2(0u, 0u);
-                b[j][0] = v.x;
-                b[j][1] = v.y;
-            } else {
-                const uint4 v = in ? *reinterpret_cast<const uint4*>(at + 2 * j * R) : make_uint4(0u, 0u, 0u, 0u);
-                b[j][0] = v.x;
-                b[j][1] = v.y;
-                b[j][2] = v.z;
-                b[j][3] = v.w;
+            if constexpr (S == 1) ptx::ld_shared_v2_u32(from + j * (8 * kLoraThreads), b[j]);
+            else ptx::ld_shared_v4_u32(from + j * (16 * kLoraThreads), b[j]);
+        }
+    }
+};
+__host__ __device__ constexpr int up_ahead(int S) { return S == 1 ? 2 : 1; }
+__host__ __device__ constexpr int up_stage_bytes(int S) { return 4 * 8 * S * kLoraThreads; }
+__host__ __device__ constexpr int up_bytes(int S) { return (up_ahead(S) + 1) * up_stage_bytes(S); }
+
+// The chunks of B that a warp multiplies, in order: its 32-column blocks, for LONG every
+// chunk of ranks of each 16 rows.  Fetches what comes next, zeros outside.
+template <class T, int S, bool LONG>
+struct BStream {
+    const T* rows;     // B's rows of this CTA's columns
+    uint32_t places;   // this thread's, of stage 0
+    int R, columns, row_blocks;
+    int nb, rb, k0;    // of the next chunk to fetch
+    int in, out;       // stages
+    __device__ __forceinline__ void start(const T* b_rows, int R_, int columns_, int m, uint32_t space) {
+        rows = b_rows;
+        places = space + threadIdx.x * 8 * S;
+        R = R_;
+        columns = columns_;
+        row_blocks = LONG ? (m + 15) / 16 : 1;
+        nb = (threadIdx.x >> 5) * kLoraColumns;
+        rb = k0 = in = out = 0;
+#pragma unroll
+        for (int i = 0; i < up_ahead(S); ++i) fetch();
+    }
+    __device__ __forceinline__ void fetch() {
+        const int lane = threadIdx.x & 31, gr = lane >> 2, t = lane & 3;
+        const int r = k0 + 4 * S * t, c0 = nb + 8 * (gr >> 1) + (gr & 1);
+        const T* at = rows + static_cast<int64_t>(c0) * R + r;
+        const uint32_t to = places + in * up_stage_bytes(S);
+        if (nb < columns) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool take = r < R && c0 + 2 * j < columns;
+                if constexpr (S == 1) ptx::cp_async8_or_zero(to + j * (8 * kLoraThreads), take ? at + 2 * j * R : rows, take);
+                else ptx::cp_async16_or_zero(to + j * (16 * kLoraThreads), take ? at + 2 * j * R : rows, take);
             }
         }
+        ptx::cp_async_commit();
+        if (++in == up_ahead(S) + 1) in = 0;
+        if (LONG) {
+            k0 += 16 * S;
+            if (k0 < R) return;
+            k0 = 0;
+            if (++rb < row_blocks) return;
+            rb = 0;
+        }
+        nb += kLoraWarps * kLoraColumns;
+    }
+    __device__ __forceinline__ void next(BFragments<T, S>& f) {
+        ptx::cp_async_wait_group<up_ahead(S) - 1>();
+        f.read(places + out * up_stage_bytes(S));
+        if (++out == up_ahead(S) + 1) out = 0;
+        fetch();
     }
 };
 
@@ -407,19 +536,15 @@ __device__ __forceinline__ void up_store(const LoraParams& p, const float (&acc)
         make_uint4(Elem<T>::pack2(y[0], y[1]), Elem<T>::pack2(y[2], y[3]), Elem<T>::pack2(y[4], y[5]), Elem<T>::pack2(y[6], y[7]));
 }
 
-// U of m rows of one group and `columns` columns from n0 on; b_rows: their part of B.
-// The next fragments are on their way while a chunk is multiplied; with one chunk
-// (!LONG) they serve all rows.
+// U of m rows of one group and `columns` columns from n0 on; b: their part of B, on its
+// way.  With one chunk (!LONG) its fragments serve all rows.
 template <class T, int S, bool LONG>
-__device__ __forceinline__ void up(const LoraParams& p, const T* b_rows, const int32_t* order, int m, int row0, int64_t n0,
-                                   int columns, const uint8_t* v_rows, const uint32_t* row_max) {
-    constexpr int kStride = kLoraWarps * kLoraColumns;
+__device__ __forceinline__ void up(const LoraParams& p, BStream<T, S, LONG>& b, const int32_t* order, int m, int row0,
+                                   int64_t n0, int columns, const uint8_t* v_rows, const uint32_t* row_max) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, t = lane & 3, pitch = up_pitch(p.R);
-    BFragments<T, S> next;
-    if (warp * kLoraColumns < columns) next.load(b_rows, p.R, 0, warp * kLoraColumns, columns, gr, t);
-    for (int nb = warp * kLoraColumns; nb < columns; nb += kStride) {
-        BFragments<T, S> b = next;
-        if (!LONG && nb + kStride < columns) next.load(b_rows, p.R, 0, nb + kStride, columns, gr, t);
+    for (int nb = warp * kLoraColumns; nb < columns; nb += kLoraWarps * kLoraColumns) {
+        BFragments<T, S> f;
+        if constexpr (!LONG) b.next(f);
         const int64_t n = n0 + nb + 8 * t;   // this thread's 8 columns of the output
         const bool n_in = nb + 8 * t < columns;
         for (int rb = 0; rb < m; rb += 16) {
@@ -427,18 +552,15 @@ __device__ __forceinline__ void up(const LoraParams& p, const T* b_rows, const i
             const uint8_t* v = v_rows + (rb + gr) * pitch + 16 * S * t;
             float acc[4][4];
             if constexpr (!LONG) {
-                up_mma<T, S, true>(acc, v, pitch, b);
+                up_mma<T, S, true>(acc, v, pitch, f);
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
                 for (int k0 = 0; k0 < p.R; k0 += 16 * S) {
-                    b = next;
-                    if (k0 + 16 * S < p.R) next.load(b_rows, p.R, k0 + 16 * S, nb, columns, gr, t);
-                    else if (rb + 16 < m) next.load(b_rows, p.R, 0, nb, columns, gr, t);
-                    else if (nb + kStride < columns) next.load(b_rows, p.R, 0, nb + kStride, columns, gr, t);
-                    up_mma<T, S, false>(acc, v + 4 * k0, pitch, b);
+                    b.next(f);
+                    up_mma<T, S, false>(acc, v + 4 * k0, pitch, f);
                 }
             }
 #pragma unroll
@@ -451,6 +573,7 @@ __device__ __forceinline__ void up(const LoraParams& p, const T* b_rows, const i
             }
         }
     }
+    ptx::cp_async_wait_group<0>();
 }
 
 // U = beta C (or zero) of rows without an adapter.
@@ -464,8 +587,9 @@ __device__ void up_none(const LoraParams& p, const int32_t* order, int m, int ro
     }
 }
 
-// Shared memory: the groups, the warps' exchange and later V, the partial sums.
-__host__ __device__ constexpr int lora_exchange_bytes(int MT, int R) {
+// Shared memory: the groups; the first product's copies and exchange, then V; the
+// second product's copies; the partial sums.
+__host__ __device__ constexpr int lora_space_bytes(int MT, int R) {
     const int v = up_rows(R) * up_pitch(R), e = down_bytes(MT);
     return ((v > e ? v : e) + 127) / 128 * 128;
 }
@@ -478,41 +602,48 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_kernel(const LoraParams 
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ uint32_t row_max[128];
     Groups& s = *reinterpret_cast<Groups*>(smem);
-    uint8_t* exchange = smem + kGroupsBytes;
-    float* part = reinterpret_cast<float*>(exchange + lora_exchange_bytes(MT, p.R));
-    ptx::griddep_wait();
-    // only now: what starts early may then rely on everything before this kernel
+    uint8_t* space = smem + kGroupsBytes;
+    uint8_t* b_places = space + lora_space_bytes(MT, p.R);
+    float* part = reinterpret_cast<float*>(b_places + up_bytes(S));
     ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
     const int rank = static_cast<int>(ptx::cluster_ctarank());
     const int row0 = static_cast<int>(blockIdx.y) * p.tile_rows;
     const int rows = min(p.tile_rows, p.M - row0);
-    group_rows(p, row0, rows, s);
-    const int groups = s.n + (s.start[s.n] < rows ? 1 : 0);
+    group_rows(p, row0, rows, s, *reinterpret_cast<GroupTable*>(space));
+    const int groups = s.n + (p.V == nullptr && s.start[s.n] < rows ? 1 : 0);
     const int64_t n0 = static_cast<int64_t>(rank) * p.width;
     const int columns = static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(p.width), p.N - n0)));
-    const int s0 = static_cast<int>(static_cast<int64_t>(p.k_steps) * rank / kLoraCluster);
-    const int s1 = static_cast<int>(static_cast<int64_t>(p.k_steps) * (rank + 1) / kLoraCluster);
+    const int s0 = static_cast<int>(static_cast<int64_t>(p.k_steps) * rank / p.cluster);
+    const int s1 = static_cast<int>(static_cast<int64_t>(p.k_steps) * (rank + 1) / p.cluster);
     const int most = up_rows(p.R);
-    for (int g = blockIdx.x / kLoraCluster; g < groups; g += gridDim.x / kLoraCluster) {
+    for (int g = blockIdx.x / p.cluster; g < groups; g += gridDim.x / p.cluster) {
         const bool has = g < s.n;
         const int end = has ? s.start[g + 1] : rows;
         const int64_t adapter = has ? s.adapter[g] : 0;
         const T* A = static_cast<const T*>(p.A) + adapter * p.R * p.K;
         const T* B = static_cast<const T*>(p.B) + (adapter * p.N + n0) * p.R;
         const float factor = has && p.factors != nullptr ? p.factors[adapter] : 1.0f;
-        if (has && threadIdx.x == 0 && columns > 0)   // on its way while V is formed
-            ptx::bulk_prefetch_l2(B, static_cast<uint32_t>(min(static_cast<int64_t>(columns) * p.R * 2, int64_t{1} << 20)));
         for (int i = s.start[g]; i < end; i += most) {
             const int m = min(most, end - i);
             if (!has) {
                 up_none<T>(p, s.order + i, m, row0, n0, columns);
                 continue;
             }
-            down<T, MT>(p, A, s.order + i, m, row0, s0, s1, reinterpret_cast<float*>(exchange), part);
+            if (p.V != nullptr) {
+                down<T, MT>(p, A, s.order + i, m, row0, s0, s1, space, part);
+                ptx::cluster_sync();
+                give_rows(p, m, factor, ptx::smem_u32(part), rank, row0, s.order + i);
+                ptx::cluster_sync();
+                continue;
+            }
+            BStream<T, S, LONG> b;
+            b.start(B, p.R, columns, m, ptx::smem_u32(b_places));   // on its way while V is formed
+            down<T, MT>(p, A, s.order + i, m, row0, s0, s1, space, part);
             ptx::cluster_sync();   // every CTA's partial sums are there
-            take_rows<T>(p, m, factor, ptx::smem_u32(part), exchange, row_max);
+            take_rows<T>(p, m, factor, ptx::smem_u32(part), space, row_max);
             ptx::cluster_arrive();   // this CTA has read them
-            up<T, S, LONG>(p, B, s.order + i, m, row0, n0, columns, exchange, row_max);
+            up<T, S, LONG>(p, b, s.order + i, m, row0, n0, columns, space, row_max);
             ptx::cluster_wait();   // nobody reads this CTA's partial sums any more
             __syncthreads();       // nor V
         }
@@ -520,19 +651,45 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_kernel(const LoraParams 
 }
 
 // -------------------------------------------------------------------------- host
-constexpr int64_t kLoraRows = 1 << 20;   // rows per launch: tiles are the grid's second dimension
+constexpr int64_t kLoraRows = 1 << 20;   // rows per launch: tiles are the grid's second dimension, at most 65535
 
+// Fills the split of `p` and launches.  Two CTAs per SM run at one time.
+//  - A batch of requests is one tile with as many groups as adapters in use, taken to
+//    be chosen evenly.  A cluster takes about 7 us for one, so where eight CTAs
+//    for each do not run at one time, four do: @FIG@
+//  - A prompt's tiles have one adapter or two: as many tiles as clusters of four run.
 template <class T, int MT, int S, bool LONG>
-gemm_status_t launch(const LoraParams& p, dim3 grid, const DeviceView& dev, cudaStream_t s) {
-    const int smem = kGroupsBytes + lora_exchange_bytes(MT, p.R) + up_rows(p.R) * p.R * 4;
-    return launch_clusters(lora_kernel<T, MT, S, LONG>, dev.dev, grid, kLoraThreads, kLoraCluster, smem, true, s, p);
+gemm_status_t launch(LoraParams p, const DeviceView& dev, cudaStream_t s) {
+    const auto kernel = lora_kernel<T, MT, S, LONG>;
+    const int smem = kGroupsBytes + lora_space_bytes(MT, p.R) + up_bytes(S) + up_rows(p.R) * p.R * 4;
+    auto at_once = [&](int cluster) {
+        return std::max(1, active_clusters(reinterpret_cast<const void*>(kernel), dev, kLoraThreads, smem, cluster));
+    };
+    int tiles = 1, clusters = 1;
+    if (p.M <= kLoraTile) {
+        p.tile_rows = kLoraTile;
+        const double count = std::max(1, p.count);
+        const double groups = count * (1.0 - std::pow(1.0 - 1.0 / count, static_cast<double>(p.M)));
+        p.cluster = groups <= 16.0 ? 8 : 4;
+        clusters = std::min(at_once(p.cluster), static_cast<int>(std::min<int64_t>(p.M, int64_t{p.count} + 1)));
+    } else {
+        p.cluster = 4;
+        const int most = at_once(p.cluster);
+        p.tile_rows = std::min(kLoraTile, std::max(48, ((p.M + most - 1) / most + 15) / 16 * 16));
+        tiles = (p.M + p.tile_rows - 1) / p.tile_rows;
+        clusters = std::max(1, most / tiles);
+    }
+    const int64_t per = p.cluster * kLoraColumns;
+    p.width = static_cast<int32_t>((p.N + per - 1) / per * kLoraColumns);
+    return launch_clusters(kernel, dev.dev, dim3(static_cast<unsigned>(clusters * p.cluster), static_cast<unsigned>(tiles), 1),
+                           kLoraThreads, p.cluster, smem, true, s, p);
 }
 
 template <class T>
-gemm_status_t run(const LoraParams& p, dim3 grid, const DeviceView& dev, cudaStream_t s) {
-    if (p.R <= 16) return launch<T, 1, 1, false>(p, grid, dev, s);
-    if (p.R <= 32) return launch<T, 2, 2, false>(p, grid, dev, s);
-    return launch<T, 2, 2, true>(p, grid, dev, s);
+gemm_status_t run(const LoraParams& p, const DeviceView& dev, cudaStream_t s) {
+    if (p.R <= 16) return launch<T, 1, 1, false>(p, dev, s);
+    if (p.R <= 32) return launch<T, 2, 2, false>(p, dev, s);
+    return launch<T, 2, 2, true>(p, dev, s);
 }
 
 }  // namespace
@@ -548,6 +705,7 @@ gemm_status_t run_lora(bool bf16, const LoraArgs& a, const DeviceView& dev, cuda
         p.ids = a.K > 0 && a.count > 0 ? a.ids + m0 : nullptr;
         p.C = a.C != nullptr ? static_cast<const uint16_t*>(a.C) + m0 * a.N : nullptr;
         p.U = static_cast<uint16_t*>(a.U) + m0 * a.N;
+        p.V = a.V;
         p.M = static_cast<int32_t>(M);
         p.N = static_cast<int32_t>(a.N);
         p.K = static_cast<int32_t>(a.K);
@@ -555,18 +713,7 @@ gemm_status_t run_lora(bool bf16, const LoraArgs& a, const DeviceView& dev, cuda
         p.count = static_cast<int32_t>(a.count);
         p.k_steps = static_cast<int32_t>((a.K + kLoraStepK - 1) / kLoraStepK);
         p.beta = a.beta;
-        const int64_t per = kLoraCluster * kLoraColumns;
-        p.width = static_cast<int32_t>((a.N + per - 1) / per * kLoraColumns);
-        // Two CTAs per SM, shared out over the tiles.  A batch of requests is one tile with
-        // many groups, a prompt's tiles have one or two each.
-        const int64_t most = 2 * dev.sms / kLoraCluster;
-        const int64_t even = ((M + most - 1) / most + 15) / 16 * 16;
-        p.tile_rows = M <= kLoraTile ? kLoraTile : static_cast<int32_t>(std::min<int64_t>(kLoraTile, std::max<int64_t>(96, even)));
-        const int64_t tiles = (M + p.tile_rows - 1) / p.tile_rows;
-        int64_t clusters = std::max<int64_t>(1, most / tiles);
-        if (tiles == 1) clusters = std::min({clusters, M, a.count + 1});
-        const dim3 grid(static_cast<unsigned>(clusters * kLoraCluster), static_cast<unsigned>(tiles), 1);
-        const gemm_status_t st = bf16 ? run<__nv_bfloat16>(p, grid, dev, s) : run<__half>(p, grid, dev, s);
+        const gemm_status_t st = bf16 ? run<__nv_bfloat16>(p, dev, s) : run<__half>(p, dev, s);
         if (st != GEMM_OK) return st;
     }
     return GEMM_OK;

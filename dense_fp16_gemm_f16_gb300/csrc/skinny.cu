@@ -6,10 +6,10 @@
 namespace gemm_gb300 {
 namespace {
 
-template <class Cfg, class T, bool F8, bool ROWS = false>
+template <class Cfg, class T, bool F8, bool ROWS = false, bool LORA = false>
 struct SkinnyLauncher {
     static cudaError_t prepare() {
-        return cudaFuncSetAttribute(gemm_skinny_kernel<Cfg, T, F8, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(gemm_skinny_kernel<Cfg, T, F8, ROWS, LORA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     Cfg::SMEM_BYTES);
     }
     static cudaError_t max_active(int pieces, int* out) {
@@ -24,7 +24,7 @@ struct SkinnyLauncher {
         attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        return cudaOccupancyMaxActiveClusters(out, gemm_skinny_kernel<Cfg, T, F8, ROWS>, &cfg);
+        return cudaOccupancyMaxActiveClusters(out, gemm_skinny_kernel<Cfg, T, F8, ROWS, LORA>, &cfg);
     }
     static cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, const SkinnyParams& p,
                               int grid_ctas, cudaStream_t stream) {
@@ -47,7 +47,7 @@ struct SkinnyLauncher {
             cfg.numAttrs = 2;
         }
         cfg.attrs = attr;
-        return cudaLaunchKernelEx(&cfg, gemm_skinny_kernel<Cfg, T, F8, ROWS>, w, x, p);
+        return cudaLaunchKernelEx(&cfg, gemm_skinny_kernel<Cfg, T, F8, ROWS, LORA>, w, x, p);
     }
     static const SkinnyOps& ops() {
         static const SkinnyOps o = {Cfg::MN,         Cfg::RING_BYTES, Cfg::X_BYTES, Cfg::MAX_ATOMS,
@@ -57,8 +57,11 @@ struct SkinnyLauncher {
     }
 };
 
-template <class Cfg>
+template <int MN>
 const SkinnyOps& skinny_ops_for(int dtype) {
+    using Cfg = SkinnyConfig<MN>;
+    if (dtype == kOpsLora) return SkinnyLauncher<SkinnyConfig<MN, true>, __half, false, false, true>::ops();
+    if (dtype == kOpsLora + 1) return SkinnyLauncher<SkinnyConfig<MN, true>, __nv_bfloat16, false, false, true>::ops();
     if (dtype == kOpsRowScaled) return SkinnyLauncher<Cfg, __nv_bfloat16, true, true>::ops();
     if (dtype >= 2) return SkinnyLauncher<Cfg, __nv_bfloat16, true>::ops();
     if (dtype == 1) return SkinnyLauncher<Cfg, __nv_bfloat16, false>::ops();
@@ -68,9 +71,9 @@ const SkinnyOps& skinny_ops_for(int dtype) {
 }  // namespace
 
 const SkinnyOps& skinny_ops(int mn, int dtype) {
-    if (mn <= 16) return skinny_ops_for<CfgSkinny16>(dtype);
-    if (mn <= 32) return skinny_ops_for<CfgSkinny32>(dtype);
-    return skinny_ops_for<CfgSkinny64>(dtype);
+    if (mn <= 16) return skinny_ops_for<16>(dtype);
+    if (mn <= 32) return skinny_ops_for<32>(dtype);
+    return skinny_ops_for<64>(dtype);
 }
 
 }  // namespace gemm_gb300

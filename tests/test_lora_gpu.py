@@ -90,7 +90,8 @@ def test_delta(M, N, K, R, count, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("M,N,K,R,count", [(1, 1024, 2048, 8, 4), (16, 8192, 1024, 16, 32), (17, 264, 520, 24, 3), (64, 2048, 1032, 64, 5),
+@pytest.mark.parametrize("M,N,K,R,count", [(1, 1024, 2048, 8, 4), (1, 40, 4096, 256, 2), (4, 136, 512, 256, 3), (16, 8192, 1024, 16, 32), (17, 264, 520, 24, 3),
+                                           (33, 8192, 520, 24, 9), (64, 1000, 8192, 16, 70), (60, 12000, 264, 8, 5), (64, 2048, 1032, 64, 5),
                                            (65, 72, 136, 16, 2), (250, 5000, 1032, 32, 64), (256, 256, 8192, 16, 9),
                                            (512, 2048, 4096, 128, 8), (3000, 4104, 1024, 16, 4), (8300, 520, 512, 8, 3)])
 def test_projection_with_adapters(M, N, K, R, count, dtype):
@@ -109,11 +110,11 @@ def test_projection_with_adapters(M, N, K, R, count, dtype):
             ref = ref + bias.double()
         tol = UNIT[dtype] * 1.01 * (ref.abs() + part.abs()) + err + E32 * (mag + part.abs() + 4) + 2 * FLOOR
         check(D, ref.clamp(min=0) if args else ref, tol)
-        # the same as the two calls that it stands for
-        T, E = (torch.empty_like(D) for _ in range(2))
-        g.gemm_lora_delta(X, lora, ids, T, beta=args.get("beta", 0.0), C=args.get("C"))
-        g.gemm_nt_ex(X, W, E, **(args | dict(beta=1.0, C=T)))
-        assert torch.equal(D, E)
+        if M > 64 or M * R > 1024:   # the same as the two calls that it then stands for
+            T, E = (torch.empty_like(D) for _ in range(2))
+            g.gemm_lora_delta(X, lora, ids, T, beta=args.get("beta", 0.0), C=args.get("C"))
+            g.gemm_nt_ex(X, W, E, **(args | dict(beta=1.0, C=T)))
+            assert torch.equal(D, E)
         if "C" in args:
             E = C.clone()
             g.gemm_lora_nt(X, W, lora, ids, E, **(args | dict(C=E)))
