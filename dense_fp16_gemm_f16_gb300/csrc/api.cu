@@ -550,9 +550,8 @@ gemm_status_t get_device(DeviceState** out, int* dev_out) {
         }
         const TiledOps* tiled[3] = {&tiled_ops_2cta256(0), &tiled_ops_1cta128(0), &tiled_ops_1cta256(0)};
         // fp16, bf16, 8-bit (one kernel for both formats), 8-bit with row scales
-        for (int mn : {16, 32, 64})
-            for (int dt : {0, 1})
-                if (skinny_ops(mn, kOpsLora + dt).prepare() != cudaSuccess) { cudaGetLastError(); return GEMM_ERR_CUDA; }
+        for (int dt : {0, 1})
+            if (skinny_ops(kLoraEpiRows, kOpsLora + dt).prepare() != cudaSuccess) { cudaGetLastError(); return GEMM_ERR_CUDA; }
         for (int dt : {0, 1, 2, kOpsRowScaled}) {
             const TiledOps* all[4] = {&tiled_ops_2cta256(dt), &tiled_ops_1cta128(dt), &tiled_ops_1cta256(dt),
                                       &tiled_ops_2cta512(dt)};

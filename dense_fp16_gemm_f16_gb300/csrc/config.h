@@ -277,7 +277,8 @@ struct SkinnyConfig {
     // partials received from the cluster: [P][128 columns][MN / P rows] fp32 = MN * 128 fp32
     static constexpr int RECV_BYTES = MN * 128 * 4;
     // with adapters: what they add to a range ([MN rows][128 columns] fp32), V and the ids
-    static constexpr int LORA_BYTES = LORA ? MN * 128 * 4 + kLoraEpiFloats * 4 + 64 * 4 : 0;
+    static constexpr int LORA_BYTES = LORA ? MN * 128 * 4 + kLoraEpiFloats * 4 + MN * 4 : 0;
+    static constexpr int BESIDE_BYTES = LORA ? kLoraBesideBytes : 0;
     static constexpr int NUM_BARS = 2 * MAX_STAGES + 5;
     // Each of the two accumulator buffers is ACCS MN-column accumulators
     // (MMA k of a K block adds into accumulator k % ACCS).
@@ -286,12 +287,13 @@ struct SkinnyConfig {
     static constexpr int ACC_COLS = ACCS * MN;
     static constexpr int TMEM_COLS = (2 * ACC_COLS < 32) ? 32 : 2 * ACC_COLS;
     // ring = [stages B slots][stages A slots], split at run time (ring_stages)
-    static constexpr int RING_BYTES = (kMaxDynSmem - 1024 - RECV_BYTES - LORA_BYTES - NUM_BARS * 8 - 16) / 1024 * 1024;
+    static constexpr int RING_BYTES = (kMaxDynSmem - 1024 - RECV_BYTES - LORA_BYTES - BESIDE_BYTES - NUM_BARS * 8 - 16) / 1024 * 1024;
     static constexpr int OFF_RECV = RING_BYTES;
     static constexpr int OFF_BAR = OFF_RECV + RECV_BYTES;
     static constexpr int OFF_SLOT = OFF_BAR + NUM_BARS * 8;
     static constexpr int OFF_LORA = OFF_SLOT + 16;
     static constexpr int SMEM_BYTES = OFF_LORA + LORA_BYTES + 1024;
+    static_assert(!LORA || MN == kLoraEpiRows, "one size");
     static_assert(!LORA || OFF_LORA % 8 == 0, "V is read as 8-byte words");
     static_assert(X_BYTES % 1024 == 0, "activation tile must stay 1024-aligned");
     static_assert(TMEM_COLS <= 512, "TMEM has 512 columns");

@@ -46,10 +46,13 @@ struct LoraEpi {
     const int32_t* ids;   // [M]
     int32_t R, count;     // R % 8 == 0
 };
-// M * R of one launch at most.  The part is summed on the epilogue's warps while the K loop
-// runs, a row and 8 ranks per load of a thread, 8 loads under way: about 1 us for
-// 64 of M * R, which the loop hides up to here.
-constexpr int kLoraEpiFloats = 1024;
+// Rows, and M * R, of one launch at most.  The part is summed on the epilogue's warps
+// while the K loop runs, a row and 8 ranks per load of a thread, 8 loads under way: about
+// 1 us for 64 of M * R, which the loop hides up to here.
+constexpr int kLoraEpiRows = 16, kLoraEpiFloats = 1024;
+// Shared memory that this kernel leaves for a CTA of the one that makes V, so that its K
+// loop runs beside it: only the epilogue waits for V.
+constexpr int kLoraBesideBytes = 26 * 1024;
 
 template <class T>
 struct Elem;
@@ -208,8 +211,15 @@ __device__ __forceinline__ float epi_apply1(const EpiParams& e, float x, int64_t
     return x;
 }
 
+// The C value of one element, 0 where C is not read.  Several are fetched before the
+// first output is written: the compiler keeps a load behind a store that may overlap it.
+template <class T>
+__device__ __forceinline__ float epi_c1(const EpiParams& e, int64_t row, int64_t col, int64_t N) {
+    return e.C != nullptr && e.beta != 0.0f ? Elem<T>::to_float(static_cast<const T*>(e.C)[row * N + col]) : 0.0f;
+}
+
 // The per-column part of the transform for one output column n (alpha *
-// s[n] and the bias), fetched ahead of use; apply() is epi_apply1 with them.
+// s[n] and the bias), fetched ahead of use; apply() is epi_apply1 with them and a C value.
 template <class T>
 struct EpiColumnFactors {
     float a = 1.0f;   // alpha * s[n]
@@ -218,9 +228,10 @@ struct EpiColumnFactors {
         a = e.scale_n != nullptr ? e.alpha * e.scale_n[n] : e.alpha;
         b = e.bias != nullptr ? Elem<T>::to_float(static_cast<const T*>(e.bias)[n]) : 0.0f;
     }
-    __device__ __forceinline__ float apply(const EpiParams& e, float x, int64_t row, int64_t col, int64_t N) const {
+    // c: the C value
+    __device__ __forceinline__ float apply(const EpiParams& e, float x, float c) const {
         x *= a;
-        if (e.C != nullptr && e.beta != 0.0f) x += e.beta * Elem<T>::to_float(static_cast<const T*>(e.C)[row * N + col]);
+        if (e.C != nullptr && e.beta != 0.0f) x += e.beta * c;
         if (e.bias != nullptr) x += b;
         if (e.act == 1) x = x < 0.0f ? 0.0f : x;
         return x;

@@ -77,11 +77,12 @@ __device__ __forceinline__ void skinny_lora_load(const LoraEpi& l, int M, int ti
     ptx::named_bar_sync(1, 32 * kEpiWarps);
 }
 
-// out[i * 128] = what the adapters add to column n of rows m0 + i, i < rows: 8 rows at
-// a time, so that 8 loads are under way.  fp32 throughout.
+// out[i * 128] = what the adapters, and beta C, add to column n of rows m0 + i, i < rows: 8
+// rows at a time, so that 8 loads are under way.  fp32 throughout.
 template <class T>
-__device__ __forceinline__ void skinny_lora_column(const LoraEpi& l, int64_t N, int64_t n, bool in, int m0, int rows,
-                                                   const float* V, const int32_t* ids, float* out) {
+__device__ __forceinline__ void skinny_lora_column(const LoraEpi& l, const EpiParams& e, int64_t N, int64_t n, bool in, int m0,
+                                                   int rows, const float* V, const int32_t* ids, float* out) {
+    const bool add = in && e.C != nullptr && e.beta != 0.0f;
     for (int i0 = 0; i0 < rows; i0 += 8) {
         float sum[8];
         const uint4* at[8];
@@ -90,13 +91,13 @@ __device__ __forceinline__ void skinny_lora_column(const LoraEpi& l, int64_t N, 
         for (int i = 0; i < 8; ++i) {
             const int m = m0 + (i0 + i < rows ? i0 + i : i0);
             const int id = ids[m];
-            sum[i] = 0.0f;
+            sum[i] = add ? e.beta * Elem<T>::to_float(static_cast<const T*>(e.C)[m * N + n]) : 0.0f;
             v[i] = V + m * l.R;
             at[i] = in && id >= 0 && i0 + i < rows
                         ? reinterpret_cast<const uint4*>(static_cast<const T*>(l.B) + (id * N + n) * l.R)
                         : nullptr;
         }
-#pragma unroll 2
+#pragma unroll 1
         for (int r = 0; r < l.R; r += 8) {
             uint4 b[8];
 #pragma unroll
@@ -114,7 +115,7 @@ __device__ __forceinline__ void skinny_lora_column(const LoraEpi& l, int64_t N, 
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i0 + i < rows) out[(i0 + i) * 128] = at[i] != nullptr ? sum[i] : 0.0f;
+            if (i0 + i < rows) out[(i0 + i) * 128] = sum[i];
     }
 }
 
@@ -197,7 +198,9 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     // of an SM's shared memory, so a CTA of this grid never shares an SM, or
     // its TMEM, with one of the last.)
     ptx::griddep_launch_dependents();
-    ptx::griddep_wait();
+    // With adapters, the kernel before this one makes V and lets this one start only when
+    // all before it has ended: A and B may be read, and the epilogue waits.
+    if constexpr (!LORA) ptx::griddep_wait();
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -294,6 +297,11 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
             for (int i = 0; i < (MN + 31) / 32; ++i)
                 row_scale[i] = 32 * i + lane < p.M ? p.epi.scale_m[32 * i + lane] : 0.0f;
         }
+        EpiParams epi = p.epi;
+        if constexpr (LORA) {
+            ptx::griddep_wait();
+            epi.C = nullptr;   // added with the adapters' part
+        }
         // this thread's column of what the adapters add, and what it is made of
         float* lora_out = reinterpret_cast<float*>(smem + Cfg::OFF_LORA) + n_local;
         float* lora_v = reinterpret_cast<float*>(smem + Cfg::OFF_LORA + MN * 128 * 4);
@@ -309,10 +317,10 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                 const bool col_in = n_local < p.width && n < p.N;
                 // this column's C values, factor and bias, fetched while the K loop runs
                 EpiColumn<T, MN> ec;
-                if ((p.epi.on || LORA) && col_in) ec.load(p.epi, n, p.M, p.N);
+                if ((p.epi.on || LORA) && col_in) ec.load(epi, n, p.M, p.N);
                 float scale_n = 1.0f;
                 if constexpr (LORA) {
-                    skinny_lora_column<T>(p.lora, p.N, n, col_in, 0, p.M, lora_v, lora_ids, lora_out);
+                    skinny_lora_column<T>(p.lora, p.epi, p.N, n, col_in, 0, p.M, lora_v, lora_ids, lora_out);
                     if (col_in) scale_n = ec.a;
                     ec.a = 1.0f;   // applied before the adapters' part is added
                 }
@@ -335,7 +343,7 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                         for (int m = 0; m < MN; ++m)
                             if (m < p.M)
                                 D[m * static_cast<int64_t>(p.N) + n] =
-                                    Elem<T>::from_float(ec.apply(p.epi, __uint_as_float(v[m]), m));
+                                    Elem<T>::from_float(ec.apply(epi, __uint_as_float(v[m]), m));
                     } else {
 #pragma unroll
                         for (int m = 0; m < MN; ++m)
@@ -351,12 +359,23 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
             const bool col_in = r < p.ranges && n_local < p.width && n < p.N;
             // this column's factor alpha * s[n] and bias, fetched while the K loop runs
             EpiColumnFactors<T> cf;
-            if (p.epi.on && col_in) cf.load(p.epi, n);
+            if (p.epi.on && col_in) cf.load(epi, n);
+            // and its C values of the rows that this CTA finishes, two to a register: loads behind the
+            // exchange would wait for one another's outputs, which may lie over C
+            // (32 rows of 8192 x 8192 with C: @C32@)
+            uint32_t c16[MN / 4] = {};
+            if (epi.on && col_in && epi.C != nullptr && epi.beta != 0.0f) {
+                const int rows = min(MN / P, p.M - j * (MN / P));
+                const uint16_t* C = static_cast<const uint16_t*>(epi.C) + static_cast<int64_t>(j * (MN / P)) * p.N + n;
+#pragma unroll
+                for (int m = 0; m < MN / 2; ++m)
+                    if (m < rows) c16[m / 2] |= static_cast<uint32_t>(C[static_cast<int64_t>(m) * p.N]) << (16 * (m & 1));
+            }
             float scale_n = 1.0f;
             if constexpr (LORA) {
                 // the rows that this CTA finishes
                 const int MS = MN / P, left = p.M - j * MS;
-                skinny_lora_column<T>(p.lora, p.N, n, col_in, j * MS, left < MS ? left : MS, lora_v, lora_ids, lora_out);
+                skinny_lora_column<T>(p.lora, p.epi, p.N, n, col_in, j * MS, left < MS ? left : MS, lora_v, lora_ids, lora_out);
                 scale_n = cf.a;
                 cf.a = 1.0f;   // applied before the adapters' part is added
             }
@@ -405,12 +424,15 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                     const int m = j * MS + ml;
                     if (m < p.M) {
                         if constexpr (LORA) acc = acc * scale_n + lora_out[ml * 128];
-                        const float x = p.epi.on ? cf.apply(p.epi, acc, m, n, p.N) : acc;
+                        const float c = (ml & 1) ? Elem<T>::hi(c16[ml / 2]) : Elem<T>::lo(c16[ml / 2]);
+                        const float x = p.epi.on ? cf.apply(epi, acc, c) : acc;
                         D[m * static_cast<int64_t>(p.N) + n] = Elem<T>::from_float(x);
                     }
                 };
                 if (MS >= 4) {
-                    for (int c = 0; c < MS; c += 4) {
+#pragma unroll
+                    for (int c = 0; c < MN / 2; c += 4) {
+                        if (c >= MS) break;
                         float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                         for (int i = 0; i < P; ++i) {
                             float t[4];

@@ -48,7 +48,8 @@ struct StreamKOps {
 // with a bf16 output, kOpsRowScaled = the latter with a scale per row of A (no
 // stream-K kernel: AUTO does not pick it)
 constexpr int kOpsRowScaled = 4;
-// the small-M kernels of 16-bit operands with adapters in the epilogue: kOpsLora + 0 or 1
+// the small-M kernels of 16-bit operands with adapters in the epilogue (up to
+// kLoraEpiRows rows): kOpsLora + 0 or 1
 constexpr int kOpsLora = 8;
 const TiledOps& tiled_ops_2cta256(int dtype);
 const TiledOps& tiled_ops_2cta512(int dtype);   // two consumers per CTA

@@ -77,7 +77,7 @@ struct LoraArgs {
     const void* C;         // nullptr: none
     float beta;
     void* U;               // may be C
-    float* V;              // [M][R], M <= 64: c_a X A_aT is all that is wanted; else nullptr
+    float* V;              // [M][R], M <= kLoraEpiRows: c_a X A_aT is all that is wanted; else nullptr
     int64_t M, N, K, R, count;
 };
 constexpr int kLoraMaxRank = 256;

@@ -413,7 +413,7 @@ gemm_status_t lora_nt(int dtype, const void* X, const gemm_weights_t* weights, c
         return w.scales != nullptr ? run_w4_gemm(dtype == GEMM_DTYPE_BF16, X, w, D, M, N, K, plain, dev, stream)
                                    : run_dense(dtype, X, w.data, D, M, N, K, epilogue, nullptr, stream);
     }
-    if (w.scales == nullptr && M <= 64 && M * a.R <= kLoraEpiFloats) {
+    if (w.scales == nullptr && M <= kLoraEpiRows && M * a.R <= kLoraEpiFloats) {
         // few rows: X Aᵀ by itself, its product with B on the idle warps of the projection's kernel
         Scratch ws;
         st = get_scratch(dev.dev, stream, static_cast<size_t>(M * a.R * 4), &ws);

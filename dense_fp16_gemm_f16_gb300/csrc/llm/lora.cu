@@ -84,41 +84,6 @@ __device__ __forceinline__ int rows_before(const uint8_t (&rows)[kLoraWarps], in
 // share an SM with one that read older ids there.
 __device__ void group_rows(const LoraParams& p, int row0, int rows, Groups& s, GroupTable& table) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (rows <= 32) {   // one warp: no table
-        if (warp == 0) {
-            int id = -2;
-            if (lane < rows) {
-                id = p.ids != nullptr ? __ldcg(p.ids + row0 + lane) : -1;
-                if (id < 0 || id >= p.count) id = -1;
-            }
-            const uint32_t mine = __match_any_sync(0xffffffffu, id), before = (1u << lane) - 1u;
-            const int lead = __ffs(mine) - 1;
-            const uint32_t leads = __ballot_sync(0xffffffffu, id >= 0 && lead == lane);
-            const uint32_t none = __ballot_sync(0xffffffffu, id == -1);
-            const int number = __popc(leads & ((1u << lead) - 1u));
-            // rows of the groups whose first row comes earlier
-            int start = 0;
-            for (uint32_t l = leads; l != 0; l &= l - 1) {
-                const int at = __ffs(l) - 1, size = __popc(__shfl_sync(0xffffffffu, mine, at));
-                start += at < lead ? size : 0;
-            }
-            if (id >= 0) {
-                s.order[start + __popc(mine & before)] = lane;
-                if (lead == lane) {
-                    s.adapter[number] = id;
-                    s.start[number] = start;
-                }
-            } else if (id == -1) {
-                s.order[rows - __popc(none) + __popc(none & before)] = lane;
-            }
-            if (lane == 0) {
-                s.n = __popc(leads);
-                s.start[s.n] = rows - __popc(none);
-            }
-        }
-        __syncthreads();
-        return;
-    }
     int id = -2;   // no row
     if (tid < rows) {
         id = p.ids != nullptr ? __ldcg(p.ids + row0 + tid) : -1;
@@ -198,28 +163,86 @@ __device__ void group_rows(const LoraParams& p, int row0, int rows, Groups& s, G
     __syncthreads();
 }
 
+// The same for up to 32 rows: one warp does it, without a table.
+__device__ void group_few_rows(const LoraParams& p, int row0, int rows, Groups& s) {
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x < 32) {
+        int id = -2;
+        if (lane < rows) {
+            id = p.ids != nullptr ? __ldcg(p.ids + row0 + lane) : -1;
+            if (id < 0 || id >= p.count) id = -1;
+        }
+        const uint32_t mine = __match_any_sync(0xffffffffu, id), before = (1u << lane) - 1u;
+        const int lead = __ffs(mine) - 1;
+        const uint32_t leads = __ballot_sync(0xffffffffu, id >= 0 && lead == lane);
+        const uint32_t none = __ballot_sync(0xffffffffu, id == -1);
+        const int number = __popc(leads & ((1u << lead) - 1u));
+        // rows of the groups whose first row comes earlier
+        int start = 0;
+        for (uint32_t l = leads; l != 0; l &= l - 1) {
+            const int at = __ffs(l) - 1, size = __popc(__shfl_sync(0xffffffffu, mine, at));
+            start += at < lead ? size : 0;
+        }
+        if (id >= 0) {
+            s.order[start + __popc(mine & before)] = lane;
+            if (lead == lane) {
+                s.adapter[number] = id;
+                s.start[number] = start;
+            }
+        } else if (id == -1) {
+            s.order[rows - __popc(none) + __popc(none & before)] = lane;
+        }
+        if (lane == 0) {
+            s.n = __popc(leads);
+            s.start[s.n] = rows - __popc(none);
+        }
+    }
+    __syncthreads();
+}
+
 // -------------------------------------------------------------------------- down
 // Every thread copies the pieces of its own fragments to places of its own in shared
 // memory (cp.async), some steps ahead, and reads them back: many bytes under way without
 // registers for them, and nobody to wait for.
-__host__ __device__ constexpr int down_slots(int MT) { return MT == 1 ? 18 : 16; }   // 16-byte places per thread
+// How a launch is built.  MT: 16-row tiles of ranks of the first product in hand; SLOTS:
+// 16-byte places per thread for its copies; S: steps of 16 ranks per chunk of the second
+// product, LONG: R has more than one chunk; AHEAD: chunks under way.  SLOTS and AHEAD leave
+// room for two CTAs per SM up to 32 ranks; with more, a CTA has enough to
+// copy to be alone (61 rows, 48 adapters of 64 x (4096 + 8192): @LONG@).
+struct Ranks16 {
+    static constexpr int MT = 1, SLOTS = 18, WARPS = kLoraWarps, S = 1, AHEAD = 2;
+    static constexpr bool LONG = false;
+};
+struct Ranks32 {
+    static constexpr int MT = 2, SLOTS = 16, WARPS = kLoraWarps, S = 2, AHEAD = 1;
+    static constexpr bool LONG = false;
+};
+struct RanksMore {
+    static constexpr int MT = 2, SLOTS = 24, WARPS = kLoraWarps, S = 2, AHEAD = 3;
+    static constexpr bool LONG = true;
+};
+struct RanksOnlyV {   // V alone, by fewer warps with little memory
+    static constexpr int MT = 1, SLOTS = 8, WARPS = 4;
+};
+
 // Floats between the sums of two rows in the warps' exchange, which takes the same
 // space: the two columns of a fragment fall into different banks.
 __host__ __device__ constexpr int down_pitch(int MT) { return 16 * MT + 4; }
-__host__ __device__ constexpr int down_bytes(int MT) { return down_slots(MT) * 16 * kLoraThreads; }
-static_assert(kLoraWarps * 32 * down_pitch(1) * 4 <= down_bytes(1) && kLoraWarps * 32 * down_pitch(2) * 4 <= down_bytes(2),
-              "the exchange fits the places");
+template <class Sh>
+constexpr int kDownBytes = Sh::SLOTS * 16 * 32 * Sh::WARPS;
 
 // part = V of m <= 8 NT WR rows (`rows`) and 16 MT ranks from r0 on over the k steps
-// [s0, s1): WR parts of 8 NT rows, the steps of each dealt out to 8 / WR warps.
-template <class T, int MT, int NT, int WR>
+// [s0, s1): WR parts of 8 NT rows, the steps of each dealt out to WARPS / WR warps.
+template <class T, class Sh, int NT, int WR>
 __device__ __forceinline__ void down_rows(const LoraParams& p, const T* A, int r0, const int32_t* rows, int m, int row0,
                                           int s0, int s1, uint8_t* space, float* part) {
-    constexpr int KW = kLoraWarps / WR, NF = 2 * MT + NT, D = down_slots(MT) / NF, P = down_pitch(MT);
+    constexpr int MT = Sh::MT, W = Sh::WARPS, KW = W / WR, NF = 2 * MT + NT, D = Sh::SLOTS / NF, P = down_pitch(MT);
+    constexpr int PLACE = 16 * 32 * W;
     static_assert(D >= 2, "a step ahead at least");
+    static_assert(W * 8 * NT * P * 4 <= kDownBytes<Sh>, "the exchange fits the places");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int first = warp / KW * 8 * NT;   // this warp's rows
-    const uint32_t places = ptx::smem_u32(space) + threadIdx.x * 16;   // f of stage d: (d * NF + f) * 4096 behind
+    const uint32_t places = ptx::smem_u32(space) + threadIdx.x * 16;   // f of stage d: (d * NF + f) * PLACE behind
     const T* a_ptr = A + static_cast<int64_t>(r0 + g) * p.K + 8 * t;
     const T* x_ptr[NT];
 #pragma unroll
@@ -231,16 +254,16 @@ __device__ __forceinline__ void down_rows(const LoraParams& p, const T* A, int r
     auto fetch = [&](int s, int d) {
         const int64_t k = static_cast<int64_t>(s) * kLoraStepK;
         const bool in = s < s1 && k + 8 * t < p.K;   // K % 8 == 0: all eight or none
-        const uint32_t to = places + d * (NF * 16 * kLoraThreads);
+        const uint32_t to = places + d * (NF * PLACE);
 #pragma unroll
         for (int i = 0; i < 2 * MT; ++i) {
             const bool take = in && r0 + 8 * i + g < p.R;
-            ptx::cp_async16_or_zero(to + i * (16 * kLoraThreads), take ? a_ptr + static_cast<int64_t>(8 * i) * p.K + k : A, take);
+            ptx::cp_async16_or_zero(to + i * PLACE, take ? a_ptr + static_cast<int64_t>(8 * i) * p.K + k : A, take);
         }
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             const bool take = in && x_ptr[j] != nullptr;
-            ptx::cp_async16_or_zero(to + (2 * MT + j) * (16 * kLoraThreads), take ? x_ptr[j] + k : A, take);
+            ptx::cp_async16_or_zero(to + (2 * MT + j) * PLACE, take ? x_ptr[j] + k : A, take);
         }
     };
     float acc[MT][NT][4];
@@ -261,11 +284,11 @@ __device__ __forceinline__ void down_rows(const LoraParams& p, const T* A, int r
         for (; s < s1; s += KW) {
             ptx::cp_async_wait_group<D - 2>();   // this step's copies, by this thread, are done
             uint32_t a[2 * MT][4], x[NT][4];
-            const uint32_t from = places + d * (NF * 16 * kLoraThreads);
+            const uint32_t from = places + d * (NF * PLACE);
 #pragma unroll
-            for (int i = 0; i < 2 * MT; ++i) ptx::ld_shared_v4_u32(from + i * (16 * kLoraThreads), a[i]);
+            for (int i = 0; i < 2 * MT; ++i) ptx::ld_shared_v4_u32(from + i * PLACE, a[i]);
 #pragma unroll
-            for (int j = 0; j < NT; ++j) ptx::ld_shared_v4_u32(from + (2 * MT + j) * (16 * kLoraThreads), x[j]);
+            for (int j = 0; j < NT; ++j) ptx::ld_shared_v4_u32(from + (2 * MT + j) * PLACE, x[j]);
             const int back = d == 0 ? D - 1 : d - 1;   // the stage read in the step before
             fetch(s + (D - 1) * KW, back);
             ptx::cp_async_commit();
@@ -294,7 +317,7 @@ __device__ __forceinline__ void down_rows(const LoraParams& p, const T* A, int r
 #pragma unroll
             for (int e = 0; e < 4; ++e) mine[(8 * j + 2 * t + (e & 1)) * P + 16 * i + g + 8 * (e >> 1)] = acc[i][j][e];
     __syncthreads();
-    for (int i = threadIdx.x; i < m * 16 * MT; i += kLoraThreads) {
+    for (int i = threadIdx.x; i < m * 16 * MT; i += 32 * W) {
         const int n = i / (16 * MT), r = i % (16 * MT);
         if (r0 + r >= p.R) continue;
         const float* from = red + (n / (8 * NT) * KW * 8 * NT + n % (8 * NT)) * P + r;
@@ -306,15 +329,15 @@ __device__ __forceinline__ void down_rows(const LoraParams& p, const T* A, int r
     __syncthreads();
 }
 
-template <class T, int MT>
+template <class T, class Sh>
 __device__ __forceinline__ void down(const LoraParams& p, const T* A, const int32_t* rows, int m, int row0, int s0, int s1,
                                      uint8_t* space, float* part) {
-    for (int r0 = 0; r0 < p.R; r0 += 16 * MT) {
-        if (m <= 8) down_rows<T, MT, 1, 1>(p, A, r0, rows, m, row0, s0, s1, space, part);
-        else if (m <= 16) down_rows<T, MT, 2, 1>(p, A, r0, rows, m, row0, s0, s1, space, part);
-        else if (m <= 32) down_rows<T, MT, 4, 1>(p, A, r0, rows, m, row0, s0, s1, space, part);
-        else if (m <= 64) down_rows<T, MT, 4, 2>(p, A, r0, rows, m, row0, s0, s1, space, part);
-        else down_rows<T, MT, 4, 4>(p, A, r0, rows, m, row0, s0, s1, space, part);
+    for (int r0 = 0; r0 < p.R; r0 += 16 * Sh::MT) {
+        if (m <= 8) down_rows<T, Sh, 1, 1>(p, A, r0, rows, m, row0, s0, s1, space, part);
+        else if (m <= 16) down_rows<T, Sh, 2, 1>(p, A, r0, rows, m, row0, s0, s1, space, part);
+        else if (m <= 32) down_rows<T, Sh, 4, 1>(p, A, r0, rows, m, row0, s0, s1, space, part);
+        else if (m <= 64) down_rows<T, Sh, 4, 2>(p, A, r0, rows, m, row0, s0, s1, space, part);
+        else down_rows<T, Sh, 4, 4>(p, A, r0, rows, m, row0, s0, s1, space, part);
     }
 }
 
@@ -405,7 +428,7 @@ __device__ __forceinline__ void take_rows(const LoraParams& p, int m, float fact
 __device__ __forceinline__ void give_rows(const LoraParams& p, int m, float factor, uint32_t part, int rank, int row0,
                                           const int32_t* order) {
     const int quads = p.R / 4;
-    for (int i = rank * kLoraThreads + threadIdx.x; i < m * quads; i += p.cluster * kLoraThreads) {
+    for (int i = rank * blockDim.x + threadIdx.x; i < m * quads; i += p.cluster * blockDim.x) {
         const int r = i / quads, q = i - r * quads;
         float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -424,7 +447,7 @@ __device__ __forceinline__ void give_rows(const LoraParams& p, int m, float fact
 // Fragments of B for 32 columns and one chunk of ranks (S steps of 16).  Column c of
 // MMA tile j is column 8 (c / 2) + 2 j + c % 2 of the 32, so that a thread's two of every tile are
 // eight in a row of the output; rank 4 S t + 4 k + e of the chunk is thread t's e-th of step k.
-// As in the first product, every thread copies its own to places of its own, up_ahead(S) chunks ahead.
+// As in the first product, every thread copies its own to places of its own, AHEAD chunks ahead.
 template <class T, int S>
 struct BFragments {
     uint32_t b[4][2 * S];
@@ -436,14 +459,16 @@ struct BFragments {
         }
     }
 };
-__host__ __device__ constexpr int up_ahead(int S) { return S == 1 ? 2 : 1; }
 __host__ __device__ constexpr int up_stage_bytes(int S) { return 4 * 8 * S * kLoraThreads; }
-__host__ __device__ constexpr int up_bytes(int S) { return (up_ahead(S) + 1) * up_stage_bytes(S); }
+template <class Sh>
+constexpr int kUpBytes = (Sh::AHEAD + 1) * up_stage_bytes(Sh::S);
 
 // The chunks of B that a warp multiplies, in order: its 32-column blocks, for LONG every
 // chunk of ranks of each 16 rows.  Fetches what comes next, zeros outside.
-template <class T, int S, bool LONG>
+template <class T, class Sh>
 struct BStream {
+    static constexpr int S = Sh::S, AHEAD = Sh::AHEAD;
+    static constexpr bool LONG = Sh::LONG;
     const T* rows;     // B's rows of this CTA's columns
     uint32_t places;   // this thread's, of stage 0
     int R, columns, row_blocks;
@@ -458,7 +483,7 @@ struct BStream {
         nb = (threadIdx.x >> 5) * kLoraColumns;
         rb = k0 = in = out = 0;
 #pragma unroll
-        for (int i = 0; i < up_ahead(S); ++i) fetch();
+        for (int i = 0; i < AHEAD; ++i) fetch();
     }
     __device__ __forceinline__ void fetch() {
         const int lane = threadIdx.x & 31, gr = lane >> 2, t = lane & 3;
@@ -474,7 +499,7 @@ struct BStream {
             }
         }
         ptx::cp_async_commit();
-        if (++in == up_ahead(S) + 1) in = 0;
+        if (++in == AHEAD + 1) in = 0;
         if (LONG) {
             k0 += 16 * S;
             if (k0 < R) return;
@@ -485,9 +510,9 @@ struct BStream {
         nb += kLoraWarps * kLoraColumns;
     }
     __device__ __forceinline__ void next(BFragments<T, S>& f) {
-        ptx::cp_async_wait_group<up_ahead(S) - 1>();
+        ptx::cp_async_wait_group<AHEAD - 1>();
         f.read(places + out * up_stage_bytes(S));
-        if (++out == up_ahead(S) + 1) out = 0;
+        if (++out == AHEAD + 1) out = 0;
         fetch();
     }
 };
@@ -538,9 +563,11 @@ __device__ __forceinline__ void up_store(const LoraParams& p, const float (&acc)
 
 // U of m rows of one group and `columns` columns from n0 on; b: their part of B, on its
 // way.  With one chunk (!LONG) its fragments serve all rows.
-template <class T, int S, bool LONG>
-__device__ __forceinline__ void up(const LoraParams& p, BStream<T, S, LONG>& b, const int32_t* order, int m, int row0,
+template <class T, class Sh>
+__device__ __forceinline__ void up(const LoraParams& p, BStream<T, Sh>& b, const int32_t* order, int m, int row0,
                                    int64_t n0, int columns, const uint8_t* v_rows, const uint32_t* row_max) {
+    constexpr int S = Sh::S;
+    constexpr bool LONG = Sh::LONG;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, t = lane & 3, pitch = up_pitch(p.R);
     for (int nb = warp * kLoraColumns; nb < columns; nb += kLoraWarps * kLoraColumns) {
         BFragments<T, S> f;
@@ -589,29 +616,30 @@ __device__ void up_none(const LoraParams& p, const int32_t* order, int m, int ro
 
 // Shared memory: the groups; the first product's copies and exchange, then V; the
 // second product's copies; the partial sums.
-__host__ __device__ constexpr int lora_space_bytes(int MT, int R) {
-    const int v = up_rows(R) * up_pitch(R), e = down_bytes(MT);
+template <class Sh>
+__host__ __device__ constexpr int lora_space_bytes(int R) {
+    const int v = up_rows(R) * up_pitch(R), e = kDownBytes<Sh>;
     return ((v > e ? v : e) + 127) / 128 * 128;
 }
 
 // Grid: clusters that share a tile, tiles; a cluster takes groups in turn, the last
-// of which is the rows without an adapter.  MT: 16-row tiles of ranks of the first
-// product in hand; S: steps of 16 ranks per chunk, LONG: R has more than one chunk.
-template <class T, int MT, int S, bool LONG>
-__global__ void __launch_bounds__(kLoraThreads, 2) lora_kernel(const LoraParams p) {
+// of which is the rows without an adapter.
+template <class T, class Sh>
+__global__ void __launch_bounds__(kLoraThreads, Sh::LONG ? 1 : 2) lora_kernel(const LoraParams p) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ uint32_t row_max[128];
     Groups& s = *reinterpret_cast<Groups*>(smem);
     uint8_t* space = smem + kGroupsBytes;
-    uint8_t* b_places = space + lora_space_bytes(MT, p.R);
-    float* part = reinterpret_cast<float*>(b_places + up_bytes(S));
-    ptx::griddep_launch_dependents();
+    uint8_t* b_places = space + lora_space_bytes<Sh>(p.R);
+    float* part = reinterpret_cast<float*>(b_places + kUpBytes<Sh>);
     ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
     const int rank = static_cast<int>(ptx::cluster_ctarank());
     const int row0 = static_cast<int>(blockIdx.y) * p.tile_rows;
     const int rows = min(p.tile_rows, p.M - row0);
-    group_rows(p, row0, rows, s, *reinterpret_cast<GroupTable*>(space));
-    const int groups = s.n + (p.V == nullptr && s.start[s.n] < rows ? 1 : 0);
+    if (rows <= 32) group_few_rows(p, row0, rows, s);
+    else group_rows(p, row0, rows, s, *reinterpret_cast<GroupTable*>(space));
+    const int groups = s.n + (s.start[s.n] < rows ? 1 : 0);
     const int64_t n0 = static_cast<int64_t>(rank) * p.width;
     const int columns = static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(p.width), p.N - n0)));
     const int s0 = static_cast<int>(static_cast<int64_t>(p.k_steps) * rank / p.cluster);
@@ -630,51 +658,97 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_kernel(const LoraParams 
                 up_none<T>(p, s.order + i, m, row0, n0, columns);
                 continue;
             }
-            if (p.V != nullptr) {
-                down<T, MT>(p, A, s.order + i, m, row0, s0, s1, space, part);
-                ptx::cluster_sync();
-                give_rows(p, m, factor, ptx::smem_u32(part), rank, row0, s.order + i);
-                ptx::cluster_sync();
-                continue;
-            }
-            BStream<T, S, LONG> b;
+            BStream<T, Sh> b;
             b.start(B, p.R, columns, m, ptx::smem_u32(b_places));   // on its way while V is formed
-            down<T, MT>(p, A, s.order + i, m, row0, s0, s1, space, part);
+            down<T, Sh>(p, A, s.order + i, m, row0, s0, s1, space, part);
             ptx::cluster_sync();   // every CTA's partial sums are there
             take_rows<T>(p, m, factor, ptx::smem_u32(part), space, row_max);
             ptx::cluster_arrive();   // this CTA has read them
-            up<T, S, LONG>(p, b, s.order + i, m, row0, n0, columns, space, row_max);
+            up<T, Sh>(p, b, s.order + i, m, row0, n0, columns, space, row_max);
             ptx::cluster_wait();   // nobody reads this CTA's partial sums any more
             __syncthreads();       // nor V
         }
     }
 }
 
+// V alone, of up to 16 rows with M R <= kLoraEpiFloats, for the product of a few rows.  That
+// runs beside this kernel and hides it, so it takes little of an SM rather than little time.
+constexpr int kLoraOnlyThreads = 32 * RanksOnlyV::WARPS;
+constexpr int kLoraOnlyBytes = kGroupsBytes + kDownBytes<RanksOnlyV> + kLoraEpiFloats * 4;
+static_assert(kLoraOnlyBytes + 2048 <= kLoraBesideBytes, "fits beside the product, with what either CTA has reserved");
+
+template <class T>
+__global__ void __launch_bounds__(kLoraOnlyThreads) lora_v_kernel(const LoraParams p) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    Groups& s = *reinterpret_cast<Groups*>(smem);
+    uint8_t* space = smem + kGroupsBytes;
+    float* part = reinterpret_cast<float*>(space + kDownBytes<RanksOnlyV>);
+    ptx::griddep_wait();
+    // only now: the product that starts early relies on everything before this kernel
+    ptx::griddep_launch_dependents();
+    const int rank = static_cast<int>(ptx::cluster_ctarank());
+    group_few_rows(p, 0, p.M, s);
+    const int s0 = static_cast<int>(static_cast<int64_t>(p.k_steps) * rank / p.cluster);
+    const int s1 = static_cast<int>(static_cast<int64_t>(p.k_steps) * (rank + 1) / p.cluster);
+    for (int g = blockIdx.x / p.cluster; g < s.n; g += gridDim.x / p.cluster) {
+        const int64_t adapter = s.adapter[g];
+        const float factor = p.factors != nullptr ? p.factors[adapter] : 1.0f;
+        const int m = s.start[g + 1] - s.start[g];
+        const int32_t* order = s.order + s.start[g];
+        const T* A = static_cast<const T*>(p.A) + adapter * p.R * p.K;
+        for (int r0 = 0; r0 < p.R; r0 += 16) {
+            if (m <= 8) down_rows<T, RanksOnlyV, 1, 1>(p, A, r0, order, m, 0, s0, s1, space, part);
+            else down_rows<T, RanksOnlyV, 2, 1>(p, A, r0, order, m, 0, s0, s1, space, part);
+        }
+        ptx::cluster_sync();   // every CTA's partial sums are there
+        give_rows(p, m, factor, ptx::smem_u32(part), rank, 0, order);
+        ptx::cluster_sync();   // and have been read
+    }
+}
+
 // -------------------------------------------------------------------------- host
 constexpr int64_t kLoraRows = 1 << 20;   // rows per launch: tiles are the grid's second dimension, at most 65535
 
-// Fills the split of `p` and launches.  Two CTAs per SM run at one time.
+// Sets a kernel's preference for shared memory over L1, once per kernel and device.
+bool keep_smem(const void* kernel, int dev) {
+    static std::mutex mu;
+    static std::map<LaunchKey, bool> done;
+    std::lock_guard<std::mutex> lock(mu);
+    bool& ready = done[LaunchKey{kernel, dev, 0, 0}];
+    if (!ready) {
+        ready = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) ==
+                cudaSuccess;
+        if (!ready) cudaGetLastError();
+    }
+    return ready;
+}
+
+// Fills the split of `p` and launches.
 //  - A batch of requests is one tile with as many groups as adapters in use, taken to
-//    be chosen evenly.  A cluster takes about 7 us for one, so where eight CTAs
-//    for each do not run at one time, four do: @FIG@
-//  - A prompt's tiles have one adapter or two: as many tiles as clusters of four run.
-template <class T, int MT, int S, bool LONG>
+//    be chosen evenly.  While all clusters fit the GPU with one CTA per SM, they get one each
+//    (by asking for more than half of its shared memory): started while the kernel before
+//    drains, two would go to the SMs that are free first (@FIG@).
+//  - A prompt's tiles have one adapter or two: as many tiles as clusters of four run
+//    with two CTAs per SM.
+template <class T, class Sh>
 gemm_status_t launch(LoraParams p, const DeviceView& dev, cudaStream_t s) {
-    const auto kernel = lora_kernel<T, MT, S, LONG>;
-    const int smem = kGroupsBytes + lora_space_bytes(MT, p.R) + up_bytes(S) + up_rows(p.R) * p.R * 4;
-    auto at_once = [&](int cluster) {
-        return std::max(1, active_clusters(reinterpret_cast<const void*>(kernel), dev, kLoraThreads, smem, cluster));
+    const auto kernel = lora_kernel<T, Sh>;
+    int smem = kGroupsBytes + lora_space_bytes<Sh>(p.R) + kUpBytes<Sh> + up_rows(p.R) * p.R * 4;
+    auto at_once = [&](int cluster, int bytes) {
+        return std::max(1, active_clusters(reinterpret_cast<const void*>(kernel), dev, kLoraThreads, bytes, cluster));
     };
     int tiles = 1, clusters = 1;
     if (p.M <= kLoraTile) {
         p.tile_rows = kLoraTile;
         const double count = std::max(1, p.count);
-        const double groups = count * (1.0 - std::pow(1.0 - 1.0 / count, static_cast<double>(p.M)));
-        p.cluster = groups <= 16.0 ? 8 : 4;
-        clusters = std::min(at_once(p.cluster), static_cast<int>(std::min<int64_t>(p.M, int64_t{p.count} + 1)));
+        const double groups = std::max(1.0, count * (1.0 - std::pow(1.0 - 1.0 / count, static_cast<double>(p.M))));
+        const int alone = std::max(smem, kMaxDynamicSmem / 2 + 2048);
+        p.cluster = groups <= at_once(8, alone) ? 8 : 4;
+        if (groups <= at_once(p.cluster, alone)) smem = alone;
+        clusters = std::min(at_once(p.cluster, smem), static_cast<int>(std::min<int64_t>(p.M, int64_t{p.count} + 1)));
     } else {
         p.cluster = 4;
-        const int most = at_once(p.cluster);
+        const int most = at_once(p.cluster, smem);
         p.tile_rows = std::min(kLoraTile, std::max(48, ((p.M + most - 1) / most + 15) / 16 * 16));
         tiles = (p.M + p.tile_rows - 1) / p.tile_rows;
         clusters = std::max(1, most / tiles);
@@ -685,11 +759,24 @@ gemm_status_t launch(LoraParams p, const DeviceView& dev, cudaStream_t s) {
                            kLoraThreads, p.cluster, smem, true, s, p);
 }
 
+// Eight CTAs per adapter in use, on as many SMs as there are.  The SMs keep all of their
+// shared memory as such, or the product's CTAs would wait for them to change over.
+template <class T>
+gemm_status_t launch_v(LoraParams p, const DeviceView& dev, cudaStream_t s) {
+    const auto kernel = lora_v_kernel<T>;
+    if (!keep_smem(reinterpret_cast<const void*>(kernel), dev.dev)) return GEMM_ERR_CUDA;
+    p.cluster = 8;
+    const int clusters = std::min(std::max(1, dev.sms / p.cluster), std::min(p.M, p.count));
+    return launch_clusters(kernel, dev.dev, dim3(static_cast<unsigned>(clusters * p.cluster), 1, 1), kLoraOnlyThreads,
+                           p.cluster, kLoraOnlyBytes, true, s, p);
+}
+
 template <class T>
 gemm_status_t run(const LoraParams& p, const DeviceView& dev, cudaStream_t s) {
-    if (p.R <= 16) return launch<T, 1, 1, false>(p, dev, s);
-    if (p.R <= 32) return launch<T, 2, 2, false>(p, dev, s);
-    return launch<T, 2, 2, true>(p, dev, s);
+    if (p.V != nullptr) return launch_v<T>(p, dev, s);
+    if (p.R <= 16) return launch<T, Ranks16>(p, dev, s);
+    if (p.R <= 32) return launch<T, Ranks32>(p, dev, s);
+    return launch<T, RanksMore>(p, dev, s);
 }
 
 }  // namespace

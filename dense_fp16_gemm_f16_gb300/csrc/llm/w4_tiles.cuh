@@ -419,12 +419,15 @@ w4_tiles_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                 ptx::tmem_ld_x16(acc + static_cast<uint32_t>(c0), v);
                 ptx::tmem_wait_ld();
                 if (in) {
+                    float c[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) c[i] = m0 + c0 + i < p.M ? epi_c1<T>(p.epi, m0 + c0 + i, n, p.N) : 0.0f;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const int64_t m = m0 + c0 + i;
                         if (m < p.M) {
                             float x = __uint_as_float(v[i]);
-                            if (p.epi.on) x = cf.apply(p.epi, x, m, n, p.N);
+                            if (p.epi.on) x = cf.apply(p.epi, x, c[i]);
                             D[m * p.N + n] = Elem<T>::from_float(x);
                         }
                     }
@@ -456,7 +459,11 @@ w4_tiles_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
             const int c = e / kTileRows * 4, r = e % kTileRows;
             const int64_t m = m0 + j * per + c, n = n0 + r;
             if (n >= p.N) continue;
-            float x[4] = {};
+            float x[4] = {}, c4[4];
+            EpiColumnFactors<T> cf;
+            if (p.epi.on) cf.load(p.epi, n);
+#pragma unroll
+            for (int q2 = 0; q2 < 4; ++q2) c4[q2] = m + q2 < p.M ? epi_c1<T>(p.epi, m + q2, n, p.N) : 0.0f;
             for (int i = 0; i < S; ++i) {
                 float t[4];
                 const uint32_t at = base + static_cast<uint32_t>((((i * per + c) >> 2) * 128 + r) * 16);
@@ -467,7 +474,7 @@ w4_tiles_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
 #pragma unroll
             for (int q2 = 0; q2 < 4; ++q2) {
                 if (m + q2 < p.M) {
-                    if (p.epi.on) x[q2] = epi_apply1<T>(p.epi, x[q2], m + q2, n, p.N);
+                    if (p.epi.on) x[q2] = cf.apply(p.epi, x[q2], c4[q2]);
                     D[(m + q2) * p.N + n] = Elem<T>::from_float(x[q2]);
                 }
             }

@@ -60,8 +60,10 @@ struct SkinnyLauncher {
 template <int MN>
 const SkinnyOps& skinny_ops_for(int dtype) {
     using Cfg = SkinnyConfig<MN>;
-    if (dtype == kOpsLora) return SkinnyLauncher<SkinnyConfig<MN, true>, __half, false, false, true>::ops();
-    if (dtype == kOpsLora + 1) return SkinnyLauncher<SkinnyConfig<MN, true>, __nv_bfloat16, false, false, true>::ops();
+    if constexpr (MN == kLoraEpiRows) {
+        if (dtype == kOpsLora) return SkinnyLauncher<SkinnyConfig<MN, true>, __half, false, false, true>::ops();
+        if (dtype == kOpsLora + 1) return SkinnyLauncher<SkinnyConfig<MN, true>, __nv_bfloat16, false, false, true>::ops();
+    }
     if (dtype == kOpsRowScaled) return SkinnyLauncher<Cfg, __nv_bfloat16, true, true>::ops();
     if (dtype >= 2) return SkinnyLauncher<Cfg, __nv_bfloat16, true>::ops();
     if (dtype == 1) return SkinnyLauncher<Cfg, __nv_bfloat16, false>::ops();
