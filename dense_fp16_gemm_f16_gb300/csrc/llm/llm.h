@@ -81,7 +81,9 @@ struct LoraArgs {
     int64_t M, N, K, R, count;
 };
 constexpr int kLoraMaxRank = 256;
-gemm_status_t run_lora(bool bf16, const LoraArgs& a, const DeviceView& dev, cudaStream_t s);
+// bytes of scratch that run_lora needs at `data` (M: rows)
+size_t lora_scratch_bytes(int64_t M);
+gemm_status_t run_lora(bool bf16, const LoraArgs& a, uint8_t* data, const DeviceView& dev, cudaStream_t s);
 
 // bytes of scratch that run_route needs at `data`; counters: one zero, left at zero
 size_t route_scratch_bytes(int64_t T, int64_t E);

@@ -386,7 +386,11 @@ gemm_status_t lora_delta(int dtype, const void* X, const gemm_lora_t* l, const i
     DeviceView dev;
     st = device_view(&dev);
     if (st != GEMM_OK) return st;
-    return run_lora(dtype == GEMM_DTYPE_BF16, a, dev, reinterpret_cast<cudaStream_t>(stream));
+    Scratch ws;
+    const size_t bytes = lora_scratch_bytes(M);
+    if (bytes > 0) st = get_scratch(dev.dev, stream, bytes, &ws);
+    if (st != GEMM_OK) return st;
+    return run_lora(dtype == GEMM_DTYPE_BF16, a, ws.data, dev, reinterpret_cast<cudaStream_t>(stream));
 }
 
 gemm_status_t lora_nt(int dtype, const void* X, const gemm_weights_t* weights, const gemm_lora_t* l, const int32_t* ids,
@@ -419,7 +423,7 @@ gemm_status_t lora_nt(int dtype, const void* X, const gemm_weights_t* weights, c
         st = get_scratch(dev.dev, stream, static_cast<size_t>(M * a.R * 4), &ws);
         if (st != GEMM_OK) return st;
         a.V = reinterpret_cast<float*>(ws.data);
-        st = run_lora(dtype == GEMM_DTYPE_BF16, a, dev, reinterpret_cast<cudaStream_t>(stream));
+        st = run_lora(dtype == GEMM_DTYPE_BF16, a, nullptr, dev, reinterpret_cast<cudaStream_t>(stream));
         if (st != GEMM_OK) return st;
         const LoraEpi part{a.V, l->B, ids, static_cast<int32_t>(a.R), static_cast<int32_t>(a.count)};
         return run_dense(dtype, X, w.data, D, M, N, K, epilogue, &part, stream);
@@ -429,7 +433,11 @@ gemm_status_t lora_nt(int dtype, const void* X, const gemm_weights_t* weights, c
     a.U = D;
     epi.beta = 1.0f;
     epi.C = D;
-    st = run_lora(dtype == GEMM_DTYPE_BF16, a, dev, reinterpret_cast<cudaStream_t>(stream));
+    Scratch ws;
+    const size_t bytes = lora_scratch_bytes(M);
+    if (bytes > 0) st = get_scratch(dev.dev, stream, bytes, &ws);
+    if (st != GEMM_OK) return st;
+    st = run_lora(dtype == GEMM_DTYPE_BF16, a, ws.data, dev, reinterpret_cast<cudaStream_t>(stream));
     if (st != GEMM_OK) return st;
     return w.scales != nullptr ? run_w4_gemm(dtype == GEMM_DTYPE_BF16, X, w, D, M, N, K, epi_params(&epi), dev, stream)
                                : run_dense(dtype, X, w.data, D, M, N, K, &epi, nullptr, stream);

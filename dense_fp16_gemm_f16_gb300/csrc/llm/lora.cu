@@ -1,10 +1,9 @@
 // lora.cu -- low-rank adapters of many requests:
 //   U[m] = beta C[m] + c_a (X[m] A_aᵀ) B_aᵀ,  a = ids[m].
 //
-// One kernel.  Rows are taken in tiles of up to 256; a CTA puts the rows of a tile in
-// order of their adapters itself, so no list has to be made by a kernel before, and every
-// adapter's matrices are read once per tile.  A cluster of eight (or four) CTAs takes one
-// adapter's rows: each CTA forms V = X Aᵀ over an eighth of K, the partial sums meet in
+// Rows are put in order of their adapters: up to 256 by every CTA for itself, so that one
+// kernel does everything, more by a kernel before (lora_list_kernel), which also cuts an adapter's
+// rows into units.  A cluster of eight (or four) CTAs takes one adapter's rows, or one unit: each CTA forms V = X Aᵀ over an eighth of K, the partial sums meet in
 // distributed shared memory in a fixed order, and each CTA multiplies V by an
 // eighth of B's rows.
 // Each byte meets few others (R is small): the operands go straight from global
@@ -22,6 +21,7 @@
 #include <cmath>
 #include <type_traits>
 
+#include "config.h"
 #include "llm/llm.h"
 #include "llm/rows_host.cuh"
 #include "llm/stream.cuh"
@@ -31,7 +31,7 @@ namespace {
 
 constexpr int kLoraThreads = 256;
 constexpr int kLoraWarps = kLoraThreads / 32;
-constexpr int kLoraTile = 256;           // most rows per tile: one per thread
+constexpr int kLoraTile = 256;           // most rows that a CTA puts in order: one per thread
 constexpr int kLoraStepK = 32;           // k per warp and step of `down`: 16 bytes per thread and row
 constexpr int kLoraColumns = 32;         // columns per warp and step of `up`
 constexpr int kLoraMaxCluster = 8;
@@ -42,23 +42,38 @@ struct LoraParams {
     const void* B;           // [count][N][R]
     const float* factors;    // [count] or nullptr
     const int32_t* ids;      // [M], or nullptr: no row has an adapter
+    const struct LoraList* list;   // the rows in order, or nullptr: every CTA makes that itself
     const void* C;           // [M][N] or nullptr
     void* U;                 // [M][N]
     float* V;                // [M][R]: factors X Aᵀ is all that is wanted, or nullptr
     int32_t M, N, K, R, count;
-    int32_t tile_rows, k_steps, width;   // width: columns per CTA of a cluster
+    int32_t k_steps, width;  // width: columns per CTA of a cluster
+    int32_t unit_rows;       // with a list: most rows of a unit, 32, 64 or 128
     int32_t cluster;         // its CTAs
     float beta;
 };
 
-// The rows of one tile in order of their adapters.
+// Up to 256 rows in order of their adapters.
 struct Groups {
-    int32_t order[kLoraTile];         // rows of the tile, group by group, each in row order
+    int32_t order[kLoraTile];         // rows, group by group, each in row order
     int32_t start[kLoraTile + 1];     // group i is order[start[i]] .. order[start[i + 1] - 1]
     int32_t adapter[kLoraTile];       // of each group, in the order of their first rows
     int32_t n;                        // groups with an adapter; rows without one lie behind them
 };
 constexpr int kGroupsBytes = (sizeof(Groups) + 127) / 128 * 128;
+
+// The same for more rows, made by a kernel of its own: units of up to unit_rows rows of one
+// adapter, rows order[start] .. order[start + rows - 1].
+constexpr int kListRows = 8192;
+struct LoraUnit {
+    int32_t adapter, start, rows, unused;
+};
+struct LoraList {
+    int32_t n, with;     // units; rows that have an adapter, behind which the others lie
+    int32_t unused[2];
+    LoraUnit units[kListRows];
+    int32_t order[kListRows];
+};
 
 // The table that finds them.
 constexpr int kLoraSlots = 2 * kLoraTile;
@@ -82,11 +97,11 @@ __device__ __forceinline__ int rows_before(const uint8_t (&rows)[kLoraWarps], in
 // Called by the whole CTA, one row per thread.  Which slot an adapter gets depends on
 // timing, groups and their order do not.  Ids are read past L1: a kernel launched early may
 // share an SM with one that read older ids there.
-__device__ void group_rows(const LoraParams& p, int row0, int rows, Groups& s, GroupTable& table) {
+__device__ void group_rows(const LoraParams& p, int rows, Groups& s, GroupTable& table) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int id = -2;   // no row
     if (tid < rows) {
-        id = p.ids != nullptr ? __ldcg(p.ids + row0 + tid) : -1;
+        id = p.ids != nullptr ? __ldcg(p.ids + tid) : -1;
         if (id < 0 || id >= p.count) id = -1;
     }
 #pragma unroll
@@ -164,12 +179,12 @@ __device__ void group_rows(const LoraParams& p, int row0, int rows, Groups& s, G
 }
 
 // The same for up to 32 rows: one warp does it, without a table.
-__device__ void group_few_rows(const LoraParams& p, int row0, int rows, Groups& s) {
+__device__ void group_few_rows(const LoraParams& p, int rows, Groups& s) {
     const int lane = threadIdx.x & 31;
     if (threadIdx.x < 32) {
         int id = -2;
         if (lane < rows) {
-            id = p.ids != nullptr ? __ldcg(p.ids + row0 + lane) : -1;
+            id = p.ids != nullptr ? __ldcg(p.ids + lane) : -1;
             if (id < 0 || id >= p.count) id = -1;
         }
         const uint32_t mine = __match_any_sync(0xffffffffu, id), before = (1u << lane) - 1u;
@@ -198,6 +213,105 @@ __device__ void group_few_rows(const LoraParams& p, int row0, int rows, Groups& 
         }
     }
     __syncthreads();
+}
+
+// The list of up to kListRows rows, by one CTA: a table in shared memory counts the rows
+// of every adapter, the counts become places.  Which of an adapter's rows share a unit depends on
+// timing; the sums of a row do not depend on what shares its unit.  @LISTUS@
+constexpr int kListThreads = 1024;
+constexpr int kListEach = kListRows / kListThreads;
+// Slots of the table: a power of two, twice the rows at least, one per thread at least.
+int list_bits(int M) {
+    int bits = 10;
+    while ((1 << bits) < 2 * M) ++bits;
+    return bits;
+}
+
+__global__ void __launch_bounds__(kListThreads) lora_list_kernel(const LoraParams p, LoraList* list, int bits) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int slots = 1 << bits;
+    int32_t* key = reinterpret_cast<int32_t*>(smem);
+    int32_t* count = key + slots;   // the last is of rows without an adapter
+    __shared__ int2 totals[32];
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    for (int i = tid; i < slots; i += kListThreads) {
+        key[i] = -1;
+        count[i] = 0;
+    }
+    if (tid == 0) count[slots] = 0;
+    int id[kListEach], slot[kListEach], rank[kListEach];
+#pragma unroll
+    for (int i = 0; i < kListEach; ++i) {
+        const int row = i * kListThreads + tid;
+        id[i] = -2;   // no row
+        if (row < p.M) {
+            id[i] = p.ids != nullptr ? __ldcg(p.ids + row) : -1;
+            if (id[i] < 0 || id[i] >= p.count) id[i] = -1;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kListEach; ++i) {
+        if (i * kListThreads >= p.M) break;
+        const uint32_t mine = __match_any_sync(0xffffffffu, id[i]);
+        const int lead = __ffs(mine) - 1;
+        int at = slots, before = 0;
+        if (lane == lead && id[i] >= -1) {
+            if (id[i] >= 0) {
+                at = static_cast<int>((static_cast<uint32_t>(id[i]) * 2654435761u) >> (32 - bits));
+                while (true) {   // at most half of the slots are taken
+                    const int other = atomicCAS(&key[at], -1, id[i]);
+                    if (other == -1 || other == id[i]) break;
+                    at = (at + 1) & (slots - 1);
+                }
+            }
+            before = atomicAdd(&count[at], __popc(mine));
+        }
+        slot[i] = __shfl_sync(0xffffffffu, at, lead);
+        rank[i] = __shfl_sync(0xffffffffu, before, lead) + __popc(mine & ((1u << lane) - 1u));
+    }
+    __syncthreads();
+    // places: each thread sums up its slots, then all threads
+    int2 sum = make_int2(0, 0);   // rows, units
+    for (int i = tid; i < slots; i += kListThreads) {
+        const int c = count[i];
+        sum.x += c;
+        sum.y += (c + p.unit_rows - 1) / p.unit_rows;
+    }
+    int2 at = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, at.x, d), y = __shfl_up_sync(0xffffffffu, at.y, d);
+        if (lane >= d) {
+            at.x += x;
+            at.y += y;
+        }
+    }
+    if (lane == 31) totals[warp] = at;
+    __syncthreads();
+    at.x -= sum.x;
+    at.y -= sum.y;
+    for (int w = 0; w < warp; ++w) {
+        at.x += totals[w].x;
+        at.y += totals[w].y;
+    }
+    for (int i = tid; i < slots; i += kListThreads) {
+        const int c = count[i];
+        count[i] = at.x;   // where the adapter's rows begin
+        for (int r = 0; r < c; r += p.unit_rows) list->units[at.y++] = LoraUnit{key[i], at.x + r, min(p.unit_rows, c - r), 0};
+        at.x += c;
+    }
+    if (tid == kListThreads - 1) {
+        list->n = at.y;
+        list->with = at.x;
+        count[slots] = at.x;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kListEach; ++i)
+        if (id[i] >= -1) list->order[count[slot[i]] + rank[i]] = i * kListThreads + tid;
 }
 
 // -------------------------------------------------------------------------- down
@@ -233,10 +347,10 @@ constexpr int kDownBytes = Sh::SLOTS * 16 * 32 * Sh::WARPS;
 
 // part = V of m <= 8 NT WR rows (`rows`) and 16 MT ranks from r0 on over the k steps
 // [s0, s1): WR parts of 8 NT rows, the steps of each dealt out to WARPS / WR warps.
-template <class T, class Sh, int NT, int WR>
-__device__ __forceinline__ void down_rows(const LoraParams& p, const T* A, int r0, const int32_t* rows, int m, int row0,
-                                          int s0, int s1, uint8_t* space, float* part) {
-    constexpr int MT = Sh::MT, W = Sh::WARPS, KW = W / WR, NF = 2 * MT + NT, D = Sh::SLOTS / NF, P = down_pitch(MT);
+template <class T, class Sh, int MT, int NT, int WR>
+__device__ __forceinline__ void down_rows(const LoraParams& p, const T* A, int r0, const int32_t* rows, int m, int s0, int s1,
+                                          uint8_t* space, float* part) {
+    constexpr int W = Sh::WARPS, KW = W / WR, NF = 2 * MT + NT, D = Sh::SLOTS / NF, P = down_pitch(MT);
     constexpr int PLACE = 16 * 32 * W;
     static_assert(D >= 2, "a step ahead at least");
     static_assert(W * 8 * NT * P * 4 <= kDownBytes<Sh>, "the exchange fits the places");
@@ -248,7 +362,7 @@ __device__ __forceinline__ void down_rows(const LoraParams& p, const T* A, int r
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
         const bool in = first + 8 * j + g < m;
-        x_ptr[j] = in ? static_cast<const T*>(p.X) + static_cast<int64_t>(row0 + rows[first + 8 * j + g]) * p.K + 8 * t : nullptr;
+        x_ptr[j] = in ? static_cast<const T*>(p.X) + static_cast<int64_t>(rows[first + 8 * j + g]) * p.K + 8 * t : nullptr;
     }
     // copies of one step into stage d; what lies outside becomes zeros
     auto fetch = [&](int s, int d) {
@@ -329,15 +443,19 @@ __device__ __forceinline__ void down_rows(const LoraParams& p, const T* A, int r
     __syncthreads();
 }
 
+// `like`: how many rows decide how the warps share the work, and so the order of a row's
+// sums.  Many rows of a high rank take 64 ranks at a time, so that X is read for twice as many; few
+// rows 32, so that more steps are under way.
 template <class T, class Sh>
-__device__ __forceinline__ void down(const LoraParams& p, const T* A, const int32_t* rows, int m, int row0, int s0, int s1,
+__device__ __forceinline__ void down(const LoraParams& p, const T* A, const int32_t* rows, int m, int like, int s0, int s1,
                                      uint8_t* space, float* part) {
-    for (int r0 = 0; r0 < p.R; r0 += 16 * Sh::MT) {
-        if (m <= 8) down_rows<T, Sh, 1, 1>(p, A, r0, rows, m, row0, s0, s1, space, part);
-        else if (m <= 16) down_rows<T, Sh, 2, 1>(p, A, r0, rows, m, row0, s0, s1, space, part);
-        else if (m <= 32) down_rows<T, Sh, 4, 1>(p, A, r0, rows, m, row0, s0, s1, space, part);
-        else if (m <= 64) down_rows<T, Sh, 4, 2>(p, A, r0, rows, m, row0, s0, s1, space, part);
-        else down_rows<T, Sh, 4, 4>(p, A, r0, rows, m, row0, s0, s1, space, part);
+    constexpr int MT = Sh::MT, MM = Sh::LONG ? 2 * MT : MT;
+    for (int r0 = 0; r0 < p.R; r0 += 16 * (like <= 16 ? MT : MM)) {
+        if (like <= 8) down_rows<T, Sh, MT, 1, 1>(p, A, r0, rows, m, s0, s1, space, part);
+        else if (like <= 16) down_rows<T, Sh, MT, 2, 1>(p, A, r0, rows, m, s0, s1, space, part);
+        else if (like <= 32) down_rows<T, Sh, MM, 4, 1>(p, A, r0, rows, m, s0, s1, space, part);
+        else if (like <= 64) down_rows<T, Sh, MM, 4, 2>(p, A, r0, rows, m, s0, s1, space, part);
+        else down_rows<T, Sh, MM, 4, 4>(p, A, r0, rows, m, s0, s1, space, part);
     }
 }
 
@@ -353,7 +471,9 @@ __host__ __device__ constexpr int up_pitch(int R) {
     return up_ranks(R) * 4 + (((R <= 16 ? 64 : 16) - up_ranks(R) * 4) & 127);
 }
 // rows of V in shared memory at one time
-__host__ __device__ constexpr int up_rows(int R) { return R <= 16 ? 128 : (R <= 32 ? 64 : 32); }
+__host__ __device__ constexpr int up_rows(int R) {
+    return R <= 16 ? 128 : (R <= 32 ? 64 : (R <= 64 ? 128 : (R <= 128 ? 64 : 32)));
+}
 
 // The two numbers of type T that v is the sum of.
 template <class T>
@@ -425,8 +545,7 @@ __device__ __forceinline__ void take_rows(const LoraParams& p, int m, float fact
 }
 
 // The same rows, not cut, to V: every CTA of the cluster writes a part.
-__device__ __forceinline__ void give_rows(const LoraParams& p, int m, float factor, uint32_t part, int rank, int row0,
-                                          const int32_t* order) {
+__device__ __forceinline__ void give_rows(const LoraParams& p, int m, float factor, uint32_t part, int rank, const int32_t* order) {
     const int quads = p.R / 4;
     for (int i = rank * blockDim.x + threadIdx.x; i < m * quads; i += p.cluster * blockDim.x) {
         const int r = i / quads, q = i - r * quads;
@@ -439,7 +558,7 @@ __device__ __forceinline__ void give_rows(const LoraParams& p, int m, float fact
 #pragma unroll
             for (int e = 0; e < 4; ++e) a[e] += o[e];
         }
-        *reinterpret_cast<float4*>(p.V + static_cast<int64_t>(row0 + order[r]) * p.R + 4 * q) =
+        *reinterpret_cast<float4*>(p.V + static_cast<int64_t>(order[r]) * p.R + 4 * q) =
             make_float4(a[0] * factor, a[1] * factor, a[2] * factor, a[3] * factor);
     }
 }
@@ -463,8 +582,12 @@ __host__ __device__ constexpr int up_stage_bytes(int S) { return 4 * 8 * S * kLo
 template <class Sh>
 constexpr int kUpBytes = (Sh::AHEAD + 1) * up_stage_bytes(Sh::S);
 
+// Row blocks of 16 that share a chunk of B in hand.
+template <class Sh>
+constexpr int kRowBlocks = Sh::LONG ? 4 : 1;
+
 // The chunks of B that a warp multiplies, in order: its 32-column blocks, for LONG every
-// chunk of ranks of each 16 rows.  Fetches what comes next, zeros outside.
+// chunk of ranks for each kRowBlocks row blocks.  Fetches what comes next, zeros outside.
 template <class T, class Sh>
 struct BStream {
     static constexpr int S = Sh::S, AHEAD = Sh::AHEAD;
@@ -479,7 +602,7 @@ struct BStream {
         places = space + threadIdx.x * 8 * S;
         R = R_;
         columns = columns_;
-        row_blocks = LONG ? (m + 15) / 16 : 1;
+        row_blocks = LONG ? (m + 16 * kRowBlocks<Sh> - 1) / (16 * kRowBlocks<Sh>) : 1;
         nb = (threadIdx.x >> 5) * kLoraColumns;
         rb = k0 = in = out = 0;
 #pragma unroll
@@ -564,8 +687,8 @@ __device__ __forceinline__ void up_store(const LoraParams& p, const float (&acc)
 // U of m rows of one group and `columns` columns from n0 on; b: their part of B, on its
 // way.  With one chunk (!LONG) its fragments serve all rows.
 template <class T, class Sh>
-__device__ __forceinline__ void up(const LoraParams& p, BStream<T, Sh>& b, const int32_t* order, int m, int row0,
-                                   int64_t n0, int columns, const uint8_t* v_rows, const uint32_t* row_max) {
+__device__ __forceinline__ void up(const LoraParams& p, BStream<T, Sh>& b, const int32_t* order, int m, int64_t n0,
+                                   int columns, const uint8_t* v_rows, const uint32_t* row_max) {
     constexpr int S = Sh::S;
     constexpr bool LONG = Sh::LONG;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, t = lane & 3, pitch = up_pitch(p.R);
@@ -574,43 +697,56 @@ __device__ __forceinline__ void up(const LoraParams& p, BStream<T, Sh>& b, const
         if constexpr (!LONG) b.next(f);
         const int64_t n = n0 + nb + 8 * t;   // this thread's 8 columns of the output
         const bool n_in = nb + 8 * t < columns;
-        for (int rb = 0; rb < m; rb += 16) {
+        constexpr int RB = kRowBlocks<Sh>;
+        for (int r0 = 0; r0 < m; r0 += 16 * RB) {
             // rows beyond m read what lies there: only outputs that are not written come of it
-            const uint8_t* v = v_rows + (rb + gr) * pitch + 16 * S * t;
-            float acc[4][4];
+            const uint8_t* v = v_rows + (r0 + gr) * pitch + 16 * S * t;
+            float acc[RB][4][4];
             if constexpr (!LONG) {
-                up_mma<T, S, true>(acc, v, pitch, f);
+                up_mma<T, S, true>(acc[0], v, pitch, f);
             } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int q = 0; q < RB; ++q)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[q][j][e] = 0.0f;
                 for (int k0 = 0; k0 < p.R; k0 += 16 * S) {
                     b.next(f);
-                    up_mma<T, S, false>(acc, v + 4 * k0, pitch, f);
+#pragma unroll
+                    for (int q = 0; q < RB; ++q)
+                        if (r0 + 16 * q < m) up_mma<T, S, false>(acc[q], v + 4 * k0 + 16 * q * pitch, pitch, f);
                 }
             }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = rb + gr + 8 * h;
+            for (int q = 0; q < 2 * RB; ++q) {
+                const int r = r0 + gr + 8 * q;
                 if (r >= m || !n_in) continue;
                 float back = 1.0f;
                 if constexpr (std::is_same<T, __half>::value) back = __uint_as_float(row_exponent(row_max[r]) << 23);
-                up_store<T>(p, acc, h, static_cast<int64_t>(row0 + order[r]) * p.N + n, back);
+                up_store<T>(p, acc[q / 2], q & 1, static_cast<int64_t>(order[r]) * p.N + n, back);
             }
         }
     }
     ptx::cp_async_wait_group<0>();
 }
 
-// U = beta C (or zero) of rows without an adapter.
+// U = beta C (or zero) of the m rows without an adapter, shared out over all warps in
+// parts of up to 1024 columns.
 template <class T>
-__device__ void up_none(const LoraParams& p, const int32_t* order, int m, int row0, int64_t n0, int columns) {
-    const int vecs = columns / 8;
-    for (int i = threadIdx.x; i < m * vecs; i += kLoraThreads) {
-        const int r = i / vecs;
+__device__ __forceinline__ void up_none(const LoraParams& p, const int32_t* order, int m) {
+    const int lane = threadIdx.x & 31;
+    const int64_t parts = (static_cast<int64_t>(p.N) + 1023) / 1024, total = m * parts;
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * kLoraWarps;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kLoraWarps + (threadIdx.x >> 5); i < total; i += warps) {
+        const int64_t r = div_nonneg(i, parts), n0 = (i - r * parts) * 1024;
+        const int64_t row = p.list != nullptr ? __ldcg(order + r) : order[r];
         const float zero[4][4] = {};
-        up_store<T>(p, zero, 0, static_cast<int64_t>(row0 + order[r]) * p.N + n0 + 8 * (i - r * vecs), 1.0f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t n = n0 + 256 * j + 8 * lane;
+            if (n < p.N) up_store<T>(p, zero, 0, row * p.N + n, 1.0f);
+        }
     }
 }
 
@@ -622,8 +758,7 @@ __host__ __device__ constexpr int lora_space_bytes(int R) {
     return ((v > e ? v : e) + 127) / 128 * 128;
 }
 
-// Grid: clusters that share a tile, tiles; a cluster takes groups in turn, the last
-// of which is the rows without an adapter.
+// Grid: clusters, which take groups (or units of the list) in turn.
 template <class T, class Sh>
 __global__ void __launch_bounds__(kLoraThreads, Sh::LONG ? 1 : 2) lora_kernel(const LoraParams p) {
     extern __shared__ __align__(16) uint8_t smem[];
@@ -635,39 +770,55 @@ __global__ void __launch_bounds__(kLoraThreads, Sh::LONG ? 1 : 2) lora_kernel(co
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const int rank = static_cast<int>(ptx::cluster_ctarank());
-    const int row0 = static_cast<int>(blockIdx.y) * p.tile_rows;
-    const int rows = min(p.tile_rows, p.M - row0);
-    if (rows <= 32) group_few_rows(p, row0, rows, s);
-    else group_rows(p, row0, rows, s, *reinterpret_cast<GroupTable*>(space));
-    const int groups = s.n + (s.start[s.n] < rows ? 1 : 0);
+    int groups;
+    if (p.list != nullptr) {
+        groups = __ldcg(&p.list->n);
+    } else {
+        if (p.M <= 32) group_few_rows(p, p.M, s);
+        else group_rows(p, p.M, s, *reinterpret_cast<GroupTable*>(space));
+        groups = s.n;
+    }
     const int64_t n0 = static_cast<int64_t>(rank) * p.width;
     const int columns = static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(p.width), p.N - n0)));
     const int s0 = static_cast<int>(static_cast<int64_t>(p.k_steps) * rank / p.cluster);
     const int s1 = static_cast<int>(static_cast<int64_t>(p.k_steps) * (rank + 1) / p.cluster);
     const int most = up_rows(p.R);
     for (int g = blockIdx.x / p.cluster; g < groups; g += gridDim.x / p.cluster) {
-        const bool has = g < s.n;
-        const int end = has ? s.start[g + 1] : rows;
-        const int64_t adapter = has ? s.adapter[g] : 0;
+        int64_t adapter;
+        int begin, end;
+        if (p.list != nullptr) {
+            const int4 unit = __ldcg(reinterpret_cast<const int4*>(&p.list->units[g]));
+            adapter = unit.x;
+            begin = 0;
+            end = unit.z;   // at most unit_rows <= most
+            if (static_cast<int>(threadIdx.x) < end) s.order[threadIdx.x] = __ldcg(&p.list->order[unit.y + threadIdx.x]);
+            __syncthreads();
+        } else {
+            adapter = s.adapter[g];
+            begin = s.start[g];
+            end = s.start[g + 1];
+        }
         const T* A = static_cast<const T*>(p.A) + adapter * p.R * p.K;
         const T* B = static_cast<const T*>(p.B) + (adapter * p.N + n0) * p.R;
-        const float factor = has && p.factors != nullptr ? p.factors[adapter] : 1.0f;
-        for (int i = s.start[g]; i < end; i += most) {
+        const float factor = p.factors != nullptr ? p.factors[adapter] : 1.0f;
+        for (int i = begin; i < end; i += most) {
             const int m = min(most, end - i);
-            if (!has) {
-                up_none<T>(p, s.order + i, m, row0, n0, columns);
-                continue;
-            }
             BStream<T, Sh> b;
             b.start(B, p.R, columns, m, ptx::smem_u32(b_places));   // on its way while V is formed
-            down<T, Sh>(p, A, s.order + i, m, row0, s0, s1, space, part);
+            down<T, Sh>(p, A, s.order + i, m, p.list != nullptr ? p.unit_rows : m, s0, s1, space, part);
             ptx::cluster_sync();   // every CTA's partial sums are there
             take_rows<T>(p, m, factor, ptx::smem_u32(part), space, row_max);
             ptx::cluster_arrive();   // this CTA has read them
-            up<T, Sh>(p, b, s.order + i, m, row0, n0, columns, space, row_max);
+            up<T, Sh>(p, b, s.order + i, m, n0, columns, space, row_max);
             ptx::cluster_wait();   // nobody reads this CTA's partial sums any more
-            __syncthreads();       // nor V
+            __syncthreads();       // nor V, nor the order
         }
+    }
+    if (p.list != nullptr) {
+        const int with = __ldcg(&p.list->with);
+        up_none<T>(p, p.list->order + with, p.M - with);
+    } else if (s.start[s.n] < p.M) {
+        up_none<T>(p, s.order + s.start[s.n], p.M - s.start[s.n]);
     }
 }
 
@@ -687,7 +838,7 @@ __global__ void __launch_bounds__(kLoraOnlyThreads) lora_v_kernel(const LoraPara
     // only now: the product that starts early relies on everything before this kernel
     ptx::griddep_launch_dependents();
     const int rank = static_cast<int>(ptx::cluster_ctarank());
-    group_few_rows(p, 0, p.M, s);
+    group_few_rows(p, p.M, s);
     const int s0 = static_cast<int>(static_cast<int64_t>(p.k_steps) * rank / p.cluster);
     const int s1 = static_cast<int>(static_cast<int64_t>(p.k_steps) * (rank + 1) / p.cluster);
     for (int g = blockIdx.x / p.cluster; g < s.n; g += gridDim.x / p.cluster) {
@@ -697,17 +848,16 @@ __global__ void __launch_bounds__(kLoraOnlyThreads) lora_v_kernel(const LoraPara
         const int32_t* order = s.order + s.start[g];
         const T* A = static_cast<const T*>(p.A) + adapter * p.R * p.K;
         for (int r0 = 0; r0 < p.R; r0 += 16) {
-            if (m <= 8) down_rows<T, RanksOnlyV, 1, 1>(p, A, r0, order, m, 0, s0, s1, space, part);
-            else down_rows<T, RanksOnlyV, 2, 1>(p, A, r0, order, m, 0, s0, s1, space, part);
+            if (m <= 8) down_rows<T, RanksOnlyV, 1, 1, 1>(p, A, r0, order, m, s0, s1, space, part);
+            else down_rows<T, RanksOnlyV, 1, 2, 1>(p, A, r0, order, m, s0, s1, space, part);
         }
         ptx::cluster_sync();   // every CTA's partial sums are there
-        give_rows(p, m, factor, ptx::smem_u32(part), rank, 0, order);
+        give_rows(p, m, factor, ptx::smem_u32(part), rank, order);
         ptx::cluster_sync();   // and have been read
     }
 }
 
 // -------------------------------------------------------------------------- host
-constexpr int64_t kLoraRows = 1 << 20;   // rows per launch: tiles are the grid's second dimension, at most 65535
 
 // Sets a kernel's preference for shared memory over L1, once per kernel and device.
 bool keep_smem(const void* kernel, int dev) {
@@ -724,12 +874,13 @@ bool keep_smem(const void* kernel, int dev) {
 }
 
 // Fills the split of `p` and launches.
-//  - A batch of requests is one tile with as many groups as adapters in use, taken to
-//    be chosen evenly.  While all clusters fit the GPU with one CTA per SM, they get one each
+//  - Up to 256 rows, a batch of requests, make as many groups as adapters in use, taken
+//    to be chosen evenly.  While all clusters fit the GPU with one CTA per SM, they get one each
 //    (by asking for more than half of its shared memory): started while the kernel before
 //    drains, two would go to the SMs that are free first (@FIG@).
-//  - A prompt's tiles have one adapter or two: as many tiles as clusters of four run
-//    with two CTAs per SM.
+//  - More rows are cut into units of 32, 64 or 128 rows for clusters of four, two CTAs per SM
+//    up to 32 ranks: what takes the fewest rounds, each of the unit's rows and what a unit costs
+//    besides (some 24 rows' time).  Up to one unit per adapter is not full.
 template <class T, class Sh>
 gemm_status_t launch(LoraParams p, const DeviceView& dev, cudaStream_t s) {
     const auto kernel = lora_kernel<T, Sh>;
@@ -737,9 +888,8 @@ gemm_status_t launch(LoraParams p, const DeviceView& dev, cudaStream_t s) {
     auto at_once = [&](int cluster, int bytes) {
         return std::max(1, active_clusters(reinterpret_cast<const void*>(kernel), dev, kLoraThreads, bytes, cluster));
     };
-    int tiles = 1, clusters = 1;
-    if (p.M <= kLoraTile) {
-        p.tile_rows = kLoraTile;
+    int clusters = 1;
+    if (p.list == nullptr) {
         const double count = std::max(1, p.count);
         const double groups = std::max(1.0, count * (1.0 - std::pow(1.0 - 1.0 / count, static_cast<double>(p.M))));
         const int alone = std::max(smem, kMaxDynamicSmem / 2 + 2048);
@@ -748,15 +898,26 @@ gemm_status_t launch(LoraParams p, const DeviceView& dev, cudaStream_t s) {
         clusters = std::min(at_once(p.cluster, smem), static_cast<int>(std::min<int64_t>(p.M, int64_t{p.count} + 1)));
     } else {
         p.cluster = 4;
-        const int most = at_once(p.cluster, smem);
-        p.tile_rows = std::min(kLoraTile, std::max(48, ((p.M + most - 1) / most + 15) / 16 * 16));
-        tiles = (p.M + p.tile_rows - 1) / p.tile_rows;
-        clusters = std::max(1, most / tiles);
+        clusters = at_once(p.cluster, smem);
+        double best = 0.0;
+        for (int rows = 32; rows <= up_rows(p.R); rows *= 2) {
+            const double whole = static_cast<double>(p.M) / rows;
+            const double units = whole + std::min(static_cast<double>(p.count), std::max(whole, static_cast<double>(clusters)));
+            const double t = std::ceil(units / clusters) * (rows + 24);
+            if (best == 0.0 || t < best) {
+                best = t;
+                p.unit_rows = rows;
+            }
+        }
+        const int bits = list_bits(p.M);
+        const gemm_status_t st = launch_clusters(lora_list_kernel, dev.dev, dim3(1, 1, 1), kListThreads, 1,
+                                                 (2 << bits) * 4 + 16, true, s, p, const_cast<LoraList*>(p.list), bits);
+        if (st != GEMM_OK) return st;
     }
     const int64_t per = p.cluster * kLoraColumns;
     p.width = static_cast<int32_t>((p.N + per - 1) / per * kLoraColumns);
-    return launch_clusters(kernel, dev.dev, dim3(static_cast<unsigned>(clusters * p.cluster), static_cast<unsigned>(tiles), 1),
-                           kLoraThreads, p.cluster, smem, true, s, p);
+    return launch_clusters(kernel, dev.dev, dim3(static_cast<unsigned>(clusters * p.cluster), 1, 1), kLoraThreads, p.cluster,
+                           smem, true, s, p);
 }
 
 // Eight CTAs per adapter in use, on as many SMs as there are.  The SMs keep all of their
@@ -781,15 +942,18 @@ gemm_status_t run(const LoraParams& p, const DeviceView& dev, cudaStream_t s) {
 
 }  // namespace
 
-gemm_status_t run_lora(bool bf16, const LoraArgs& a, const DeviceView& dev, cudaStream_t s) {
-    for (int64_t m0 = 0; m0 < a.M; m0 += kLoraRows) {
-        const int64_t M = std::min(kLoraRows, a.M - m0);
+size_t lora_scratch_bytes(int64_t M) { return M > kLoraTile ? sizeof(LoraList) : 0; }
+
+gemm_status_t run_lora(bool bf16, const LoraArgs& a, uint8_t* data, const DeviceView& dev, cudaStream_t s) {
+    for (int64_t m0 = 0; m0 < a.M; m0 += kListRows) {
+        const int64_t M = std::min<int64_t>(kListRows, a.M - m0);
         LoraParams p{};
         p.X = static_cast<const uint16_t*>(a.X) + m0 * a.K;
         p.A = a.A;
         p.B = a.B;
         p.factors = a.factors;
         p.ids = a.K > 0 && a.count > 0 ? a.ids + m0 : nullptr;
+        p.list = M > kLoraTile ? reinterpret_cast<const LoraList*>(data) : nullptr;
         p.C = a.C != nullptr ? static_cast<const uint16_t*>(a.C) + m0 * a.N : nullptr;
         p.U = static_cast<uint16_t*>(a.U) + m0 * a.N;
         p.V = a.V;
