@@ -49,6 +49,7 @@ struct LoraParams {
     int32_t M, N, K, R, count;
     int32_t k_steps, width;  // width: columns per CTA of a cluster
     int32_t unit_rows;       // with a list: most rows of a unit, 32, 64 or 128
+    int32_t most_rows;       // rows of V in hand at one time
     int32_t cluster;         // its CTAs
     float beta;
 };
@@ -318,25 +319,25 @@ __global__ void __launch_bounds__(kListThreads) lora_list_kernel(const LoraParam
 // Every thread copies the pieces of its own fragments to places of its own in shared
 // memory (cp.async), some steps ahead, and reads them back: many bytes under way without
 // registers for them, and nobody to wait for.
-// How a launch is built.  MT: 16-row tiles of ranks of the first product in hand; SLOTS:
-// 16-byte places per thread for its copies; S: steps of 16 ranks per chunk of the second
+// How a launch is built.  MT: 16-row tiles of ranks of the first product in hand, TILE: ranks
+// with many rows; SLOTS: 16-byte places per thread for its copies; S: steps of 16 ranks per chunk of the second
 // product, LONG: R has more than one chunk; AHEAD: chunks under way.  SLOTS and AHEAD leave
 // room for two CTAs per SM up to 32 ranks; with more, a CTA has enough to
 // copy to be alone (61 rows, 48 adapters of 64 x (4096 + 8192): @LONG@).
 struct Ranks16 {
-    static constexpr int MT = 1, SLOTS = 18, WARPS = kLoraWarps, S = 1, AHEAD = 2;
+    static constexpr int MT = 1, TILE = 16, SLOTS = 18, WARPS = kLoraWarps, S = 1, AHEAD = 2;
     static constexpr bool LONG = false;
 };
 struct Ranks32 {
-    static constexpr int MT = 2, SLOTS = 16, WARPS = kLoraWarps, S = 2, AHEAD = 1;
+    static constexpr int MT = 2, TILE = 32, SLOTS = 16, WARPS = kLoraWarps, S = 2, AHEAD = 1;
     static constexpr bool LONG = false;
 };
 struct RanksMore {
-    static constexpr int MT = 2, SLOTS = 24, WARPS = kLoraWarps, S = 2, AHEAD = 3;
+    static constexpr int MT = 2, TILE = 64, SLOTS = 24, WARPS = kLoraWarps, S = 2, AHEAD = 3;
     static constexpr bool LONG = true;
 };
 struct RanksOnlyV {   // V alone, by fewer warps with little memory
-    static constexpr int MT = 1, SLOTS = 8, WARPS = 4;
+    static constexpr int SLOTS = 8, WARPS = 4;
 };
 
 // Floats between the sums of two rows in the warps' exchange, which takes the same
@@ -443,19 +444,128 @@ __device__ __forceinline__ void down_rows(const LoraParams& p, const T* A, int r
     __syncthreads();
 }
 
-// `like`: how many rows decide how the warps share the work, and so the order of a row's
-// sums.  Many rows of a high rank take 64 ranks at a time, so that X is read for twice as many; few
-// rows 32, so that more steps are under way.
+// The same for units of ROWS = 64 or 128 rows and TILE ranks from r0 on: rows and ranks meet
+// so often that they are copied once for the whole CTA, 64 k at a time, in 128-byte rows whose
+// 16-byte pieces are swapped by the row's number, and read by ldmatrix; 32 rows per warp, the steps
+// of 16 k dealt out to the warps of the same rows.  (The form above, where every warp copies the
+// ranks for itself, took @TILED@.)
+template <class T, class Sh, int ROWS>
+__device__ __forceinline__ void down_tile(const LoraParams& p, const T* A, int r0, const int32_t* rows, int m, int s0, int s1,
+                                          uint8_t* space, float* part) {
+    constexpr int RT = Sh::TILE, STAGE = (ROWS + RT) * 128, D = kDownBytes<Sh> / STAGE < 6 ? kDownBytes<Sh> / STAGE : 6;
+    constexpr int PARTS = ROWS / 32, KW = kLoraWarps / PARTS, P = RT + 2;
+    static_assert(D >= 3 && kLoraWarps * 32 * P * 4 <= kDownBytes<Sh>, "two stages ahead; the exchange fits");
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const uint32_t base = ptx::smem_u32(space);
+    // this thread's pieces: column c of rows tid / 8 + 32 i
+    const int c = tid & 7, row = tid >> 3;
+    const int64_t k_first = static_cast<int64_t>(s0) * kLoraStepK;
+    const int64_t k_last = min(static_cast<int64_t>(s1) * kLoraStepK, static_cast<int64_t>(p.K));
+    const int chunks = static_cast<int>((k_last - k_first + 63) / 64);
+    const uint32_t place = base + row * 128 + ((c ^ (row & 7)) << 4);
+    const T* x_ptr[ROWS / 32];
+#pragma unroll
+    for (int i = 0; i < ROWS / 32; ++i)
+        x_ptr[i] = row + 32 * i < m ? static_cast<const T*>(p.X) + static_cast<int64_t>(rows[row + 32 * i]) * p.K + k_first + 8 * c
+                                    : nullptr;
+    const T* a_ptr = A + static_cast<int64_t>(r0 + row) * p.K + k_first + 8 * c;
+    auto fetch = [&](int chunk, int d) {
+        const int64_t k = static_cast<int64_t>(chunk) * 64;
+        const bool in = k_first + k + 8 * c < k_last;
+#pragma unroll
+        for (int i = 0; i < ROWS / 32; ++i) {
+            const bool take = in && x_ptr[i] != nullptr;
+            ptx::cp_async16_or_zero(place + d * STAGE + i * 4096, take ? x_ptr[i] + k : A, take);
+        }
+#pragma unroll
+        for (int i = 0; i < (RT + 31) / 32; ++i) {
+            if (RT < 32 && row >= RT) break;
+            const bool take = in && r0 + row + 32 * i < p.R;
+            ptx::cp_async16_or_zero(place + d * STAGE + ROWS * 128 + i * 4096,
+                                    take ? a_ptr + static_cast<int64_t>(32 * i) * p.K + k : A, take);
+        }
+        ptx::cp_async_commit();
+    };
+    float acc[2][RT / 8][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < RT / 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.0f;
+#pragma unroll
+    for (int d = 0; d < D - 1; ++d) fetch(d, d);
+    // ldmatrix: lane l gives the address of row l % 8 of matrix l / 8.  Rows: matrices are
+    // (rows, k) = (lo, lo), (hi, lo), (lo, hi), (hi, hi); ranks: (lo, lo), (lo, hi), (hi, lo), (hi, hi).
+    const int x_row = warp % PARTS * 32 + (lane & 15), x_half = lane >> 4;
+    const int a_row = (lane & 7) + ((lane >> 4) << 3), a_half = (lane >> 3) & 1;
+    int d = 0;
+    for (int i = 0; i < chunks; ++i) {
+        ptx::cp_async_wait_group<D - 2>();
+        __syncthreads();   // everybody's copies of this chunk are there, the stage before has been read
+        fetch(i + D - 1, d == 0 ? D - 1 : d - 1);
+        const uint32_t x_at = base + d * STAGE + x_row * 128, a_at = base + d * STAGE + (ROWS + a_row) * 128;
+        for (int k = warp / PARTS; k < 4; k += KW) {
+            uint32_t x[2][4];
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                ptx::ldmatrix_x4_now(x_at + q * 2048 + (((2 * k + x_half) ^ (x_row & 7)) << 4), x[q]);
+#pragma unroll
+            for (int j = 0; j < RT / 16; ++j) {
+                uint32_t a[4];
+                ptx::ldmatrix_x4_now(a_at + j * 2048 + (((2 * k + a_half) ^ (a_row & 7)) << 4), a);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    ptx::mma16816<T>(acc[q][2 * j], x[q], a[0], a[1]);
+                    ptx::mma16816<T>(acc[q][2 * j + 1], x[q], a[2], a[3]);
+                }
+            }
+        }
+        if (++d == D) d = 0;
+    }
+    ptx::cp_async_wait_group<0>();
+    __syncthreads();
+    float* red = reinterpret_cast<float*>(space);
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int j = 0; j < RT / 8; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                *reinterpret_cast<float2*>(red + (warp * 32 + 16 * q + 8 * h + g) * P + 8 * j + 2 * t) =
+                    make_float2(acc[q][j][2 * h], acc[q][j][2 * h + 1]);
+    __syncthreads();
+    for (int i = tid; i < m * RT; i += kLoraThreads) {
+        const int n = i / RT, r = i % RT;
+        if (r0 + r >= p.R) continue;
+        const float* from = red + n * P + r;   // row n of part n / 32, of the first warp that has it
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < KW; ++w) v += from[w * PARTS * 32 * P];
+        part[n * p.R + r0 + r] = v;
+    }
+    __syncthreads();
+}
+
+// `like`: how many rows decide how the warps share the work, and so the order of a row's sums.
 template <class T, class Sh>
 __device__ __forceinline__ void down(const LoraParams& p, const T* A, const int32_t* rows, int m, int like, int s0, int s1,
                                      uint8_t* space, float* part) {
-    constexpr int MT = Sh::MT, MM = Sh::LONG ? 2 * MT : MT;
-    for (int r0 = 0; r0 < p.R; r0 += 16 * (like <= 16 ? MT : MM)) {
-        if (like <= 8) down_rows<T, Sh, MT, 1, 1>(p, A, r0, rows, m, s0, s1, space, part);
-        else if (like <= 16) down_rows<T, Sh, MT, 2, 1>(p, A, r0, rows, m, s0, s1, space, part);
-        else if (like <= 32) down_rows<T, Sh, MM, 4, 1>(p, A, r0, rows, m, s0, s1, space, part);
-        else if (like <= 64) down_rows<T, Sh, MM, 4, 2>(p, A, r0, rows, m, s0, s1, space, part);
-        else down_rows<T, Sh, MM, 4, 4>(p, A, r0, rows, m, s0, s1, space, part);
+    if (like > 32) {
+        for (int r0 = 0; r0 < p.R; r0 += Sh::TILE) {
+            if constexpr (Sh::TILE == 32) {   // never more than 64 rows
+                down_tile<T, Sh, 64>(p, A, r0, rows, m, s0, s1, space, part);
+            } else {
+                if (like <= 64) down_tile<T, Sh, 64>(p, A, r0, rows, m, s0, s1, space, part);
+                else down_tile<T, Sh, 128>(p, A, r0, rows, m, s0, s1, space, part);
+            }
+        }
+        return;
+    }
+    for (int r0 = 0; r0 < p.R; r0 += 16 * Sh::MT) {
+        if (like <= 8) down_rows<T, Sh, Sh::MT, 1, 1>(p, A, r0, rows, m, s0, s1, space, part);
+        else if (like <= 16) down_rows<T, Sh, Sh::MT, 2, 1>(p, A, r0, rows, m, s0, s1, space, part);
+        else down_rows<T, Sh, Sh::MT, 4, 1>(p, A, r0, rows, m, s0, s1, space, part);
     }
 }
 
@@ -471,9 +581,7 @@ __host__ __device__ constexpr int up_pitch(int R) {
     return up_ranks(R) * 4 + (((R <= 16 ? 64 : 16) - up_ranks(R) * 4) & 127);
 }
 // rows of V in shared memory at one time
-__host__ __device__ constexpr int up_rows(int R) {
-    return R <= 16 ? 128 : (R <= 32 ? 64 : (R <= 64 ? 128 : (R <= 128 ? 64 : 32)));
-}
+int up_rows(int R) { return R <= 16 ? 128 : (R <= 32 ? 64 : (R <= 64 ? 128 : (R <= 128 ? 64 : 32))); }
 
 // The two numbers of type T that v is the sum of.
 template <class T>
@@ -686,7 +794,7 @@ __device__ __forceinline__ void up_store(const LoraParams& p, const float (&acc)
 
 // U of m rows of one group and `columns` columns from n0 on; b: their part of B, on its
 // way.  With one chunk (!LONG) its fragments serve all rows.
-template <class T, class Sh>
+template <class T, class Sh, int RB>
 __device__ __forceinline__ void up(const LoraParams& p, BStream<T, Sh>& b, const int32_t* order, int m, int64_t n0,
                                    int columns, const uint8_t* v_rows, const uint32_t* row_max) {
     constexpr int S = Sh::S;
@@ -697,7 +805,6 @@ __device__ __forceinline__ void up(const LoraParams& p, BStream<T, Sh>& b, const
         if constexpr (!LONG) b.next(f);
         const int64_t n = n0 + nb + 8 * t;   // this thread's 8 columns of the output
         const bool n_in = nb + 8 * t < columns;
-        constexpr int RB = kRowBlocks<Sh>;
         for (int r0 = 0; r0 < m; r0 += 16 * RB) {
             // rows beyond m read what lies there: only outputs that are not written come of it
             const uint8_t* v = v_rows + (r0 + gr) * pitch + 16 * S * t;
@@ -753,8 +860,8 @@ __device__ __forceinline__ void up_none(const LoraParams& p, const int32_t* orde
 // Shared memory: the groups; the first product's copies and exchange, then V; the
 // second product's copies; the partial sums.
 template <class Sh>
-__host__ __device__ constexpr int lora_space_bytes(int R) {
-    const int v = up_rows(R) * up_pitch(R), e = kDownBytes<Sh>;
+__host__ __device__ constexpr int lora_space_bytes(int R, int rows) {
+    const int v = rows * up_pitch(R), e = kDownBytes<Sh>;
     return ((v > e ? v : e) + 127) / 128 * 128;
 }
 
@@ -765,7 +872,7 @@ __global__ void __launch_bounds__(kLoraThreads, Sh::LONG ? 1 : 2) lora_kernel(co
     __shared__ uint32_t row_max[128];
     Groups& s = *reinterpret_cast<Groups*>(smem);
     uint8_t* space = smem + kGroupsBytes;
-    uint8_t* b_places = space + lora_space_bytes<Sh>(p.R);
+    uint8_t* b_places = space + lora_space_bytes<Sh>(p.R, p.most_rows);
     float* part = reinterpret_cast<float*>(b_places + kUpBytes<Sh>);
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
@@ -782,7 +889,7 @@ __global__ void __launch_bounds__(kLoraThreads, Sh::LONG ? 1 : 2) lora_kernel(co
     const int columns = static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(p.width), p.N - n0)));
     const int s0 = static_cast<int>(static_cast<int64_t>(p.k_steps) * rank / p.cluster);
     const int s1 = static_cast<int>(static_cast<int64_t>(p.k_steps) * (rank + 1) / p.cluster);
-    const int most = up_rows(p.R);
+    const int most = p.most_rows;
     for (int g = blockIdx.x / p.cluster; g < groups; g += gridDim.x / p.cluster) {
         int64_t adapter;
         int begin, end;
@@ -809,7 +916,8 @@ __global__ void __launch_bounds__(kLoraThreads, Sh::LONG ? 1 : 2) lora_kernel(co
             ptx::cluster_sync();   // every CTA's partial sums are there
             take_rows<T>(p, m, factor, ptx::smem_u32(part), space, row_max);
             ptx::cluster_arrive();   // this CTA has read them
-            up<T, Sh>(p, b, s.order + i, m, n0, columns, space, row_max);
+            if (m > 16) up<T, Sh, kRowBlocks<Sh>>(p, b, s.order + i, m, n0, columns, space, row_max);
+            else up<T, Sh, 1>(p, b, s.order + i, m, n0, columns, space, row_max);
             ptx::cluster_wait();   // nobody reads this CTA's partial sums any more
             __syncthreads();       // nor V, nor the order
         }
@@ -884,7 +992,8 @@ bool keep_smem(const void* kernel, int dev) {
 template <class T, class Sh>
 gemm_status_t launch(LoraParams p, const DeviceView& dev, cudaStream_t s) {
     const auto kernel = lora_kernel<T, Sh>;
-    int smem = kGroupsBytes + lora_space_bytes<Sh>(p.R) + kUpBytes<Sh> + up_rows(p.R) * p.R * 4;
+    p.most_rows = up_rows(p.R);
+    int smem = kGroupsBytes + lora_space_bytes<Sh>(p.R, p.most_rows) + kUpBytes<Sh> + p.most_rows * p.R * 4;
     auto at_once = [&](int cluster, int bytes) {
         return std::max(1, active_clusters(reinterpret_cast<const void*>(kernel), dev, kLoraThreads, bytes, cluster));
     };
@@ -900,7 +1009,7 @@ gemm_status_t launch(LoraParams p, const DeviceView& dev, cudaStream_t s) {
         p.cluster = 4;
         clusters = at_once(p.cluster, smem);
         double best = 0.0;
-        for (int rows = 32; rows <= up_rows(p.R); rows *= 2) {
+        for (int rows = 32; rows <= p.most_rows; rows *= 2) {
             const double whole = static_cast<double>(p.M) / rows;
             const double units = whole + std::min(static_cast<double>(p.count), std::max(whole, static_cast<double>(clusters)));
             const double t = std::ceil(units / clusters) * (rows + 24);
