@@ -19,6 +19,7 @@ namespace {
 constexpr int kNormVec = 8;            // elements per 16-byte access
 constexpr int kNormMaxThreads = 1024;  // per row
 constexpr int kNormMaxVecs = 4;        // 16-byte pieces of a row per thread
+constexpr int kStayThreads = 512;      // per SM where CTAs stay
 
 struct NormParams {
     const void* X;
@@ -30,7 +31,7 @@ struct NormParams {
     void* total;          // or nullptr
     int64_t T;
     int32_t H;
-    int32_t row_threads;  // a power of two, 32 .. 1024
+    int32_t row_threads;  // the whole CTA, or a power of two from 4 on of it
     float eps, scale, top;
     int32_t e5m2;
 };
@@ -63,18 +64,19 @@ __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(
 __device__ __forceinline__ void reduce_row(float& sum, uint32_t& top, int row_threads) {
     __shared__ float part_sum[kNormMaxThreads / 32];
     __shared__ uint32_t part_top[kNormMaxThreads / 32];
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    top = __reduce_max_sync(0xffffffffu, top);
+    for (int d = row_threads < 32 ? row_threads / 2 : 16; d > 0; d >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+    }
     const int warps = row_threads >> 5;
-    if (warps == 1) return;
+    if (warps <= 1) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0) {
         part_sum[warp] = sum;
         part_top[warp] = top;
     }
     __syncthreads();
-    const int first = warp & ~(warps - 1);
+    const int first = warp / warps * warps;
     sum = lane < warps ? part_sum[first + lane] : 0.0f;
     top = lane < warps ? part_top[first + lane] : 0u;
 #pragma unroll
@@ -175,7 +177,7 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormParams p) {
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     const int row_threads = p.row_threads;
-    const int in_row = threadIdx.x & (row_threads - 1);
+    const int in_row = threadIdx.x % row_threads;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / row_threads) + threadIdx.x / row_threads;
     const int vecs = p.H / kNormVec;
     const int64_t base = row * vecs;
@@ -205,6 +207,59 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormParams p) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
         if (in[i]) write_piece<T>(p, f, h[i], w[i], base + in_row + i * row_threads);
+}
+
+// The same for many rows: CTAs stay and fetch the next rows while they work on these; the
+// weight stays in registers.  NV pieces of each of x, r and w per thread.
+template <class T, int NV>
+__global__ void __launch_bounds__(kStayThreads) norm_stay_kernel(const NormParams p) {
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    const int row_threads = p.row_threads, rows = blockDim.x / row_threads;
+    const int in_row = threadIdx.x % row_threads;
+    const int vecs = p.H / kNormVec;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
+    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+    uint4 w[NV], xn[NV], rn[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int v = in_row + i * row_threads;
+        w[i] = v < vecs && p.W != nullptr ? load8<T>(p.W, v) : none;
+    }
+    auto fetch = [&](int64_t row) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = in_row + i * row_threads;
+            const bool in = row < p.T && v < vecs;
+            xn[i] = in ? load8<T>(p.X, row * vecs + v) : none;
+            rn[i] = in && p.R != nullptr ? load8<T>(p.R, row * vecs + v) : none;
+        }
+    };
+    int64_t row = static_cast<int64_t>(blockIdx.x) * rows + threadIdx.x / row_threads;
+    fetch(row);
+    // whole CTAs go round: the sums meet at a barrier
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * rows; first < p.T; first += step, row += step) {
+        float h[NV][8], sum = 0.0f;
+        uint32_t top = 0u;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) take_piece<T>(p, xn[i], rn[i], w[i], h[i], sum, top);
+        fetch(row + step);   // other rows than any output written now
+        const int64_t base = row * vecs;
+        if (p.total != nullptr && row < p.T) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (in_row + i * row_threads < vecs)
+                    static_cast<uint4*>(p.total)[base + in_row + i * row_threads] = pack8<T>(h[i]);
+        }
+        reduce_row(sum, top, row_threads);
+        if (row < p.T) {
+            const RowFactors f = row_factors(p, sum, top, row, in_row == 0);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (in_row + i * row_threads < vecs) write_piece<T>(p, f, h[i], w[i], base + in_row + i * row_threads);
+        }
+        if (row_threads > 32) __syncthreads();   // the sums have been read
+    }
 }
 
 // Rows too long for registers: read a second time, each piece by the thread that
@@ -248,13 +303,24 @@ gemm_status_t run(NormParams p, const DeviceView& dev, cudaStream_t s) {
         p.row_threads = kNormMaxThreads;
         return launch_clusters(norm_long_kernel<T>, dev.dev, static_cast<int>(p.T), kNormMaxThreads, 1, 0, true, s, p);
     }
-    // Few rows leave SMs idle whatever the split, so a row gets a thread per piece;
-    // with many, four pieces per thread keep enough loads in flight.
+    // Few rows leave SMs idle whatever the split, so a row gets a thread per piece; with
+    // many, four pieces per thread keep enough loads under way.
     const int want = p.T <= 2 * dev.sms ? 1 : kNormMaxVecs;
-    p.row_threads = std::min(kNormMaxThreads, std::max(32, power_of_two((vecs + want - 1) / want)));
+    const int each = (vecs + want - 1) / want;
+    p.row_threads = each > 128 ? std::min(kNormMaxThreads, (each + 31) / 32 * 32) : std::max(want == 1 ? 32 : 4, power_of_two(each));
+    if (want > 1 && each > 128 && p.row_threads < kStayThreads)   // as many as cost no CTA
+        p.row_threads = kStayThreads / (kStayThreads / p.row_threads) / 32 * 32;
     const int nv = (vecs + p.row_threads - 1) / p.row_threads;
     const int rows = want == 1 ? 1 : std::max(1, 256 / p.row_threads);
     const int grid = static_cast<int>((p.T + rows - 1) / rows), threads = rows * p.row_threads;
+    // CTAs stay where each has several turns (4096 x 8192 bf16 to E4M3 48 -> 38 us)
+    const int stay = dev.sms * (kStayThreads / std::min(threads, kStayThreads));
+    if (threads <= kStayThreads && grid >= 2 * stay) {
+        if (nv <= 1) return launch_clusters(norm_stay_kernel<T, 1>, dev.dev, stay, threads, 1, 0, true, s, p);
+        if (nv <= 2) return launch_clusters(norm_stay_kernel<T, 2>, dev.dev, stay, threads, 1, 0, true, s, p);
+        if (nv <= 3) return launch_clusters(norm_stay_kernel<T, 3>, dev.dev, stay, threads, 1, 0, true, s, p);
+        return launch_clusters(norm_stay_kernel<T, 4>, dev.dev, stay, threads, 1, 0, true, s, p);
+    }
     if (nv <= 1) return launch_clusters(norm_kernel<T, 1, 1024>, dev.dev, grid, threads, 1, 0, true, s, p);
     if (nv <= 2) return launch_clusters(norm_kernel<T, 2, 1024>, dev.dev, grid, threads, 1, 0, true, s, p);
     // 1024 threads leave 64 registers each, 512 enough for four pieces without spills
