@@ -718,7 +718,7 @@ gemm_status_t run(const void* A, const void* B, void* D, int64_t M, int64_t N, i
     st = check_epilogue(epilogue, D, M, N);
     if (st != GEMM_OK) return st;
     if (scale_m != nullptr) {
-        if (!aligned16(scale_m)) return GEMM_ERR_MISALIGNED;
+        if (!aligned4(scale_m)) return GEMM_ERR_MISALIGNED;
         if (ranges_overlap(scale_m, M * 4, D, M * N * 2)) return GEMM_ERR_INVALID_VALUE;
         if (K > 0) {   // the empty sum is zero whatever the scales
             epi.scale_m = scale_m;
@@ -1108,7 +1108,11 @@ GEMM_API gemm_status_t gemm_nt_scaled(gemm_dtype_t dtype, const void* A, const f
                                       gemm_stream_t stream) {
     if (dtype != GEMM_DTYPE_E4M3 && dtype != GEMM_DTYPE_E5M2) return GEMM_ERR_INVALID_VALUE;
     if (scale_m == nullptr && M > 0 && N > 0) return GEMM_ERR_INVALID_VALUE;
-    return run(A, B, D, M, N, K, GEMM_VARIANT_AUTO, stream, static_cast<int>(dtype), epilogue, scale_m);
+    try {   // no exception leaves a C entry (the map behind device state allocates)
+        return run(A, B, D, M, N, K, GEMM_VARIANT_AUTO, stream, static_cast<int>(dtype), epilogue, scale_m);
+    } catch (...) {
+        return GEMM_ERR_CUDA;
+    }
 }
 
 GEMM_API gemm_status_t gemm_f16_nt_check(gemm_stream_t stream) {

@@ -42,6 +42,7 @@ bool encode_map(CUtensorMap* map, const void* base, int elem_bytes, int64_t inne
                 uint32_t box_outer, bool swizzle128);
 
 bool ranges_overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes);
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // What scratch memory belongs to: one stream of one device.  A handle does not tell

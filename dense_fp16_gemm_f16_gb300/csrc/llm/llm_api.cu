@@ -321,7 +321,7 @@ gemm_status_t rmsnorm(int dtype, const void* X, const void* residual, const void
     if (X == nullptr) return GEMM_ERR_INVALID_VALUE;
     if (H % 8 != 0) return GEMM_ERR_MISALIGNED;
     if (!aligned16(X) || !aligned16(residual) || !aligned16(weight) || !aligned16(out->Y) || !aligned16(out->Y8) ||
-        !aligned16(out->scales) || !aligned16(out->total))
+        !aligned4(out->scales) || !aligned16(out->total))
         return GEMM_ERR_MISALIGNED;
     if (mul_sat(T, H) < 0) return GEMM_ERR_INVALID_VALUE;
     // Y and total may be X or the residual themselves (a row is read before it is
@@ -358,7 +358,7 @@ gemm_status_t check_lora(int dtype, const void* X, const gemm_lora_t* l, const i
         if (count > 0 && K > 0 && (l->A == nullptr || l->B == nullptr || ids == nullptr)) return GEMM_ERR_INVALID_VALUE;
     }
     if (K % 8 != 0 || N % 8 != 0 || R % 8 != 0) return GEMM_ERR_MISALIGNED;
-    if (!aligned16(X) || !aligned16(U) || !aligned16(ids) || !aligned16(l->A) || !aligned16(l->B) || !aligned16(l->factors))
+    if (!aligned16(X) || !aligned16(U) || !aligned4(ids) || !aligned16(l->A) || !aligned16(l->B) || !aligned4(l->factors))
         return GEMM_ERR_MISALIGNED;
     const int64_t out = mul_sat(M, N) < 0 ? -1 : M * N * 2;
     if (out < 0 || mul_sat(M, K) < 0) return GEMM_ERR_INVALID_VALUE;

@@ -2,14 +2,21 @@
 //   U[m] = beta C[m] + c_a (X[m] A_aᵀ) B_aᵀ,  a = ids[m].
 //
 // Rows are put in order of their adapters: up to 256 by every CTA for itself, so that one
-// kernel does everything, more by a kernel before (lora_list_kernel), which also cuts an adapter's
-// rows into units.  A cluster of eight (or four) CTAs takes one adapter's rows, or one unit: each CTA forms V = X Aᵀ over an eighth of K, the partial sums meet in
-// distributed shared memory in a fixed order, and each CTA multiplies V by an
-// eighth of B's rows.
-// Each byte meets few others (R is small): the operands go straight from global
-// memory to mma.sync fragments.  The k order within an MMA is free, so a thread's
-// 16 (or 8) consecutive bytes of a row are its slots of two steps (or one).
-// Bound by bytes: A and B of the adapters in use for a few rows, X, C and U for many.
+// kernel does everything, more by a kernel before (lora_list_kernel), which also cuts an
+// adapter's rows into units.  A cluster of eight or four CTAs takes one adapter's rows, or one
+// unit: each CTA forms V = X Aᵀ over its share of K, the partial sums meet in distributed shared
+// memory in a fixed order, and each CTA multiplies V by its share of B's rows.
+// Up to 16 rows beside a 16-bit projection, V alone is made (lora_v_kernel), while that
+// product already streams its weights, and the product's epilogue does the rest.
+//
+// What bounds it.  A few rows: bytes (A and B of the adapters in use) and a chain of
+// latencies; 250 rows, 62 adapters of rank 32 beside 5000 x 4104: 15.7 us for 39 MB, of
+// which 1.5 put the rows in order, 5 form V, 2 exchange it, 4 to 5 multiply it.  Many rows: X, C and U up
+// to rank 16 (4096 rows of 8192, runs of 8 adapters: 48 us for 140 MB: 14 us a unit for V, at
+// 5 TB/s, and 12 for U), the rate of mma.sync above (rank 64: 108 us; hi and lo below double the
+// second product).  Each byte meets few others in the first two cases, so the operands go to mma.sync by
+// way of copies that every thread makes for itself; the k order within an MMA is free, so a
+// thread's 16 (or 8) consecutive bytes of a row are its slots of two steps (or one).
 //
 // V is a sum in fp32.  For the second product it is cut into two numbers of the
 // operands' type, hi + lo (for fp16 after scaling each row by a power of two to about 1, so
@@ -218,7 +225,7 @@ __device__ void group_few_rows(const LoraParams& p, int rows, Groups& s) {
 
 // The list of up to kListRows rows, by one CTA: a table in shared memory counts the rows
 // of every adapter, the counts become places.  Which of an adapter's rows share a unit depends on
-// timing; the sums of a row do not depend on what shares its unit.  @LISTUS@
+// timing; the sums of a row do not depend on what shares its unit.  4 us for 300 rows, 5 for 4096.
 constexpr int kListThreads = 1024;
 constexpr int kListEach = kListRows / kListThreads;
 // Slots of the table: a power of two, twice the rows at least, one per thread at least.
@@ -319,11 +326,13 @@ __global__ void __launch_bounds__(kListThreads) lora_list_kernel(const LoraParam
 // Every thread copies the pieces of its own fragments to places of its own in shared
 // memory (cp.async), some steps ahead, and reads them back: many bytes under way without
 // registers for them, and nobody to wait for.
-// How a launch is built.  MT: 16-row tiles of ranks of the first product in hand, TILE: ranks
-// with many rows; SLOTS: 16-byte places per thread for its copies; S: steps of 16 ranks per chunk of the second
-// product, LONG: R has more than one chunk; AHEAD: chunks under way.  SLOTS and AHEAD leave
-// room for two CTAs per SM up to 32 ranks; with more, a CTA has enough to
-// copy to be alone (61 rows, 48 adapters of 64 x (4096 + 8192): @LONG@).
+//
+// How a launch is built.  MT: 16-row tiles of ranks of the first product in hand, TILE:
+// ranks in hand with many rows; SLOTS: 16-byte places per thread for its copies; S: steps of 16
+// ranks per chunk of the second product, LONG: R has more than one chunk; AHEAD: chunks
+// under way.  SLOTS and AHEAD leave room for two CTAs per SM up to 32 ranks; with more, a CTA has
+// enough to copy to be alone (61 rows, 48 adapters of rank 64 beside 4-bit 8192 x 4096, the whole
+// call: 36 -> 33 us).
 struct Ranks16 {
     static constexpr int MT = 1, TILE = 16, SLOTS = 18, WARPS = kLoraWarps, S = 1, AHEAD = 2;
     static constexpr bool LONG = false;
@@ -448,7 +457,7 @@ __device__ __forceinline__ void down_rows(const LoraParams& p, const T* A, int r
 // so often that they are copied once for the whole CTA, 64 k at a time, in 128-byte rows whose
 // 16-byte pieces are swapped by the row's number, and read by ldmatrix; 32 rows per warp, the steps
 // of 16 k dealt out to the warps of the same rows.  (The form above, where every warp copies the
-// ranks for itself, took @TILED@.)
+// ranks for itself, took 117 us where this takes 108: 4096 rows of 8192, rank 64.)
 template <class T, class Sh, int ROWS>
 __device__ __forceinline__ void down_tile(const LoraParams& p, const T* A, int r0, const int32_t* rows, int m, int s0, int s1,
                                           uint8_t* space, float* part) {
@@ -985,7 +994,8 @@ bool keep_smem(const void* kernel, int dev) {
 //  - Up to 256 rows, a batch of requests, make as many groups as adapters in use, taken
 //    to be chosen evenly.  While all clusters fit the GPU with one CTA per SM, they get one each
 //    (by asking for more than half of its shared memory): started while the kernel before
-//    drains, two would go to the SMs that are free first (@FIG@).
+//    drains, two would go to the SMs that are free first (61 rows, 48
+//    adapters of rank 64 beside 4-bit 8192 x 4096, the whole call: 39 -> 36 us).
 //  - More rows are cut into units of 32, 64 or 128 rows for clusters of four, two CTAs per SM
 //    up to 32 ranks: what takes the fewest rounds, each of the unit's rows and what a unit costs
 //    besides (some 24 rows' time).  Up to one unit per adapter is not full.

@@ -216,7 +216,8 @@ GEMM_API gemm_status_t gemm_nt_ex(gemm_dtype_t dtype, const void* A, const void*
  * gemm_nt_scaled -- gemm_nt_ex for 8-bit operands (GEMM_DTYPE_E4M3, GEMM_DTYPE_E5M2)
  * quantised with a scale per row of A, as gemm_rmsnorm (gemm_llm.h) leaves them:
  *     D = act(alpha * scale_m[m] * scale_n[n] * (A B^T) + beta * C + bias[n])
- *   scale_m  [M] fp32, device memory, 16-byte aligned, must not overlap D
+ *   scale_m  [M] fp32, device memory, 4-byte aligned (a slice of a batch's scales will
+ *            do), must not overlap D
  * Everything else as for gemm_nt_ex with GEMM_VARIANT_AUTO.  Errors: also
  * GEMM_ERR_INVALID_VALUE for a 16-bit dtype or a NULL scale_m with work to do.
  */

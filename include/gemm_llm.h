@@ -102,7 +102,8 @@ GEMM_API gemm_status_t gemm_w4_nt(gemm_dtype_t dtype, const void* A, const gemm_
  * What gemm_rmsnorm writes: Y, Y8 or both, and the sum.
  *   Y       [T][H] in the call's dtype, or NULL
  *   Y8      [T][H] in 8 bits, or NULL
- *   scales  [T] fp32, the scale of each row of Y8; NULL where `scale` is given
+ *   scales  [T] fp32, 4-byte aligned, the scale of each row of Y8; NULL where `scale`
+ *           is given
  *   total   [T][H] in the call's dtype: X + residual; NULL where it is not wanted
  *   dtype8  GEMM_DTYPE_E4M3 or GEMM_DTYPE_E5M2, the type of Y8
  *   scale   0 for a scale per row, else one positive scale for every row of Y8
@@ -138,7 +139,7 @@ GEMM_API gemm_status_t gemm_rmsnorm(gemm_dtype_t dtype, const void* X, const voi
 /*
  * A stack of `count` low-rank adapters of rank R beside an [N][K] projection.
  *   A [count][R][K] and B [count][N][R] in the call's dtype
- *   factors [count] fp32, or NULL for ones
+ *   factors [count] fp32, 4-byte aligned, or NULL for ones
  * R a multiple of 8 up to 256.  An adapter of a lower rank is stored with zeros.
  */
 typedef struct {
@@ -154,7 +155,7 @@ typedef struct {
  * their rows, each row with an adapter of its own:
  *     U[m] = beta * C[m] + factors[a] * (X[m] A_a^T) B_a^T,   a = ids[m]
  *   X [M][K], C and U [M][N] in dtype; C may be U itself and is not read with beta 0
- *   ids [M] int32, device memory; an id outside [0, count) leaves beta * C[m]
+ *   ids [M] int32, device memory, 4-byte aligned; an id outside [0, count) leaves beta * C[m]
  * Rows may come in any order; rows of one adapter share its reads, within 256 rows
  * (128 where M is larger).  X A^T is held in fp32 and enters the second product with
  * twice the precision of dtype, so U is rounded once.

@@ -209,6 +209,24 @@ def test_special_values_stay_in_their_rows_and_adapters():
     assert not bool(got[6].isfinite().any())
 
 
+@pytest.mark.parametrize("M", [12, 40])
+def test_special_values_beside_a_projection(M):
+    """Adapters that no row uses are not read; an infinity or NaN in a row of X stays in that row."""
+    N, K, R = 264, 512, 16
+    X, lora, ids, gen = draw(M, N, K, R, 4, torch.bfloat16, 13)
+    W = (torch.randn(N, K, generator=gen, device=DEV) * K ** -0.5).bfloat16()
+    ids[ids == 2] = -7
+    D, E = (torch.empty(M, N, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    g.gemm_lora_nt(X, W, lora, ids, D)
+    lora.A[2], lora.B[2], lora.factors[2] = float("nan"), float("inf"), float("nan")
+    X[1, 5], X[3, 7] = float("nan"), float("-inf")
+    g.gemm_lora_nt(X, W, lora, ids, E)
+    keep = torch.ones(M, dtype=torch.bool, device=DEV)
+    keep[1], keep[3] = False, False
+    assert torch.equal(D[keep], E[keep])
+    assert bool(E[1].isnan().all()) and not bool(E[3].isfinite().any())
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_large_and_small_inner_values(dtype):
     """X Aᵀ may lie far outside fp16's range: only U is a number of the type."""
@@ -232,6 +250,62 @@ def test_a_row_does_not_depend_on_its_place():
     p = torch.randperm(M, generator=gen, device=DEV)
     assert torch.equal(g.gemm_lora_delta(X[p], lora, ids[p]), want[p])
     assert torch.equal(g.gemm_lora_delta(X, lora, ids), want)
+
+
+@pytest.mark.parametrize("M,R", [(16, 32), (300, 16), (5000, 40)])
+def test_same_result_again(M, R):
+    """Which rows share a unit of work may change from run to run; results do not."""
+    X, lora, ids, _ = draw(M, 520, 1032, R, 7, torch.float16, M)
+    want = g.gemm_lora_delta(X, lora, ids)
+    for _ in range(10):
+        assert torch.equal(g.gemm_lora_delta(X, lora, ids), want)
+
+
+def test_two_host_threads_on_one_stream():
+    """Calls of two threads on one stream share its scratch and keep out of each other's way."""
+    import threading
+    N, K = 264, 520
+    stream = torch.cuda.Stream()
+    jobs = []
+    for i, M in enumerate((10, 400)):
+        X, lora, ids, gen = draw(M, N, K, 16, 5, torch.bfloat16, i)
+        W = (torch.randn(N, K, generator=gen, device=DEV) * K ** -0.5).bfloat16()
+        D = torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+        torch.cuda.synchronize()
+        g.gemm_lora_nt(X, W, lora, ids, D, stream=stream)
+        stream.synchronize()
+        jobs.append((X, W, lora, ids, D, D.clone()))
+    failed = []
+
+    def work(job):
+        X, W, lora, ids, D, want = job
+        for _ in range(40):
+            g.gemm_lora_nt(X, W, lora, ids, D, stream=stream)
+            stream.synchronize()
+            if not torch.equal(D, want):
+                failed.append(len(X))
+
+    threads = [threading.Thread(target=work, args=(j,)) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    g.gemm_f16_nt_check(device=DEV)
+
+
+def test_a_part_of_a_batch():
+    """Slices of a batch, whose ids begin anywhere, give the batch's rows."""
+    X, lora, ids, _ = draw(90, 264, 520, 16, 5, torch.bfloat16, 12)
+    ref, err = delta64(X, lora, ids)
+    for first, last in ((1, 12), (5, 90), (3, 40)):
+        got = g.gemm_lora_delta(X[first:last], lora, ids[first:last])
+        r = ref[first:last]
+        check(got, r, 1.01 * UNIT[torch.bfloat16] * r.abs() + err[first:last] + FLOOR)
+        W = torch.zeros(264, 520, dtype=torch.bfloat16, device=DEV)
+        D = torch.empty_like(got)
+        g.gemm_lora_nt(X[first:last], W, lora, ids[first:last], D)
+        check(D, r, 2.02 * UNIT[torch.bfloat16] * r.abs() + 2 * err[first:last] + FLOOR)
 
 
 def test_no_factors_no_adapters_and_empty():

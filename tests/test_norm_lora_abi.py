@@ -32,7 +32,7 @@ def test_norm_refusals(lib):
                 dict(Y=A + 64), dict(total=B + 64), dict(Y=C), dict(Y8=A), dict(Y8=B + 256), dict(scales=A), dict(scales=C),
                 dict(total=D), dict(total=D + 128), dict(Y8=D), dict(scales=E + 16), dict(scales=G), dict(Y=A, total=A)):
         assert call(**bad) == S.ERR_INVALID_VALUE, bad
-    for bad in (dict(H=60), dict(X=A + 8), dict(r=B + 2), dict(w=C + 8), dict(Y=D + 8), dict(Y8=E + 8), dict(scales=F + 4),
+    for bad in (dict(H=60), dict(X=A + 8), dict(r=B + 2), dict(w=C + 8), dict(Y=D + 8), dict(Y8=E + 8), dict(scales=F + 2),
                 dict(total=G + 2)):
         assert call(**bad) == S.ERR_MISALIGNED, bad
     for nothing in (dict(T=0), dict(H=0), dict(T=0, Y=None)):
@@ -45,7 +45,7 @@ def test_scaled_product_refusals(lib):
     for bad in (dict(dtype=0), dict(dtype=1), dict(dtype=4), dict(sm=0), dict(sm=D), dict(sm=D + 16), dict(M=-1), dict(a=0),
                 dict(b=0), dict(d=0), dict(d=A), dict(M=2 ** 31)):
         assert call(**bad) == S.ERR_INVALID_VALUE, bad
-    for bad in (dict(sm=B + 4), dict(K=72), dict(N=12), dict(a=A + 8)):
+    for bad in (dict(sm=B + 2), dict(K=72), dict(N=12), dict(a=A + 8)):
         assert call(**bad) == S.ERR_MISALIGNED, bad
     epi = g.Epilogue(1.0, 1.0, None, None, 0, 0, None)
     assert call(epi=ctypes.byref(epi)) == S.ERR_INVALID_VALUE   # beta without C
@@ -72,8 +72,8 @@ def test_adapter_refusals(lib):
                     dict(U=A), dict(U=B + 64), dict(U=C), dict(U=D), dict(U=E),
                     dict(l=_lora(count=2 ** 31 - 1, R=256), K=2 ** 30, N=8)):
             assert f(**bad) == S.ERR_INVALID_VALUE, bad
-        for bad in (dict(K=60), dict(N=12), dict(l=_lora(R=12)), dict(X=A + 8), dict(U=F + 8), dict(ids=E + 4),
-                    dict(l=_lora(a=B + 8)), dict(l=_lora(b=C + 2)), dict(l=_lora(f=D + 4))):
+        for bad in (dict(K=60), dict(N=12), dict(l=_lora(R=12)), dict(X=A + 8), dict(U=F + 8), dict(ids=E + 2),
+                    dict(l=_lora(a=B + 8)), dict(l=_lora(b=C + 2)), dict(l=_lora(f=D + 2))):
             assert f(**bad) == S.ERR_MISALIGNED, bad
         assert f(M=0, X=0, U=0, ids=0) == S.OK
         assert f(N=0, U=0) == S.OK

@@ -81,6 +81,14 @@ def test_zero_and_nan_scales_stay_in_their_rows():
         assert not bool(D[1].any()) and bool(D[2].isnan().all())
 
 
+def test_a_part_of_a_batch():
+    for first, last in ((1, 9), (3, 200)):
+        A, B, sm, sn, _ = draw(last, 264, 512, torch.float8_e4m3fn, last)
+        D = torch.empty(last - first, 264, dtype=torch.bfloat16, device=DEV)
+        g.gemm_nt_ex(A[first:], B, D, scale_m=sm[first:], scale_n=sn)
+        check(D, A[first:], B, sm[first:], sn)
+
+
 def test_empty_sum():
     A, B = (torch.empty(n, 0, dtype=torch.float8_e4m3fn, device=DEV) for n in (3, 16))
     D = torch.full((3, 16), 9.0, dtype=torch.bfloat16, device=DEV)
