@@ -31,6 +31,7 @@
 #include <cuda_fp16.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "config.h"
 #include "epilogue.cuh"
@@ -420,12 +421,12 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                 // ascending piece order
                 const uint32_t col = recv + static_cast<uint32_t>(n_local * MS * 4);
                 const uint32_t piece_bytes = static_cast<uint32_t>(128 * MS * 4);
-                auto finish = [&](int ml, float acc) {
+                auto finish = [&](int ml, float acc, auto many) {   // many: four rows or more per CTA
                     const int m = j * MS + ml;
                     if (m < p.M) {
                         if constexpr (LORA) acc = acc * scale_n + lora_out[ml * 128];
                         const float c = (ml & 1) ? Elem<T>::hi(c16[ml / 2]) : Elem<T>::lo(c16[ml / 2]);
-                        const float x = p.epi.on ? cf.apply(epi, acc, c) : acc;
+                        const float x = p.epi.on ? cf.template apply<decltype(many)::value>(epi, acc, c) : acc;
                         D[m * static_cast<int64_t>(p.N) + n] = Elem<T>::from_float(x);
                     }
                 };
@@ -441,7 +442,7 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                             for (int r = 0; r < 4; ++r) acc[r] += t[r];
                         }
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) finish(c + r, acc[r]);
+                        for (int r = 0; r < 4; ++r) finish(c + r, acc[r], std::true_type{});
                     }
                 } else {
                     float acc[2] = {0.0f, 0.0f};
@@ -451,8 +452,8 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                         acc[0] += t[0];
                         acc[1] += t[1];
                     }
-                    finish(0, acc[0]);
-                    finish(1, acc[1]);
+                    finish(0, acc[0], std::false_type{});
+                    finish(1, acc[1], std::false_type{});
                 }
             }
         }

@@ -355,24 +355,23 @@ __host__ __device__ constexpr int down_pitch(int MT) { return 16 * MT + 4; }
 template <class Sh>
 constexpr int kDownBytes = Sh::SLOTS * 16 * 32 * Sh::WARPS;
 
-// part = V of m <= 8 NT WR rows (`rows`) and 16 MT ranks from r0 on over the k steps
-// [s0, s1): WR parts of 8 NT rows, the steps of each dealt out to WARPS / WR warps.
-template <class T, class Sh, int MT, int NT, int WR>
+// part = V of m <= 8 NT rows (`rows`) and 16 MT ranks from r0 on over the k steps
+// [s0, s1), which are dealt out to the warps.
+template <class T, class Sh, int MT, int NT>
 __device__ __forceinline__ void down_rows(const LoraParams& p, const T* A, int r0, const int32_t* rows, int m, int s0, int s1,
                                           uint8_t* space, float* part) {
-    constexpr int W = Sh::WARPS, KW = W / WR, NF = 2 * MT + NT, D = Sh::SLOTS / NF, P = down_pitch(MT);
+    constexpr int W = Sh::WARPS, NF = 2 * MT + NT, D = Sh::SLOTS / NF, P = down_pitch(MT);
     constexpr int PLACE = 16 * 32 * W;
     static_assert(D >= 2, "a step ahead at least");
     static_assert(W * 8 * NT * P * 4 <= kDownBytes<Sh>, "the exchange fits the places");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int first = warp / KW * 8 * NT;   // this warp's rows
     const uint32_t places = ptx::smem_u32(space) + threadIdx.x * 16;   // f of stage d: (d * NF + f) * PLACE behind
     const T* a_ptr = A + static_cast<int64_t>(r0 + g) * p.K + 8 * t;
     const T* x_ptr[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-        const bool in = first + 8 * j + g < m;
-        x_ptr[j] = in ? static_cast<const T*>(p.X) + static_cast<int64_t>(rows[first + 8 * j + g]) * p.K + 8 * t : nullptr;
+        const bool in = 8 * j + g < m;
+        x_ptr[j] = in ? static_cast<const T*>(p.X) + static_cast<int64_t>(rows[8 * j + g]) * p.K + 8 * t : nullptr;
     }
     // copies of one step into stage d; what lies outside becomes zeros
     auto fetch = [&](int s, int d) {
@@ -397,41 +396,39 @@ __device__ __forceinline__ void down_rows(const LoraParams& p, const T* A, int r
         for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.0f;
-    if (first < m) {
-        int s = s0 + warp % KW;
+    int s = s0 + warp;
 #pragma unroll
-        for (int d = 0; d < D - 1; ++d) {
-            fetch(s + d * KW, d);
-            ptx::cp_async_commit();
-        }
-        int d = 0;
-        for (; s < s1; s += KW) {
-            ptx::cp_async_wait_group<D - 2>();   // this step's copies, by this thread, are done
-            uint32_t a[2 * MT][4], x[NT][4];
-            const uint32_t from = places + d * (NF * PLACE);
+    for (int d = 0; d < D - 1; ++d) {
+        fetch(s + d * W, d);
+        ptx::cp_async_commit();
+    }
+    int d = 0;
+    for (; s < s1; s += W) {
+        ptx::cp_async_wait_group<D - 2>();   // this step's copies, by this thread, are done
+        uint32_t a[2 * MT][4], x[NT][4];
+        const uint32_t from = places + d * (NF * PLACE);
 #pragma unroll
-            for (int i = 0; i < 2 * MT; ++i) ptx::ld_shared_v4_u32(from + i * PLACE, a[i]);
+        for (int i = 0; i < 2 * MT; ++i) ptx::ld_shared_v4_u32(from + i * PLACE, a[i]);
 #pragma unroll
-            for (int j = 0; j < NT; ++j) ptx::ld_shared_v4_u32(from + (2 * MT + j) * PLACE, x[j]);
-            const int back = d == 0 ? D - 1 : d - 1;   // the stage read in the step before
-            fetch(s + (D - 1) * KW, back);
-            ptx::cp_async_commit();
-            if (++d == D) d = 0;
+        for (int j = 0; j < NT; ++j) ptx::ld_shared_v4_u32(from + (2 * MT + j) * PLACE, x[j]);
+        const int back = d == 0 ? D - 1 : d - 1;   // the stage read in the step before
+        fetch(s + (D - 1) * W, back);
+        ptx::cp_async_commit();
+        if (++d == D) d = 0;
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                const uint32_t lo[4] = {a[2 * i][0], a[2 * i + 1][0], a[2 * i][1], a[2 * i + 1][1]};
-                const uint32_t hi[4] = {a[2 * i][2], a[2 * i + 1][2], a[2 * i][3], a[2 * i + 1][3]};
+        for (int i = 0; i < MT; ++i) {
+            const uint32_t lo[4] = {a[2 * i][0], a[2 * i + 1][0], a[2 * i][1], a[2 * i + 1][1]};
+            const uint32_t hi[4] = {a[2 * i][2], a[2 * i + 1][2], a[2 * i][3], a[2 * i + 1][3]};
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    ptx::mma16816<T>(acc[i][j], lo, x[j][0], x[j][1]);
-                    ptx::mma16816<T>(acc[i][j], hi, x[j][2], x[j][3]);
-                }
+            for (int j = 0; j < NT; ++j) {
+                ptx::mma16816<T>(acc[i][j], lo, x[j][0], x[j][1]);
+                ptx::mma16816<T>(acc[i][j], hi, x[j][2], x[j][3]);
             }
         }
-        ptx::cp_async_wait_group<0>();
     }
+    ptx::cp_async_wait_group<0>();
     __syncthreads();   // nobody's copies are under way
-    // the sums of a part's warps meet in shared memory and are added in their order
+    // the warps' sums meet in shared memory and are added in their order
     float* red = reinterpret_cast<float*>(space);
     float* mine = red + warp * 8 * NT * P;
 #pragma unroll
@@ -444,10 +441,10 @@ __device__ __forceinline__ void down_rows(const LoraParams& p, const T* A, int r
     for (int i = threadIdx.x; i < m * 16 * MT; i += 32 * W) {
         const int n = i / (16 * MT), r = i % (16 * MT);
         if (r0 + r >= p.R) continue;
-        const float* from = red + (n / (8 * NT) * KW * 8 * NT + n % (8 * NT)) * P + r;
+        const float* from = red + n * P + r;
         float v = 0.0f;
 #pragma unroll
-        for (int w = 0; w < KW; ++w) v += from[w * 8 * NT * P];
+        for (int w = 0; w < W; ++w) v += from[w * 8 * NT * P];
         part[n * p.R + r0 + r] = v;
     }
     __syncthreads();
@@ -572,9 +569,9 @@ __device__ __forceinline__ void down(const LoraParams& p, const T* A, const int3
         return;
     }
     for (int r0 = 0; r0 < p.R; r0 += 16 * Sh::MT) {
-        if (like <= 8) down_rows<T, Sh, Sh::MT, 1, 1>(p, A, r0, rows, m, s0, s1, space, part);
-        else if (like <= 16) down_rows<T, Sh, Sh::MT, 2, 1>(p, A, r0, rows, m, s0, s1, space, part);
-        else down_rows<T, Sh, Sh::MT, 4, 1>(p, A, r0, rows, m, s0, s1, space, part);
+        if (like <= 8) down_rows<T, Sh, Sh::MT, 1>(p, A, r0, rows, m, s0, s1, space, part);
+        else if (like <= 16) down_rows<T, Sh, Sh::MT, 2>(p, A, r0, rows, m, s0, s1, space, part);
+        else down_rows<T, Sh, Sh::MT, 4>(p, A, r0, rows, m, s0, s1, space, part);
     }
 }
 
@@ -965,8 +962,8 @@ __global__ void __launch_bounds__(kLoraOnlyThreads) lora_v_kernel(const LoraPara
         const int32_t* order = s.order + s.start[g];
         const T* A = static_cast<const T*>(p.A) + adapter * p.R * p.K;
         for (int r0 = 0; r0 < p.R; r0 += 16) {
-            if (m <= 8) down_rows<T, RanksOnlyV, 1, 1, 1>(p, A, r0, order, m, s0, s1, space, part);
-            else down_rows<T, RanksOnlyV, 1, 2, 1>(p, A, r0, order, m, s0, s1, space, part);
+            if (m <= 8) down_rows<T, RanksOnlyV, 1, 1>(p, A, r0, order, m, s0, s1, space, part);
+            else down_rows<T, RanksOnlyV, 1, 2>(p, A, r0, order, m, s0, s1, space, part);
         }
         ptx::cluster_sync();   // every CTA's partial sums are there
         give_rows(p, m, factor, ptx::smem_u32(part), rank, order);

@@ -474,7 +474,7 @@ w4_tiles_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
 #pragma unroll
             for (int q2 = 0; q2 < 4; ++q2) {
                 if (m + q2 < p.M) {
-                    if (p.epi.on) x[q2] = cf.apply(p.epi, x[q2], c4[q2]);
+                    if (p.epi.on) x[q2] = cf.template apply<true, true>(p.epi, x[q2], c4[q2]);
                     D[(m + q2) * p.N + n] = Elem<T>::from_float(x[q2]);
                 }
             }

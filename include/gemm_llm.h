@@ -127,7 +127,8 @@ typedef struct {
  * y is taken from h before its rounding and Y8 from y before its own.  A row whose
  * y is all zero has scale 0 and codes 0.  A row that holds an infinity or NaN, or
  * whose squares or products with the weight pass fp32's largest number, has
- * NaN or zeros in Y as the formula gives them and unspecified scale and codes.
+ * NaN or zeros in Y as the formula gives them and unspecified scale and codes.  With eps 0,
+ * squares below fp32's smallest number count as zero.
  * X, residual, Y, total [T][H] and weight [H] in dtype; H a multiple of 8; eps >= 0.
  * Y and total may each be X or residual itself; outputs overlap nothing else.
  * T or H of zero is a no-op.  The 8-bit rows and their scales are what
@@ -156,12 +157,14 @@ typedef struct {
  *     U[m] = beta * C[m] + factors[a] * (X[m] A_a^T) B_a^T,   a = ids[m]
  *   X [M][K], C and U [M][N] in dtype; C may be U itself and is not read with beta 0
  *   ids [M] int32, device memory, 4-byte aligned; an id outside [0, count) leaves beta * C[m]
- * Rows may come in any order; rows of one adapter share its reads, within 256 rows
- * (128 where M is larger).  X A^T is held in fp32 and enters the second product with
- * twice the precision of dtype, so U is rounded once.
+ * Rows may come in any order; rows of one adapter share its reads: all of them up to 256
+ * rows, up to 32, 64 or 128 of them where M is larger.  X A^T is held in fp32 and enters the
+ * second product with twice the precision of dtype (an infinity in B may give NaN for it), so
+ * U is rounded once.  A row's result does not depend on the other rows' values or
+ * order; in its last bit it may depend on how many rows its adapter has in the call.
  * U is what any product of the library takes as C with beta = 1: gemm_nt_scaled for
  * 8-bit operands, or gemm_lora_nt in one call.  K and N multiples of 8.  M or N of zero
- * is a no-op.  Uses the stream's scratch memory.
+ * is a no-op.  More than 256 rows use the stream's scratch memory.
  */
 GEMM_API gemm_status_t gemm_lora_delta(gemm_dtype_t dtype, const void* X, const gemm_lora_t* lora, const int32_t* ids,
                                        float beta, const void* C, void* U, int64_t M, int64_t N, int64_t K,
@@ -171,11 +174,14 @@ GEMM_API gemm_status_t gemm_lora_delta(gemm_dtype_t dtype, const void* X, const 
  * gemm_lora_nt -- a projection shared by many requests, with their adapters:
  *     D[m] = act(alpha * scale_n[n] * X[m] W^T + factors[a] * (X[m] A_a^T) B_a^T + beta * C[m] + bias)
  * W [N][K] 16-bit or 4-bit weights; the rest as for gemm_lora_delta and the
- * epilogue of gemm_nt_ex (NULL: none).  D may be C itself.  beta * C and the adapters'
- * part are summed in fp32 and rounded to dtype once before the projection's sum in fp32
- * joins them and D is rounded: an error of at most half a unit in the last place of
- * each.  Rows without an adapter whose beta * C is a number of dtype (beta 0 or 1) get the
- * plain product's D.  count == 0: the plain product.
+ * epilogue of gemm_nt_ex (NULL: none).  D may be C itself.
+ * 16-bit W, M up to 16 and M * R up to 1024: everything is summed in fp32 and D is rounded
+ * once.  Else beta * C and the adapters' part are summed in fp32 and rounded to dtype (beyond
+ * fp16's largest number: to infinity) before the projection's sum in fp32 joins them and D is
+ * rounded: an error of at most half a unit in the last place of each.
+ * Rows without an adapter get the plain product's D where beta is 0 or 1 (with other betas, and
+ * with up to 16 rows where an epilogue is given, up to those roundings); count == 0: the plain
+ * product.  Uses the stream's scratch memory (up to 16 rows beside 16-bit W, above 256 rows).
  */
 GEMM_API gemm_status_t gemm_lora_nt(gemm_dtype_t dtype, const void* X, const gemm_weights_t* W, const gemm_lora_t* lora,
                                     const int32_t* ids, void* D, int64_t M, int64_t N, int64_t K,

@@ -308,6 +308,54 @@ def test_a_part_of_a_batch():
         check(D, r, 2.02 * UNIT[torch.bfloat16] * r.abs() + 2 * err[first:last] + FLOOR)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,H,I,R", [(1, 2048, 1024, 16), (7, 1024, 520, 64), (16, 8192, 1032, 24), (40, 1024, 2048, 16),
+                                     (300, 1024, 520, 32)])
+def test_layers_without_a_pause(M, H, I, R, dtype):
+    """Norms and products that start while the one before them drains, over the same few buffers: the same as with
+    a synchronisation after every call, and in a graph."""
+    X, up, ids, gen = draw(M, I, H, R, 5, dtype, M + H)
+    _, down, _, _ = draw(1, H, I, R, 5, dtype, M + I)
+    W1, W2 = ((torch.randn(s, generator=gen, device=DEV) * s[1] ** -0.5).to(dtype) for s in ((I, H), (H, I)))
+    w = (torch.rand(H, generator=gen, device=DEV) + 0.5).to(dtype)
+    x, y, h = torch.empty_like(X), torch.empty_like(X), torch.empty(M, I, dtype=dtype, device=DEV)
+
+    def layers(between):
+        x.copy_(X)
+        for i in range(6):
+            g.gemm_rmsnorm(x, w, Y=y)
+            between()
+            g.gemm_lora_nt(y, W1, up, ids, h, activation=g.Activation.RELU)
+            between()
+            g.gemm_lora_nt(h, W2, down, ids, x, beta=1.0, C=x)
+            between()
+            if i % 2:
+                g.gemm_lora_nt(y, W1, up, ids, h)      # the same buffers with nothing in between
+                g.gemm_lora_nt(h, W2, down, ids, y)
+                between()
+                x.add_(y)
+                between()
+
+    layers(torch.cuda.synchronize)
+    want = x.clone()
+    assert bool(want.isfinite().all())
+    for _ in range(5):
+        layers(lambda: None)
+        assert torch.equal(x, want)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        layers(lambda: None)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            layers(lambda: None)
+        for _ in range(5):
+            graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(x, want)
+    g.gemm_f16_nt_check(device=DEV)
+
+
 def test_no_factors_no_adapters_and_empty():
     X, lora, ids, gen = draw(6, 64, 128, 8, 3, torch.float16, 5)
     one = g.Lora(lora.A, lora.B)

@@ -92,7 +92,7 @@ def test_given_scale_saturates(scale):
     check(g.gemm_rmsnorm(x, w, r, Y8=g.Dtype.E4M3, scale=scale), x, r, w, 1e-6, 512)
 
 
-@pytest.mark.parametrize("T,H", [(3, 640), (400, 8192), (2, 40000)])
+@pytest.mark.parametrize("T,H", [(3, 640), (400, 8192), (2, 40000), (2000, 4104), (20001, 72), (700, 16384), (2000, 11000)])
 def test_in_place(T, H):
     """total over the residual and Y over X, or the other way round, change nothing."""
     x, r, w = draw(T, H, torch.bfloat16, 11)
