@@ -3,7 +3,7 @@
 //
 // Rows are put in order of their adapters: up to 256 by every CTA for itself, so that one
 // kernel does everything, more by a kernel before (lora_list_kernel), which also cuts an
-// adapter's rows into units.  A cluster of eight or four CTAs takes one adapter's rows, or one
+// adapter's rows into units.  A cluster of up to eight CTAs takes one adapter's rows, or one
 // unit: each CTA forms V = X Aᵀ over its share of K, the partial sums meet in distributed shared
 // memory in a fixed order, and each CTA multiplies V by its share of B's rows.
 // Up to 16 rows beside a 16-bit projection, V alone is made (lora_v_kernel), while that
@@ -871,7 +871,14 @@ __host__ __device__ constexpr int lora_space_bytes(int R, int rows) {
     return ((v > e ? v : e) + 127) / 128 * 128;
 }
 
-// Grid: clusters, which take groups (or units of the list) in turn.
+// Clusters that share a unit's columns at most.
+constexpr int kLoraMaxShare = 8;
+
+// Grid: clusters, which take groups (or units of the list) in turn.  Where the last round leaves
+// two clusters or more per unit, they share its columns, each forming V for itself (61 rows
+// beside 4-bit 8192 x 4096, rank 64, the whole call: 3 adapters in use 39 -> 29 us, 8 31.5 -> 28,
+// 38, two more than the GPU holds at one time, 45 -> 40; where nothing is left to share, 0.2 to 0.7 us
+// more.  As code of its own behind the loop: 30.5, 28.3, 46 and 0 to 0.4).
 template <class T, class Sh>
 __global__ void __launch_bounds__(kLoraThreads, Sh::LONG ? 1 : 2) lora_kernel(const LoraParams p) {
     extern __shared__ __align__(16) uint8_t smem[];
@@ -891,12 +898,28 @@ __global__ void __launch_bounds__(kLoraThreads, Sh::LONG ? 1 : 2) lora_kernel(co
         else group_rows(p, p.M, s, *reinterpret_cast<GroupTable*>(space));
         groups = s.n;
     }
-    const int64_t n0 = static_cast<int64_t>(rank) * p.width;
-    const int columns = static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(p.width), p.N - n0)));
     const int s0 = static_cast<int>(static_cast<int64_t>(p.k_steps) * rank / p.cluster);
     const int s1 = static_cast<int>(static_cast<int64_t>(p.k_steps) * (rank + 1) / p.cluster);
-    const int most = p.most_rows;
-    for (int g = blockIdx.x / p.cluster; g < groups; g += gridDim.x / p.cluster) {
+    const int most = p.most_rows, clusters = static_cast<int>(ptx::cluster_count());
+    // turns: one per unit, or several for each of the last round's; the divisions for these are kept
+    // out of the others' way
+    int turns = groups;
+    if (const int left = groups < clusters ? groups : groups % clusters; left > 0 && 2 * left <= clusters)
+        turns += left * (min(clusters / left, kLoraMaxShare) - 1);
+    for (int turn = static_cast<int>(ptx::cluster_id()); turn < turns; turn += clusters) {
+        int g = turn, from = 0, width = p.width;   // `width` of this CTA's columns, from `from` on
+        if (turns > groups) {
+            const int whole = groups - groups % clusters;
+            if (turn >= whole) {
+                const int share = (turns - whole) / (groups - whole);
+                width = (p.width / kLoraColumns + share - 1) / share * kLoraColumns;
+                g = whole + (turn - whole) / share;
+                from = (turn - whole) % share * width;
+                width = min(width, p.width - from);
+            }
+        }
+        const int64_t n0 = static_cast<int64_t>(rank) * p.width + from;
+        const int columns = static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(width), p.N - n0)));
         int64_t adapter;
         int begin, end;
         if (p.list != nullptr) {
@@ -955,7 +978,7 @@ __global__ void __launch_bounds__(kLoraOnlyThreads) lora_v_kernel(const LoraPara
     group_few_rows(p, p.M, s);
     const int s0 = static_cast<int>(static_cast<int64_t>(p.k_steps) * rank / p.cluster);
     const int s1 = static_cast<int>(static_cast<int64_t>(p.k_steps) * (rank + 1) / p.cluster);
-    for (int g = blockIdx.x / p.cluster; g < s.n; g += gridDim.x / p.cluster) {
+    for (int g = static_cast<int>(ptx::cluster_id()); g < s.n; g += static_cast<int>(ptx::cluster_count())) {
         const int64_t adapter = s.adapter[g];
         const float factor = p.factors != nullptr ? p.factors[adapter] : 1.0f;
         const int m = s.start[g + 1] - s.start[g];
@@ -987,49 +1010,103 @@ bool keep_smem(const void* kernel, int dev) {
     return ready;
 }
 
+// Clusters of 1 .. kLoraMaxCluster CTAs that run at one time.
+struct Slots {
+    int of[kLoraMaxCluster + 1];
+};
+Slots cluster_slots(const void* kernel, const DeviceView& dev, int smem) {
+    static std::mutex mu;
+    static std::map<LaunchKey, Slots> known;
+    std::lock_guard<std::mutex> lock(mu);
+    const LaunchKey key{kernel, dev.dev, smem, 0};
+    const auto at = known.find(key);
+    if (at != known.end()) return at->second;
+    Slots s{};
+    for (int c = 1; c <= kLoraMaxCluster; ++c) s.of[c] = std::max(1, active_clusters(kernel, dev, kLoraThreads, smem, c));
+    return known[key] = s;
+}
+
+// Work of a launch, as far as the host knows: `units` pieces, within about `spread`, of `rows` rows.
+struct Work {
+    double units, spread, rows;
+};
+
+// How it is shared out: clusters of which size, and with a list units of how many rows.  A
+// unit takes 8 us and what its CTAs share, 24 us and one more per row (at 8192 x 4096, rank
+// 64; other sizes scale all three), once for every round of units that the GPU cannot hold at
+// one time.  Adapters are taken to be chosen evenly, from all or from half of them.
+// Measured, adapters alone in a graph:
+//   61 rows, rank 64, clusters of 8, 6, 4, 3, 2: 16 adapters in use 17.8, 12.3, 14.6, 17.1, 21.8 us
+//   (the GPU holds 15, 23, 36, 46, 76 of them), 36 adapters 28.7, 24.0, 17.2, 19.1, 23.4, 40 adapters
+//   29.2, 24.4, 28.6, 19.4, 23.5;  4096 rows of 30 adapters, 4096 x 1024, rank 128, units of 64
+//   rows, clusters of 4, 2, 1: 78, 64, 100;  four of rank 256, units of 32: 204, 166, 155.
+//   Five and seven gain nothing on their neighbours (rank 16: 9.6 us with five, 8.3 with four).
+struct Share {
+    int cluster = 0, rows = 0;
+    double cost = 0.0;
+};
+void weigh(Share& best, const Slots& slots, const Work (&work)[2], int unit_rows) {
+    for (int c : {8, 6, 4, 3, 2, 1}) {
+        const double s = slots.of[c];
+        double cost = 0.0;
+        for (const Work& w : work) {
+            const double rounds = 0.5 * std::ceil(w.units / s) + 0.25 * std::ceil(std::max(w.units - w.spread, 1.0) / s) +
+                                  0.25 * std::ceil((w.units + w.spread) / s);
+            cost += rounds * (8.0 + (24.0 + w.rows) / c);
+        }
+        if (best.cluster == 0 || cost < best.cost) best = Share{c, unit_rows, cost};
+    }
+}
+
 // Fills the split of `p` and launches.
-//  - Up to 256 rows, a batch of requests, make as many groups as adapters in use, taken
-//    to be chosen evenly.  While all clusters fit the GPU with one CTA per SM, they get one each
-//    (by asking for more than half of its shared memory): started while the kernel before
-//    drains, two would go to the SMs that are free first (61 rows, 48
-//    adapters of rank 64 beside 4-bit 8192 x 4096, the whole call: 39 -> 36 us).
-//  - More rows are cut into units of 32, 64 or 128 rows for clusters of four, two CTAs per SM
-//    up to 32 ranks: what takes the fewest rounds, each of the unit's rows and what a unit costs
-//    besides (some 24 rows' time).  Up to one unit per adapter is not full.
+//  - Up to 256 rows, a batch of requests, make as many groups as adapters are in use.  Where
+//    all clusters fit the GPU with one CTA per SM, they get one each (by asking for
+//    more than half of its shared memory): started while the kernel before drains, two would go
+//    to the SMs that are free first (61 rows, 48 adapters of rank 64 beside 4-bit
+//    8192 x 4096, the whole call: 39 -> 36 us).
+//  - More rows are cut into units of 32, 64 or 128 rows; an adapter's last one is half full.
 template <class T, class Sh>
 gemm_status_t launch(LoraParams p, const DeviceView& dev, cudaStream_t s) {
     const auto kernel = lora_kernel<T, Sh>;
     p.most_rows = up_rows(p.R);
     int smem = kGroupsBytes + lora_space_bytes<Sh>(p.R, p.most_rows) + kUpBytes<Sh> + p.most_rows * p.R * 4;
-    auto at_once = [&](int cluster, int bytes) {
-        return std::max(1, active_clusters(reinterpret_cast<const void*>(kernel), dev, kLoraThreads, bytes, cluster));
-    };
-    int clusters = 1;
+    const Slots slots = cluster_slots(reinterpret_cast<const void*>(kernel), dev, smem);
+    const double M = p.M, all = std::max(1, p.count), half = std::max(1.0, all / 2);
+    Share share;
+    int clusters;
     if (p.list == nullptr) {
-        const double count = std::max(1, p.count);
-        const double groups = std::max(1.0, count * (1.0 - std::pow(1.0 - 1.0 / count, static_cast<double>(p.M))));
+        auto groups = [&](double count) {   // adapters in use, their standard deviation
+            const double empty = std::exp(-M / count), n = std::max(1.0, count * (1.0 - std::pow(1.0 - 1.0 / count, M)));
+            return Work{n, 1.2 * std::sqrt(std::max(0.0, count * empty * (1.0 - (1.0 + M / count) * empty))), M / n};
+        };
+        const Work work[2] = {groups(all), groups(half)};
+        weigh(share, slots, work, 0);
         const int alone = std::max(smem, kMaxDynamicSmem / 2 + 2048);
-        p.cluster = groups <= at_once(8, alone) ? 8 : 4;
-        if (groups <= at_once(p.cluster, alone)) smem = alone;
-        clusters = std::min(at_once(p.cluster, smem), static_cast<int>(std::min<int64_t>(p.M, int64_t{p.count} + 1)));
-    } else {
-        p.cluster = 4;
-        clusters = at_once(p.cluster, smem);
-        double best = 0.0;
-        for (int rows = 32; rows <= p.most_rows; rows *= 2) {
-            const double whole = static_cast<double>(p.M) / rows;
-            const double units = whole + std::min(static_cast<double>(p.count), std::max(whole, static_cast<double>(clusters)));
-            const double t = std::ceil(units / clusters) * (rows + 24);
-            if (best == 0.0 || t < best) {
-                best = t;
-                p.unit_rows = rows;
-            }
+        const Slots slots_alone = cluster_slots(reinterpret_cast<const void*>(kernel), dev, alone);
+        clusters = slots.of[share.cluster];
+        if (work[0].units <= slots_alone.of[share.cluster]) {
+            smem = alone;
+            clusters = slots_alone.of[share.cluster];
         }
+        // one CTA per SM; more only where there may be as many groups
+        const int most = static_cast<int>(std::min<int64_t>(p.M, std::max(1, p.count)));
+        clusters = std::min(clusters, std::max(most, dev.sms / share.cluster));
+    } else {
+        for (int rows = 32; rows <= p.most_rows; rows *= 2) {
+            auto units = [&](double count) {
+                const double used = count * (1.0 - std::exp(-M / count));
+                return Work{used * std::max(1.0, M / count / rows + 0.5), 0.6 * std::sqrt(used), static_cast<double>(rows)};
+            };
+            weigh(share, slots, {units(all), units(half)}, rows);
+        }
+        p.unit_rows = share.rows;
+        clusters = slots.of[share.cluster];
         const int bits = list_bits(p.M);
         const gemm_status_t st = launch_clusters(lora_list_kernel, dev.dev, dim3(1, 1, 1), kListThreads, 1,
                                                  (2 << bits) * 4 + 16, true, s, p, const_cast<LoraList*>(p.list), bits);
         if (st != GEMM_OK) return st;
     }
+    p.cluster = share.cluster;
     const int64_t per = p.cluster * kLoraColumns;
     p.width = static_cast<int32_t>((p.N + per - 1) / per * kLoraColumns);
     return launch_clusters(kernel, dev.dev, dim3(static_cast<unsigned>(clusters * p.cluster), 1, 1), kLoraThreads, p.cluster,
