@@ -13,7 +13,7 @@
 // latencies; 250 rows, 62 adapters of rank 32 beside 5000 x 4104: 15.7 us for 39 MB, of
 // which 1.5 put the rows in order, 5 form V, 2 exchange it, 4 to 5 multiply it.  Many rows: X, C and U up
 // to rank 16 (4096 rows of 8192, runs of 8 adapters: 48 us for 140 MB: 14 us a unit for V, at
-// 5 TB/s, and 12 for U), the rate of mma.sync above (rank 64: 108 us; hi and lo below double the
+// 5 TB/s, and 12 for U), the rate of mma.sync above (rank 64: 82 us; hi and lo below double the
 // second product).  Each byte meets few others in the first two cases, so the operands go to mma.sync by
 // way of copies that every thread makes for itself; the k order within an MMA is free, so a
 // thread's 16 (or 8) consecutive bytes of a row are its slots of two steps (or one).

@@ -161,7 +161,7 @@ typedef struct {
  * rows, up to 32, 64 or 128 of them where M is larger.  X A^T is held in fp32 and enters the
  * second product with twice the precision of dtype (an infinity in B may give NaN for it), so
  * U is rounded once.  A row's result does not depend on the other rows' values or
- * order; in its last bit it may depend on how many rows its adapter has in the call.
+ * order; in its last bit it may depend on how many rows its adapter and the call have.
  * U is what any product of the library takes as C with beta = 1: gemm_nt_scaled for
  * 8-bit operands, or gemm_lora_nt in one call.  K and N multiples of 8.  M or N of zero
  * is a no-op.  More than 256 rows use the stream's scratch memory.
