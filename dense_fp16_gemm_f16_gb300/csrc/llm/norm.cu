@@ -113,10 +113,13 @@ __device__ __forceinline__ RowFactors row_factors(const NormParams& p, float sum
     return f;
 }
 
-// The quotient y / scale from its reciprocal, put right by its remainder.
+// The quotient y / scale from its reciprocal, put right by its remainder.  A given scale may be so
+// small that it passes fp32's numbers: rounded towards zero it is the largest of them and not
+// infinite, so that it has a remainder, and becomes the largest code.  (A comparison that leaves out the
+// remainder there cost 0.45 us of 39.4 at 4096 x 8192, limits on y or q up to 1.4.)
 __device__ __forceinline__ float divided(float y, const RowFactors& f) {
-    y *= f.lift;
-    const float q = y * f.inv;
+    y = __fmul_rz(y, f.lift);
+    const float q = __fmul_rz(y, f.inv);
     return fmaf(fmaf(-q, f.scale, y), f.inv, q);
 }
 

@@ -186,3 +186,26 @@ def test_refusals():
             g.gemm_rmsnorm(**args)
     with pytest.raises(g.GemmError):
         g.gemm_rmsnorm(torch.empty(4, 60, dtype=torch.float16, device=DEV))
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("T,H", [(3, 512), (2, 40000), (700, 8192)])
+def test_given_scales_of_any_size(T, H, dtype):
+    """A quotient y / scale beyond fp32's numbers gives the largest code, not NaN: scales down to fp32's smallest
+    number, which is not a normal one."""
+    x, r, w = draw(T, H, dtype, 4)
+    for kind in (g.Dtype.E4M3, g.Dtype.E5M2):
+        for scale in (2.0 ** -149, 1e-38, 2.0 ** -101, 2.0 ** -99, 1e-30, 1e5, 3e38):
+            check.scale = float(torch.tensor(scale))
+            out = g.gemm_rmsnorm(x, w, r, Y8=kind, scale=scale)
+            assert not bool(out.Y8.float().isnan().any())
+            check(out, x, r, w, 1e-6, H)
+
+
+def test_given_scale_below_large_rows():
+    """y near fp32's largest number over a scale of ordinary size."""
+    x, r, _ = draw(5, 1024, torch.bfloat16, 14)
+    w = torch.full((1024,), 2.0 ** 124, device=DEV, dtype=torch.bfloat16)
+    for scale in (0.0078125, 2.0 ** -110):
+        check.scale = scale
+        check(g.gemm_rmsnorm(x, w, r, Y8=g.Dtype.E4M3, scale=scale), x, r, w, 1e-6, 1024)
