@@ -65,3 +65,30 @@ def test_more_rows_than_one_list():
     X, lora, ids, _ = lo.draw(M, N, K, R, 900, torch.float16, 4)
     ref, err = lo.delta64(X, lora, ids)
     lo.check(g.gemm_lora_delta(X, lora, ids), ref, 1.01 * 2.0 ** -11 * ref.abs() + err + 2.0 ** -25)
+
+
+def test_sum_of_a_long_row_of_one_value():
+    """Equal numbers make every rounding of a long sum fall to the same side.  y is 1.  The sum may be off by eight
+    roundings of 2^-24 in a piece, two of the pieces' sum and ten between threads, whatever the row's length; the root
+    halves that, and the division by H, eps, the root and the product leave four more at most: 14 for y, 15 for the scale."""
+    for H in (1 << 24, (1 << 27) + 8):
+        for k in (2, 6, 14):
+            x = torch.full((2, H), 1.0 + k * 2.0 ** -10, device=DEV, dtype=torch.float16)
+            total = torch.empty_like(x)
+            out = g.gemm_rmsnorm(x, eps=0.0, Y=torch.empty_like(x), Y8=g.Dtype.E4M3, total=total)
+            assert bool(((out.Y.double() - 1.0).abs() <= 1.01 * 2.0 ** -11 + 14 * 2.0 ** -24).all())
+            assert bool(((out.scales.double() * 448.0 - 1.0).abs() <= 15 * 2.0 ** -24).all())
+            assert torch.equal(total, x) and bool((out.Y8.float() == 448.0).all())
+            del out, total
+
+
+def test_long_rows_of_special_values():
+    """A sum of squares beyond fp32's numbers is infinite and its row zero, as in short rows."""
+    H = 40000
+    x = torch.ones(4, H, device=DEV, dtype=torch.bfloat16)
+    x[0] = 2.0 ** 60                    # the sum of one thread's squares is infinite half way
+    x[1, 5], x[2, 39999] = float("inf"), float("nan")
+    Y = g.gemm_rmsnorm(x).Y
+    assert not bool(Y[0].any())
+    assert bool(Y[1, 5].isnan()) and int(Y[1].count_nonzero()) == 1
+    assert bool(Y[2].isnan().all()) and bool((Y[3] == 1.0).all())
