@@ -44,6 +44,7 @@ struct LoraEpi {
     const float* V;       // [M][R], 16-byte aligned; not used where ids[m] is outside [0, count)
     const void* B;        // [count][N][R] in D's type
     const int32_t* ids;   // [M]
+    uint32_t* ready;      // not zero: what is ahead of the kernel that makes V has ended.  Left at zero
     int32_t R, count;     // R % 8 == 0
 };
 // Rows, and M * R, of one launch at most.  The part is summed on the epilogue's warps

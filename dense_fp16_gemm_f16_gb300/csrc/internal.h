@@ -61,6 +61,7 @@ gemm_status_t stream_key(int dev, gemm_stream_t stream, StreamKey* out);   // ap
 // other threads' calls on the pair waiting for as long as it lives: until the call's
 // last launch.
 constexpr int kScratchCounters = 1024;
+constexpr int kCounterLora = 32;   // of the adapters' small calls; the first is the router's
 struct Scratch {
     uint8_t* data = nullptr;
     uint32_t* counters = nullptr;

@@ -78,6 +78,7 @@ struct LoraArgs {
     float beta;
     void* U;               // may be C
     float* V;              // [M][R], M <= kLoraEpiRows: c_a X A_aT is all that is wanted; else nullptr
+    uint32_t* ready;       // with V: set as soon as all before has ended (LoraEpi)
     int64_t M, N, K, R, count;
 };
 constexpr int kLoraMaxRank = 256;

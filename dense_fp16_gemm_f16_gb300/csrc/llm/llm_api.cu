@@ -367,7 +367,7 @@ gemm_status_t check_lora(int dtype, const void* X, const gemm_lora_t* l, const i
         (l->factors != nullptr && ranges_overlap(U, out, l->factors, count * 4)) ||
         (ids != nullptr && ranges_overlap(U, out, ids, M * 4)))
         return GEMM_ERR_INVALID_VALUE;
-    *a = LoraArgs{X, l->A, l->B, l->factors, ids, nullptr, 0.0f, nullptr, nullptr, M, N, K, R, count};
+    *a = LoraArgs{X, l->A, l->B, l->factors, ids, nullptr, 0.0f, nullptr, nullptr, nullptr, M, N, K, R, count};
     return GEMM_OK;
 }
 
@@ -423,10 +423,13 @@ gemm_status_t lora_nt(int dtype, const void* X, const gemm_weights_t* weights, c
         st = get_scratch(dev.dev, stream, static_cast<size_t>(M * a.R * 4), &ws);
         if (st != GEMM_OK) return st;
         a.V = reinterpret_cast<float*>(ws.data);
+        a.ready = ws.counters + kCounterLora;
         st = run_lora(dtype == GEMM_DTYPE_BF16, a, nullptr, dev, reinterpret_cast<cudaStream_t>(stream));
         if (st != GEMM_OK) return st;
-        const LoraEpi part{a.V, l->B, ids, static_cast<int32_t>(a.R), static_cast<int32_t>(a.count)};
-        return run_dense(dtype, X, w.data, D, M, N, K, epilogue, &part, stream);
+        const LoraEpi part{a.V, l->B, ids, a.ready, static_cast<int32_t>(a.R), static_cast<int32_t>(a.count)};
+        st = run_dense(dtype, X, w.data, D, M, N, K, epilogue, &part, stream);
+        if (st != GEMM_OK) cudaMemsetAsync(a.ready, 0, sizeof(uint32_t), reinterpret_cast<cudaStream_t>(stream));   // nobody took it back
+        return st;
     }
     a.C = epi.beta != 0.0f ? epi.C : nullptr;
     a.beta = epi.beta;

@@ -53,6 +53,7 @@ struct LoraParams {
     const void* C;           // [M][N] or nullptr
     void* U;                 // [M][N]
     float* V;                // [M][R]: factors X Aᵀ is all that is wanted, or nullptr
+    uint32_t* ready;         // with V: for the product behind, which starts early
     int32_t M, N, K, R, count;
     int32_t k_steps, width;  // width: columns per CTA of a cluster
     int32_t unit_rows;       // with a list: most rows of a unit, 32, 64 or 128
@@ -975,7 +976,10 @@ __global__ void __launch_bounds__(kLoraOnlyThreads) lora_v_kernel(const LoraPara
     uint8_t* space = smem + kGroupsBytes;
     float* part = reinterpret_cast<float*>(space + kDownBytes<RanksOnlyV>);
     ptx::griddep_wait();
-    // only now: the product that starts early relies on everything before this kernel
+    // only now: the product that starts early reads what is written before this kernel, and finds the
+    // flag that says so
+    if (blockIdx.x == 0 && threadIdx.x == 0) ptx::st_release_gpu(p.ready, 1u);
+    __syncthreads();
     ptx::griddep_launch_dependents();
     const int rank = static_cast<int>(ptx::cluster_ctarank());
     group_few_rows(p, p.M, s);
@@ -1153,6 +1157,7 @@ gemm_status_t run_lora(bool bf16, const LoraArgs& a, uint8_t* data, const Device
         p.C = a.C != nullptr ? static_cast<const uint16_t*>(a.C) + m0 * a.N : nullptr;
         p.U = static_cast<uint16_t*>(a.U) + m0 * a.N;
         p.V = a.V;
+        p.ready = a.ready;
         p.M = static_cast<int32_t>(M);
         p.N = static_cast<int32_t>(a.N);
         p.K = static_cast<int32_t>(a.K);

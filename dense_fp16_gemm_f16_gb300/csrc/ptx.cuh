@@ -161,6 +161,17 @@ __device__ __forceinline__ void ld_shared_v2_u32(uint32_t addr, uint32_t (&v)[2]
     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(addr) : "memory");
 }
 
+// A flag for ld_acquire_gpu of another kernel, which then sees what this thread has seen; and its
+// taking back, which orders nothing.
+__device__ __forceinline__ void st_release_gpu(uint32_t* addr, uint32_t v) {
+    asm volatile("st.release.gpu.global.u32 [%0], %1;" :: "l"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_relaxed_gpu(uint32_t* addr, uint32_t v) {
+    asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" :: "l"(addr), "r"(v) : "memory");
+}
+// Orders this thread's view of global memory before its later copies by TMA.
+__device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+
 // ---------------------------------------------------------------- TMA
 __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" :: "l"(map) : "memory");
