@@ -161,7 +161,8 @@ typedef struct {
  * rows, up to 32, 64 or 128 of them where M is larger.  X A^T is held in fp32 and enters the
  * second product with twice the precision of dtype (an infinity in B may give NaN for it), so
  * U is rounded once.  A row's result does not depend on the other rows' values or
- * order; in its last bit it may depend on how many rows its adapter and the call have.
+ * order; in its last bit it may depend on how many rows its adapter and the call have, and on
+ * `count`, adapters that no row uses included: they decide how K is shared out.
  * U is what any product of the library takes as C with beta = 1: gemm_nt_scaled for
  * 8-bit operands, or gemm_lora_nt in one call.  K and N multiples of 8.  M or N of zero
  * is a no-op.  More than 256 rows use the stream's scratch memory.
@@ -179,8 +180,9 @@ GEMM_API gemm_status_t gemm_lora_delta(gemm_dtype_t dtype, const void* X, const 
  * once.  Else beta * C and the adapters' part are summed in fp32 and rounded to dtype (beyond
  * fp16's largest number: to infinity) before the projection's sum in fp32 joins them and D is
  * rounded: an error of at most half a unit in the last place of each.
- * Rows without an adapter get the plain product's D where beta is 0 or 1 (with other betas, and
- * with up to 16 rows where an epilogue is given, up to those roundings); count == 0: the plain
+ * Rows without an adapter get the plain product's D, bit for bit, where beta is 1, or 0 without a
+ * bias (else, and with up to 16 rows where an epilogue is given, up to those roundings and one more
+ * in fp32: beside 4-bit W, a plain product adds the bias before it rounds); count == 0: the plain
  * product.  Uses the stream's scratch memory (up to 16 rows beside 16-bit W, above 256 rows).
  */
 GEMM_API gemm_status_t gemm_lora_nt(gemm_dtype_t dtype, const void* X, const gemm_weights_t* W, const gemm_lora_t* lora,

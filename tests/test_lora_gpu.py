@@ -439,3 +439,40 @@ def test_refusals():
         args["U"] = args.pop("D")
         with pytest.raises(error):
             g.gemm_lora_delta(**args)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,four", [(8, True), (13, True), (40, True), (64, True), (300, True), (24, False), (64, False), (130, False), (600, False)])
+def test_rows_without_an_adapter(M, four, dtype):
+    """The plain product's bits with beta 1, or 0 without a bias; with a bias and beta 0 up to one more rounding in fp32."""
+    N, K = 1032, 1024
+    X, lora, ids, gen = draw(M, N, K, 16, 6, dtype, M)
+    W = random_w4(torch.Generator().manual_seed(M), (), N, K, 64, True, dtype, DEV) if four else \
+        (torch.randn(N, K, generator=gen, device=DEV) * K ** -0.5).to(dtype)
+    product = g.gemm_w4_nt if four else g.gemm_nt_ex
+    C, bias = (torch.randn(s, generator=gen, device=DEV).to(dtype) for s in ((M, N), (N,)))
+    sn = torch.rand(N, generator=gen, device=DEV) + 0.5
+    ids[1::3] = -1
+    none = ids < 0
+    D, P = (torch.empty(M, N, dtype=dtype, device=DEV) for _ in range(2))
+    for args in (dict(), dict(alpha=0.6, scale_n=sn), dict(alpha=0.6, activation=g.Activation.RELU),
+                 dict(alpha=0.6, scale_n=sn, beta=1.0, C=C, bias=bias, activation=g.Activation.RELU)):
+        g.gemm_lora_nt(X, W, lora, ids, D, **args)
+        product(X, W, P, **args)
+        assert torch.equal(D[none], P[none])
+    args = dict(alpha=0.6, scale_n=sn, bias=bias)
+    g.gemm_lora_nt(X, W, lora, ids, D, **args)
+    product(X, W, P, **args)
+    d, p = D[none].double(), P[none].double()
+    # two fp32 sums that differ in the rounding of one product and of the whole, each then rounded to the type
+    x = (p - bias.double()).abs()
+    assert bool(((d - p).abs() <= 2.02 * UNIT[dtype] * p.abs() + 2.0 ** -22 * (x + bias.double().abs()) + 2 * FLOOR).all())
+
+
+def test_adapters_that_nobody_uses():
+    """A stack with more adapters may share K out in another way: sums change by their roundings and no more."""
+    X, lora, ids, _ = draw(64, 1032, 4096, 64, 4, torch.bfloat16, 22)
+    more = g.Lora(torch.cat([lora.A] * 20), torch.cat([lora.B] * 20), torch.cat([lora.factors] * 20))
+    ref, err = delta64(X, lora, ids)
+    for l in (lora, more):
+        check(g.gemm_lora_delta(X, l, ids), ref, 1.01 * UNIT[torch.bfloat16] * ref.abs() + err + FLOOR)
