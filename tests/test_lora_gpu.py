@@ -476,3 +476,37 @@ def test_adapters_that_nobody_uses():
     ref, err = delta64(X, lora, ids)
     for l in (lora, more):
         check(g.gemm_lora_delta(X, l, ids), ref, 1.01 * UNIT[torch.bfloat16] * ref.abs() + err + FLOOR)
+
+
+# by the rule that shares rows out: clusters of 3, 1, 3, 1 and 1 CTAs for up to 256 rows, with units of 32 rows
+# clusters of 1, 3, 8, 6, 3 and 1, then units of 128
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,N,K,R,count", [(100, 1032, 1032, 8, 150), (256, 264, 1032, 8, 900), (40, 1032, 520, 40, 200),
+                                           (150, 520, 1032, 40, 200), (150, 520, 264, 256, 200),
+                                           (300, 520, 1032, 16, 500), (257, 1032, 520, 40, 44), (300, 1032, 1032, 256, 3),
+                                           (700, 520, 2056, 136, 1), (260, 264, 520, 200, 44), (500, 520, 264, 256, 300),
+                                           (2000, 264, 520, 64, 8), (1000, 1032, 520, 144, 5)])
+def test_ways_to_share_the_rows(M, N, K, R, count, dtype):
+    for runs in (False, True):
+        X, lora, ids, gen = draw(M, N, K, R, count, dtype, M + N + R, runs)
+        C = torch.randn(M, N, generator=gen, device=DEV).to(dtype)
+        ref, err = delta64(X, lora, ids, 0.3, C)
+        U = g.gemm_lora_delta(X, lora, ids, beta=0.3, C=C)
+        check(U, ref, 1.01 * UNIT[dtype] * ref.abs() + err + FLOOR)
+        assert torch.equal(g.gemm_lora_delta(X, lora, ids, beta=0.3, C=C), U)
+    g.gemm_f16_nt_check(device=DEV)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,R", [(9, 16), (40, 16), (40, 64), (200, 32), (300, 16), (300, 136)])
+def test_not_a_number_reaches_its_row(M, R, dtype):
+    """A NaN in a row whose adapter is in use makes that row NaN, whatever the other rows of the adapter hold."""
+    X, lora, ids, _ = draw(M, 264, 512, R, 4, dtype, 21, none=0.0)
+    want = g.gemm_lora_delta(X, lora, ids)
+    rows = [3, M - 2]
+    X[rows[0], 0] = X[rows[1], 511] = float("nan")
+    got = g.gemm_lora_delta(X, lora, ids)
+    assert bool(got[rows].isnan().all())
+    keep = torch.ones(M, dtype=torch.bool, device=DEV)
+    keep[rows] = False
+    assert torch.equal(got[keep], want[keep])

@@ -209,3 +209,25 @@ def test_given_scale_below_large_rows():
     for scale in (0.0078125, 2.0 ** -110):
         check.scale = scale
         check(g.gemm_rmsnorm(x, w, r, Y8=g.Dtype.E4M3, scale=scale), x, r, w, 1e-6, 1024)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("T,H", [(39001, 24), (39001, 64), (40000, 96), (1300, 4096), (700, 8192), (500, 11000), (400, 16384)])
+def test_rows_of_ctas_that_stay(T, H, dtype):
+    """Enough rows that CTAs take several, with one to four pieces per thread, in every output."""
+    x, r, w = draw(T, H, dtype, T + H)
+    total, Y = torch.empty_like(x), torch.empty_like(x)
+    check(g.gemm_rmsnorm(x, w, r, 1e-5, Y=Y, Y8=g.Dtype.E4M3, total=total), x, r, w, 1e-5, H, total)
+    check(g.gemm_rmsnorm(x, w), x, None, w, 1e-6, H)
+    check(g.gemm_rmsnorm(x, Y8=g.Dtype.E5M2), x, None, None, 1e-6, H)
+
+
+@pytest.mark.parametrize("T,H", [(3, 208), (700, 8192), (2, 40000)])
+def test_nothing_is_written_around_the_rows(T, H):
+    x, r, w = draw(T, H, torch.float16, 9)
+    wide = [torch.full((T + 2, H), 7.0, device=DEV).to(kind) for kind in (x.dtype, torch.float8_e4m3fn, x.dtype)]
+    scales = torch.full((T + 2,), 7.0, device=DEV)
+    Y, Y8, total = (t[1:T + 1] for t in wide)
+    check(g.gemm_rmsnorm(x, w, r, Y=Y, Y8=Y8, scales=scales[1:T + 1], total=total), x, r, w, 1e-6, H, total)
+    for t in (*wide, scales):
+        assert bool((t[0].float() == 7.0).all()) and bool((t[T + 1].float() == 7.0).all())
