@@ -128,7 +128,9 @@ typedef struct {
  * y is all zero has scale 0 and codes 0.  A row that holds an infinity or NaN, or
  * whose squares or products with the weight pass fp32's largest number, has
  * NaN or zeros in Y as the formula gives them and unspecified scale and codes.  With eps 0,
- * squares below fp32's smallest number count as zero.
+ * squares below fp32's smallest number count as zero.  The row's scale is taken from max|h * weight|
+ * before the root: where that lies below 2^-126 it has a subnormal number's bits, below 2^-150
+ * none (scale and codes 0); Y does not go by it.
  * X, residual, Y, total [T][H] and weight [H] in dtype; H a multiple of 8; eps >= 0.
  * Y and total may each be X or residual itself; outputs overlap nothing else.
  * T or H of zero is a no-op.  The 8-bit rows and their scales are what

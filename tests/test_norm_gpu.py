@@ -231,3 +231,19 @@ def test_nothing_is_written_around_the_rows(T, H):
     check(g.gemm_rmsnorm(x, w, r, Y=Y, Y8=Y8, scales=scales[1:T + 1], total=total), x, r, w, 1e-6, H, total)
     for t in (*wide, scales):
         assert bool((t[0].float() == 7.0).all()) and bool((t[T + 1].float() == 7.0).all())
+
+
+def test_products_with_the_weight_below_normal_numbers():
+    """The scale has the bits that max|h w| has in fp32, half a step of 2^-149; Y keeps all of its own."""
+    for h, w in ((2.0 ** -60, 2.0 ** -80), (2.0 ** -62, 2.0 ** -86), (2.0 ** -60, 2.0 ** -95)):
+        x = draw(4, 512, torch.bfloat16, 6, residual=False, weight=False)[0] * h
+        W = torch.full((512,), w, device=DEV, dtype=torch.bfloat16)
+        out = g.gemm_rmsnorm(x, W, eps=0.0, Y=torch.empty_like(x), Y8=g.Dtype.E4M3)
+        v = x.double()
+        root = 1 / torch.sqrt((v * v).mean(1))
+        y, top = v * root[:, None] * w, v.abs().amax(1) * w
+        off = roundings(512) * 2.0 ** -24
+        assert bool(((out.Y.double() - y).abs() <= (1.01 * U[x.dtype] + off) * y.abs()).all())
+        assert bool(((out.scales.double() - top * root / 448).abs() <= 1.01 * 2.0 ** -150 * root / 448 + 2 * off * top * root / 448).all())
+        if w == 2.0 ** -95:
+            assert not bool(out.scales.any()) and not bool(out.Y8.float().any())
