@@ -251,7 +251,8 @@ struct EpiColumnFactors {
 // One output column n of the small-M kernel (rows 0..MN-1): the C values and
 // the bias are fetched with independent loads before any output is written,
 // so their latencies overlap (and an in-place C == D is read before it is
-// overwritten).  apply() is epi_apply1 on the fetched values.
+// overwritten).  apply() is epi_apply1 on the fetched values, its products' roundings written out
+// as in EpiColumnFactors.
 // The C values stay in their 16-bit form, two to a register.
 template <class T, int MN>
 struct EpiColumn {
@@ -269,11 +270,15 @@ struct EpiColumn {
         b = e.bias != nullptr ? Elem<T>::to_float(static_cast<const T*>(e.bias)[n]) : 0.0f;
         a = e.scale_n != nullptr ? e.alpha * e.scale_n[n] : e.alpha;
     }
+    template <bool AC = true>
     __device__ __forceinline__ float apply(const EpiParams& e, float x, int m) const {
-        x *= a;
-        if (e.C != nullptr && e.beta != 0.0f)
-            x += e.beta * ((m & 1) ? Elem<T>::hi(c[m >> 1]) : Elem<T>::lo(c[m >> 1]));
-        if (e.bias != nullptr) x += b;
+        if (e.C != nullptr && e.beta != 0.0f) {
+            const float cv = (m & 1) ? Elem<T>::hi(c[m >> 1]) : Elem<T>::lo(c[m >> 1]);
+            x = AC ? fmaf(x, a, __fmul_rn(e.beta, cv)) : fmaf(e.beta, cv, __fmul_rn(x, a));
+        } else {
+            x = __fmul_rn(x, a);
+        }
+        if (e.bias != nullptr) x = __fadd_rn(x, b);
         if (e.act == 1) x = x < 0.0f ? 0.0f : x;
         return x;
     }

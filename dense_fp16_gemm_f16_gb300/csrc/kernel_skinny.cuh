@@ -345,7 +345,7 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                 if constexpr (LORA) {
 #pragma unroll
                     for (int m = 0; m < MN; ++m)
-                        if (m < p.M) v[m] = __float_as_uint(__uint_as_float(v[m]) * scale_n + lora_out[m * 128]);
+                        if (m < p.M) v[m] = __float_as_uint(fmaf(__uint_as_float(v[m]), scale_n, lora_out[m * 128]));
                 }
                 if (col_in) {
                     if (p.epi.on) {
@@ -433,7 +433,7 @@ gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                 auto finish = [&](int ml, float acc, auto many) {   // many: four rows or more per CTA
                     const int m = j * MS + ml;
                     if (m < p.M) {
-                        if constexpr (LORA) acc = acc * scale_n + lora_out[ml * 128];
+                        if constexpr (LORA) acc = fmaf(acc, scale_n, lora_out[ml * 128]);
                         const float c = (ml & 1) ? Elem<T>::hi(c16[ml / 2]) : Elem<T>::lo(c16[ml / 2]);
                         const float x = p.epi.on ? cf.template apply<decltype(many)::value>(epi, acc, c) : acc;
                         D[m * static_cast<int64_t>(p.N) + n] = Elem<T>::from_float(x);

@@ -207,7 +207,7 @@ gemm_streamk_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
                         for (int m = 0; m < MN; ++m)
                             if (m < p.M)
                                 D[m * static_cast<int64_t>(p.N) + n] =
-                                    Elem<T>::from_float(ec.apply(p.epi, __uint_as_float(v[m]), m));
+                                    Elem<T>::from_float(ec.template apply<false>(p.epi, __uint_as_float(v[m]), m));
                     } else {
 #pragma unroll
                         for (int m = 0; m < MN; ++m)
@@ -294,7 +294,7 @@ gemm_streamk_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_consta
 #pragma unroll
                         for (int m = 0; m < MN; ++m) {
                             if (m < p.M) {
-                                const float x = p.epi.on ? ec.apply(p.epi, acc[m], m) : acc[m];
+                                const float x = p.epi.on ? ec.template apply<false>(p.epi, acc[m], m) : acc[m];
                                 D[m * static_cast<int64_t>(p.N) + n] = Elem<T>::from_float(x);
                             }
                         }
