@@ -880,6 +880,7 @@ constexpr int kLoraMaxShare = 8;
 // beside 4-bit 8192 x 4096, rank 64, the whole call: 3 adapters in use 39 -> 29 us, 8 31.5 -> 28,
 // 38, two more than the GPU holds at one time, 45 -> 40; where nothing is left to share, 0.2 to 0.7 us
 // more.  As code of its own behind the loop: 30.5, 28.3, 46 and 0 to 0.4).
+// Two CTAs per SM leave 128 registers: Ranks32 spills 80 bytes there.
 template <class T, class Sh>
 __global__ void __launch_bounds__(kLoraThreads, Sh::LONG ? 1 : 2) lora_kernel(const LoraParams p) {
     extern __shared__ __align__(16) uint8_t smem[];
@@ -1039,9 +1040,13 @@ struct Work {
 };
 
 // How it is shared out: clusters of which size, and with a list units of how many rows.  A
-// unit takes 8 us and what its CTAs share, 24 us and one more per row (at 8192 x 4096, rank
-// 64; other sizes scale all three), once for every round of units that the GPU cannot hold at
-// one time.  Adapters are taken to be chosen evenly, from all or from half of them.
+// unit takes 8 us and what its CTAs share, 24 us and one more per row, once for every round of units
+// that the GPU cannot hold at one time.  That is 8192 x 4096, rank 64.  The 8, which are order, barriers and
+// exchange, do not shrink with K, N and R, but the rule takes them to: small projections get clusters that
+// are too large by up to 0.8 us (20, 64 and 200 rows of 4 to 64 adapters: 256 x 256, rank 8, 5.2 to 6.2 us,
+// with one CTA each 4.7 to 5.6; 2048 x 2048, rank 16, 5.4 to 7.2, the best sizes 5.3 to 7.1; 4096 x
+// 4096, rank 32, no size is better by more than 0.1).
+// Adapters are taken to be chosen evenly, from all or from half of them.
 // Measured, adapters alone in a graph:
 //   61 rows, rank 64, clusters of 8, 6, 4, 3, 2: 16 adapters in use 17.8, 12.3, 14.6, 17.1, 21.8 us
 //   (the GPU holds 15, 23, 36, 46, 76 of them), 36 adapters 28.7, 24.0, 17.2, 19.1, 23.4, 40 adapters
@@ -1071,6 +1076,10 @@ void weigh(Share& best, const Slots& slots, const Work (&work)[2], int unit_rows
 //    more than half of its shared memory): started while the kernel before drains, two would go
 //    to the SMs that are free first (61 rows, 48 adapters of rank 64 beside 4-bit
 //    8192 x 4096, the whole call: 39 -> 36 us).
+//    An adapter's rows are not cut: one with most of them is taken by one cluster, up_rows at a time,
+//    and by the clusters that share its columns, which each form V again.  256 rows of one adapter of
+//    8192 x 8192, rank 16, 64, 256: 23, 52, 278 us, and 257 rows, in units, 13, 20, 54; of four adapters 11, 20,
+//    82 and 14, 20, 55.
 //  - More rows are cut into units of 32, 64 or 128 rows; an adapter's last one is half full.
 template <class T, class Sh>
 gemm_status_t launch(LoraParams p, const DeviceView& dev, cudaStream_t s) {

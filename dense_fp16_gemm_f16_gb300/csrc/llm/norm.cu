@@ -4,8 +4,9 @@
 // A row stays in its threads' registers between the one pass that reads it and
 // the one that writes it, so x, r, w, the stored sum and y each cross memory once
 // and many rows are bound by those bytes: 4096 x 8192 bf16 with residual, sum and E4M3
-// rows 39 us for 235 MB, 6.0 TB/s, 0.88 of the measured copy rate (in 16 bits and no more 30 us
-// for 134 MB: fewer bytes are under way); 4096 x 11000 63 us where the bytes take 46.
+// rows 39 us for 235 MB, 6.0 TB/s, 0.88 of the measured copy rate (in 16 bits without a residual 30 us
+// for 134 MB: the registers that would hold the residual's pieces fetch nothing); 4096 x 11000 63 us
+// where the bytes take 46.
 // A few rows are bound by the launch and one round of sums (37 x 5128: 3 us in a graph).
 // One round serves both the mean and the scale: max|h w| is taken beside the sum of
 // squares, and the root's factor multiplies it afterwards.
@@ -337,7 +338,7 @@ gemm_status_t run(NormParams p, const DeviceView& dev, cudaStream_t s) {
     }
     if (nv <= 1) return launch_clusters(norm_kernel<T, 1, 1024>, dev.dev, grid, threads, 1, 0, true, s, p);
     if (nv <= 2) return launch_clusters(norm_kernel<T, 2, 1024>, dev.dev, grid, threads, 1, 0, true, s, p);
-    // 1024 threads leave 64 registers each, 512 enough for four pieces without spills
+    // 512 threads have registers enough for four pieces, 1024 (rows of more than 16384) spill 72 bytes
     if (threads <= 512) return launch_clusters(norm_kernel<T, 4, 512>, dev.dev, grid, threads, 1, 0, true, s, p);
     return launch_clusters(norm_kernel<T, 4, 1024>, dev.dev, grid, threads, 1, 0, true, s, p);
 }
