@@ -481,7 +481,7 @@ def test_adapters_that_nobody_uses():
 # by the rule that shares rows out, on 152 SMs: clusters of 3, 1, 3, 3, 1 and 1 CTAs for up to 256 rows; with units
 # of 32 rows clusters of 1, 3, 8, 6, 3, 1 and 4, of 64 rows of 3, of 128 rows of 6
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("M,N,K,R,count", [(200, 1032, 1032, 8, 130), (256, 264, 1032, 8, 900), (180, 520, 1032, 24, 130), (40, 1032, 520, 40, 200),
+@pytest.mark.parametrize("M,N,K,R,count", [(200, 1032, 1032, 8, 105), (256, 264, 1032, 8, 900), (180, 520, 1032, 24, 105), (40, 1032, 520, 40, 200),
                                            (150, 520, 1032, 40, 200), (150, 520, 264, 256, 200),
                                            (300, 520, 1032, 16, 500), (257, 1032, 520, 40, 44), (300, 1032, 1032, 256, 3),
                                            (700, 520, 2056, 136, 1), (260, 264, 520, 200, 44), (500, 520, 264, 256, 300),
